@@ -1,8 +1,10 @@
-"""Build libmoe.so (the CUDA kernels + C ABI) in-tree for sm_103a.
+"""Build libmoe.so and libmoe_block.so (the CUDA kernels + C ABIs) in-tree for
+sm_103a.
 
-Each translation unit compiles in parallel with nvcc, then one shared library
-is linked next to this file.  No cmake, no torch extension machinery: the
-library has a plain C ABI (include/moe.h) and is loaded with ctypes.
+Each translation unit compiles in parallel with nvcc, then the shared libraries
+are linked next to this file.  No cmake, no torch extension machinery: the
+libraries have plain C ABIs (include/moe.h, include/moe_block.h) and are loaded
+with ctypes.
 """
 from __future__ import annotations
 
@@ -18,6 +20,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe.so")
+CSRC_BLOCK = os.path.join(HERE, "csrc_block")
+LIB_BLOCK = os.path.join(HERE, "libmoe_block.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -37,44 +41,52 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def block_sources():
+    return sorted(glob.glob(os.path.join(CSRC_BLOCK, "*.cu")))
+
+
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
+    return [f for d in (CSRC, CSRC_BLOCK, INCLUDE) for ext in ("*.cu", "*.cuh", "*.h")
+            for f in glob.glob(os.path.join(d, ext))]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(LIB_BLOCK)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(LIB_BLOCK))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
+    """Build both libraries; returns the path of libmoe.so."""
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     flags = NVCC_FLAGS + list(extra_flags or [])
 
-    def compile_one(src):
-        obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-        cmd = [nvcc, *ARCH, *flags, "-c", src, "-o", obj]
+    def run(cmd, what):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr, file=sys.stderr)
+
+    def compile_one(src):
+        name = os.path.basename(src)
+        obj = os.path.join(BUILD_DIR, os.path.basename(os.path.dirname(src)) + "_" + name + ".o")
+        run([nvcc, *ARCH, *flags, "-c", src, "-o", obj], f"nvcc failed on {name}")
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        objs = list(ex.map(compile_one, sources()))
-    tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt",
-           "-lpthread"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    libs = ((LIB, sources()), (LIB_BLOCK, block_sources()))
+    with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 4)) as ex:
+        objs = dict(zip((src for _, srcs in libs for src in srcs),
+                        ex.map(compile_one, (src for _, srcs in libs for src in srcs))))
+    for lib, srcs in libs:
+        tmp = lib + ".tmp"
+        run([nvcc, *ARCH, "-shared", "-o", tmp, *(objs[s] for s in srcs), "-lcudart_static", "-ldl", "-lrt",
+             "-lpthread"], "link failed")
+        os.replace(tmp, lib)
     return LIB
 
 

@@ -1,0 +1,137 @@
+// Rows of fp32 or bf16 elements, moved eight elements per lane.
+//
+// A row is cut into pieces of 8 elements per thread.  Where rows start on
+// 8-element boundaries (VEC) a thread's eight elements are adjacent: one 16
+// byte access for bf16, one 32 byte access for fp32, so that bf16 and fp32
+// rows of one call are indexed alike and every access fills whole 32 byte
+// sectors.  Else they are n threads apart and every access is one element
+// wide.  The last piece of a row may be partial in both forms.
+#pragma once
+
+#include <stdint.h>
+
+#include "../csrc/common.cuh"
+
+namespace moe {
+namespace blk {
+
+using bf16_t = uint16_t;
+
+// Eight raw elements as they sit in registers.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float v[8];
+};
+template <>
+struct Raw8<bf16_t> {
+  uint32_t v[4];
+};
+
+__device__ __forceinline__ void unpack(const Raw8<float>& r, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = r.v[i];
+}
+__device__ __forceinline__ void unpack(const Raw8<bf16_t>& r, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(r.v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(r.v[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;  // round to nearest even, NaN stays NaN
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void pack(const float (&f)[8], Raw8<float>& r) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.v[i] = f[i];
+}
+__device__ __forceinline__ void pack(const float (&f)[8], Raw8<bf16_t>& r) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+
+// Whole pieces.  Plain (coherent) loads: an output may be its own input.
+__device__ __forceinline__ void load_vec(const float* p, Raw8<float>& r) {
+  asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(r.v[0]), "=f"(r.v[1]), "=f"(r.v[2]), "=f"(r.v[3]), "=f"(r.v[4]), "=f"(r.v[5]), "=f"(r.v[6]),
+                 "=f"(r.v[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void load_vec(const bf16_t* p, Raw8<bf16_t>& r) {
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.v[0]), "=r"(r.v[1]), "=r"(r.v[2]), "=r"(r.v[3])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void store_vec(float* p, const Raw8<float>& r) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(r.v[0]), "f"(r.v[1]), "f"(r.v[2]),
+               "f"(r.v[3]), "f"(r.v[4]), "f"(r.v[5]), "f"(r.v[6]), "f"(r.v[7])
+               : "memory");
+}
+__device__ __forceinline__ void store_vec(bf16_t* p, const Raw8<bf16_t>& r) {
+  asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(r.v[0]), "r"(r.v[1]), "r"(r.v[2]), "r"(r.v[3])
+               : "memory");
+}
+
+__device__ __forceinline__ float as_f32(float v) { return v; }
+__device__ __forceinline__ float as_f32(bf16_t v) { return bf16_to_f32(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(bf16_t* p, float v) { *p = f32_to_bf16(v); }
+
+__device__ __forceinline__ uint32_t raw_bits(float v) { return __float_as_uint(v); }
+__device__ __forceinline__ uint32_t raw_bits(bf16_t v) { return v; }
+__device__ __forceinline__ void raw_set(Raw8<float>& r, int i, float v) { r.v[i] = v; }
+__device__ __forceinline__ void raw_set(Raw8<bf16_t>& r, int i, bf16_t v) {
+  if (i & 1)
+    r.v[i >> 1] |= static_cast<uint32_t>(v) << 16;
+  else
+    r.v[i >> 1] = v;
+}
+template <typename T>
+__device__ __forceinline__ void raw_zero(Raw8<T>& r) {
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(r.v) / sizeof(r.v[0]); ++i) r.v[i] = 0;
+}
+
+// Which columns thread `tid` of `n` holds of the piece that starts at
+// column `base` and spans 8 n columns: element i is column first + i * step.
+template <bool VEC>
+struct Cols {
+  int first;
+  int step;
+  __device__ __forceinline__ Cols(int base, int tid, int n) : first(base + (VEC ? tid * 8 : tid)), step(VEC ? 1 : n) {}
+};
+
+// Elements past column H read as zero.
+template <bool VEC, typename T>
+__device__ __forceinline__ void load8(const T* row, const Cols<VEC>& c, int H, Raw8<T>& r) {
+  if (VEC && c.first + 8 <= H) {
+    load_vec(row + c.first, r);
+  } else {
+    raw_zero(r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c.first + i * c.step < H) raw_set(r, i, row[c.first + i * c.step]);
+  }
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8(T* row, const Cols<VEC>& c, int H, const float (&f)[8]) {
+  if (VEC && c.first + 8 <= H) {
+    Raw8<T> r;
+    pack(f, r);
+    store_vec(row + c.first, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c.first + i * c.step < H) put(row + c.first + i * c.step, f[i]);
+  }
+}
+
+}  // namespace blk
+}  // namespace moe
