@@ -1,0 +1,96 @@
+// What the two directions of the block norm share on the host.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "launch.h"
+
+namespace moe {
+namespace blk {
+
+constexpr int kMaxGroupThreads = 512;      // threads of a row's group, 8 * nch columns each
+constexpr int kNormSmem = 220 * 1024;      // shared memory for staged rows per CTA
+constexpr int kMaxStages = 4;              // rows staged per group
+constexpr int kMaxStagedChunks = 2;        // wider rows (H > 8192) are read without staging
+
+// How a launch cuts its rows: CTAs of `groups` groups of `nt` threads, each
+// group with `stages` rows of `stage` bytes in shared memory.
+struct NormPlan {
+  int nt, nch, groups, stages, stage, grid, smem;
+};
+
+// slot: bytes per thread of all operands' eight columns; max_threads: threads
+// per CTA where a thread has eight columns.  One CTA per SM walks the rows (more where CTAs are small): a row's
+// two sums put two barriers between its reads and its writes, so the copies
+// of the rows ahead, not more threads, keep the memory busy.
+inline NormPlan norm_plan(int T, int H, int slot, int max_threads) {
+  NormPlan p;
+  const int chunks = (H + 7) / 8;
+  p.nch = chunks <= kMaxGroupThreads ? 1 : chunks <= 2 * kMaxGroupThreads ? 2 : 4;
+  p.nt = ((chunks + p.nch - 1) / p.nch + 31) / 32 * 32;
+  if (p.nch > 1) max_threads = kMaxGroupThreads;
+  const int sms = sm_count();
+  p.groups = std::max(1, std::min(p.nt == 32 ? 32 : 15, max_threads / p.nt));
+  p.groups = std::max(1, std::min(p.groups, (T + sms - 1) / sms));
+  p.stage = p.nch <= kMaxStagedChunks ? slot * p.nch * p.nt : 0;
+  while (p.groups > 1 && p.stage * p.groups * 2 > kNormSmem) --p.groups;
+  p.stages = p.stage > 0 ? std::max(1, std::min(kMaxStages, kNormSmem / (p.stage * p.groups))) : 1;
+  const int per_sm = std::max(1, std::min(max_threads / (p.nt * p.groups),
+                                          p.stage > 0 ? kNormSmem / (p.stage * p.groups * p.stages) : 8));
+  p.grid = std::max(1, std::min((T + p.groups - 1) / p.groups, sms * per_sm));
+  const int rows = (T + p.grid * p.groups - 1) / (p.grid * p.groups);  // per group
+  p.stages = std::max(1, std::min(p.stages, rows));
+  p.smem = p.stage * p.groups * p.stages;
+  return p;
+}
+
+// The widest unit of adjacent columns that every row allows.
+inline int norm_unit(std::initializer_list<Rows> all) {
+  int g = 4;
+  for (const Rows& r : all) {
+    if (r.p == nullptr) continue;
+    const int bytes = r.type == MOE_ROW_F32 ? 4 : 2;
+    while (g > 1 && (r.ld % g != 0 || reinterpret_cast<uintptr_t>(r.p) % (g * bytes) != 0)) g /= 2;
+  }
+  return g;
+}
+
+// Raise a kernel's shared memory limit once per device.
+template <typename K>
+cudaError_t allow_smem(K kern, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t r = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
+  if (r == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return r;
+}
+
+// f(type tag of x, type tag of y, unit, chunks) with the numbers as integral
+// constants.
+template <typename F>
+cudaError_t norm_dispatch(int xt, int yt, int unit, int nch, F&& f) {
+  auto c = [&](auto tx, auto ty, auto g) {
+    if (nch == 1) return f(tx, ty, g, std::integral_constant<int, 1>());
+    if (nch == 2) return f(tx, ty, g, std::integral_constant<int, 2>());
+    return f(tx, ty, g, std::integral_constant<int, 4>());
+  };
+  auto u = [&](auto tx, auto ty) {
+    if (unit == 4) return c(tx, ty, std::integral_constant<int, 4>());
+    if (unit == 2) return c(tx, ty, std::integral_constant<int, 2>());
+    return c(tx, ty, std::integral_constant<int, 1>());
+  };
+  using B = uint16_t;
+  if (xt == MOE_ROW_F32) return yt == MOE_ROW_F32 ? u(float(), float()) : u(float(), B());
+  return yt == MOE_ROW_F32 ? u(B(), float()) : u(B(), B());
+}
+
+inline int row_bytes8(const Rows& r) { return r.p == nullptr ? 0 : r.type == MOE_ROW_F32 ? 32 : 16; }
+
+}  // namespace blk
+}  // namespace moe
