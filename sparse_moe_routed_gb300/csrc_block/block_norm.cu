@@ -9,8 +9,7 @@
 //   x_out = scale x + g c1 y r1,   n = x_out r2 c2
 //
 // Bound by HBM: every operand's row moves once.  A group of threads owns a
-// row; the rows ahead are staged in shared memory (stage.cuh), c1 and c2 stay
-// in registers for the launch.
+// row; the rows ahead are staged in shared memory (stage.cuh), with c1 and c2 beside them.
 #include <math.h>
 
 #include "norm.h"
@@ -21,19 +20,24 @@ namespace blk {
 
 namespace {
 
-constexpr int kThreads = 1024;
+#ifndef FT
+#define FT 1024
+#endif
+constexpr int kThreads = FT;
 
 template <typename TX, typename TY, int G, int NCH>
 __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     block_norm_kernel(const NormArgs a, const NormPlan p) {
   constexpr bool STAGED = NCH <= kMaxStagedChunks;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float red[15][2][16];
-  pdl_wait();
-  pdl_trigger();
+  __shared__ __align__(16) float red[15][2][16];
   const int nt = p.nt, H = a.H;
   const int group = threadIdx.x / nt, tid = threadIdx.x - group * nt;
   const bool has_y = a.y.p != nullptr, has_n = a.n_out.p != nullptr;
+  // without a block before it y is a row of zeros: its places are never written
+  stage_init(red, smem, !has_y ? p.smem : 0);
+  pdl_wait();
+  pdl_trigger();
   const bool full = a.gate_kind == MOE_GATE_FULL, token = a.gate_kind == MOE_GATE_TOKEN;
   const TX* x = static_cast<const TX*>(a.x.p);
   const TY* y = static_cast<const TY*>(a.y.p);
@@ -45,124 +49,135 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     if (a.gate_kind == MOE_GATE_CHANNEL) v *= gate_v[c];
     return v;
   };
-  float c1[NCH == 1 ? 8 : 1], c2[NCH == 1 ? 8 : 1];
-  if (NCH == 1) {
+  // c1 and c2 of every column behind the stages, laid out like fp32 rows;
+  // unstaged kernels read them from global memory
+  unsigned char* m1 = smem + static_cast<size_t>(p.groups) * p.stages * p.stage + tid * (G * 4);
+  unsigned char* m2 = m1 + NCH * nt * 32;
+  auto read_c = [&](const unsigned char* m, int h, V8& f) {
+    if (STAGED) {
+      read_staged<float, G>(m, h, nt, f);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = col0<G>(0, i, tid, nt);
-      c1[NCH == 1 ? i : 0] = has_y && c < H ? c1_at(c) : 0.f;
-      c2[NCH == 1 ? i : 0] = c < H ? gain(a.gamma_pre, c) : 0.f;
+      for (int i = 0; i < 8; ++i) {
+        const int c = col0<G>(h, i, tid, nt);
+        el(f, i) = c >= H ? 0.f : m == m1 ? c1_at(c) : gain(a.gamma_pre, c);
+      }
     }
-  }
-  const int off_y = NCH * nt * kSlot<TX>, off_g = off_y + (has_y ? NCH * nt * kSlot<TY> : 0);
-  unsigned char* mine = smem + static_cast<size_t>(group) * p.stages * p.stage;
+  };
+  const int off_y = NCH * nt * kSlot<TX>, off_g = off_y + NCH * nt * kSlot<TY>;
   const int64_t step = static_cast<int64_t>(gridDim.x) * p.groups;
   int64_t t = static_cast<int64_t>(blockIdx.x) * p.groups + group;
-  auto stage = [&](int64_t row, int s) {
-    if (row < a.T) {
-      unsigned char* at = mine + static_cast<size_t>(s) * p.stage;
-      stage_row<TX, G, NCH>(at, x + row * a.x.ld, tid, nt, H);
-      if (has_y) stage_row<TY, G, NCH>(at + off_y, y + row * a.y.ld, tid, nt, H);
-      if (full) stage_row<TY, G, NCH>(at + off_g, gate + row * a.gate.ld, tid, nt, H);
+  // the thread's first place of each operand, in the group's first stage
+  unsigned char* mine = smem + static_cast<size_t>(group) * p.stages * p.stage;
+  unsigned char *mx = mine + tid * (G * sizeof(TX)), *my = mine + tid * (G * sizeof(TY));
+  auto s_x = first_column<const TX>(a.x, t, tid * G);
+  auto s_y = first_column<const TY>(a.y, t, tid * G), s_g = first_column<const TY>(a.gate, t, tid * G);
+  auto w_x = first_column<TX>(a.x_out, t, tid * G);
+  auto w_n = first_column<TY>(a.n_out, t, tid * G);
+  int64_t ahead = t;  // the row that is staged next
+  auto stage = [&](int at) {
+    if (ahead < a.T) {
+      stage_row<TX, G, NCH>(mx + at, s_x, tid, nt, H);
+      if (has_y) stage_row<TY, G, NCH>(my + at + off_y, s_y, tid, nt, H);
+      if (full) stage_row<TY, G, NCH>(my + at + off_g, s_g, tid, nt, H);
     }
+    ahead += step;
+    advance(s_x, p.by[0]);
+    advance(s_y, p.by[1]);
+    if (full) advance(s_g, p.by[2]);
     copies_commit();
   };
   if (STAGED)
-    for (int s = 0; s < p.stages - 1; ++s) stage(t + s * step, s);
+    for (int s = 0; s < p.stages - 1; ++s) stage(s * p.stage);
   float gt_next = token && t < a.T ? gate_v[t] : 1.0f;
-  int which = 0, slot = 0;
-  for (; t < a.T; t += step) {
-    const unsigned char* at = mine + static_cast<size_t>(slot) * p.stage;
+  // after the first rows' copies are on their way
+  if (STAGED) {
+    // place i holds column i: units of G columns are adjacent
+    float* g = reinterpret_cast<float*>(smem + static_cast<size_t>(p.groups) * p.stages * p.stage);
+    for (int i0 = threadIdx.x; i0 < NCH * 8 * nt; i0 += 8 * blockDim.x) {
+      float v1[8], v2[8];  // eight columns' loads in flight
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * blockDim.x;
+        v1[k] = i < H ? c1_at(i) : 0.f;
+        v2[k] = i < H ? gain(a.gamma_pre, i) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * blockDim.x;
+        if (i < NCH * 8 * nt) g[i] = v1[k], g[NCH * 8 * nt + i] = v2[k];
+      }
+    }
+    __syncthreads();
+  }
+  int which = 0, at = 0;
+  for (; t < a.T; t += step, advance(w_x, p.by[3]), advance(w_n, p.by[4])) {
+    const unsigned char *ax = mx + at, *ay = my + at;
     if (STAGED) {
       if (p.stages == 1) {
-        stage(t, 0);
+        stage(0);
         copies_wait(0);
       } else {
         copies_wait(p.stages - 2);
-        stage(t + (p.stages - 1) * step, slot == 0 ? p.stages - 1 : slot - 1);
+        stage(at == 0 ? (p.stages - 1) * p.stage : at - p.stage);
       }
-      slot = slot + 1 == p.stages ? 0 : slot + 1;
+      at = at + p.stage == p.stages * p.stage ? 0 : at + p.stage;
     }
     const float gt = gt_next;
     if (token && t + step < a.T) gt_next = gate_v[t + step];
-    auto read_y = [&](int h, float(&f)[8]) {
+    auto read_y = [&](int h, V8& f) {
       if (STAGED)
-        read_staged<TY, G>(at + off_y, h, tid, nt, f);
+        read_staged<TY, G>(ay + off_y, h, nt, f);
       else
-        read_global<TY, G>(y + t * a.y.ld, h, tid, nt, H, f);
+        read_global<TY, G>(has_y ? y + t * a.y.ld : y, h, tid, nt, has_y ? H : 0, f);
     };
-    float r1 = gt;  // the factor of c1 y: the norm's and the token's
-    if (has_y && a.post_norm) {
-      float ss = 0.f;
+    V8 f;  // y, held between its two uses where a thread has eight columns
+    if (NCH == 1) read_y(0, f);
+    float r1 = 1.0f;
+    if (a.post_norm) {
+      float2 ss = splat(0.f);
 #pragma unroll
       for (int h = 0; h < NCH; ++h) {
-        float f[8];
-        read_y(h, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+        if (NCH > 1) read_y(h, f);
+        dot8(f, f, ss);
       }
-      r1 = 1.0f / sqrtf(group_sum(ss, red[group], which, tid, nt, group) * inv_h + a.eps);
+      r1 = 1.0f / sqrtf(group_sum(ss.x + ss.y, red[group], which, tid, nt, group) * inv_h + a.eps);
       if (tid == 0 && a.rstd_post != nullptr) a.rstd_post[t] = r1;
     }
-    float xo[NCH][8];
-    float ss = 0.f;
+    V8 xo[NCH];
+    float2 ss = splat(0.f);
 #pragma unroll
     for (int h = 0; h < NCH; ++h) {
       if (STAGED)
-        read_staged<TX, G>(at, h, tid, nt, xo[h]);
+        read_staged<TX, G>(ax, h, nt, xo[h]);
       else
         read_global<TX, G>(x + t * a.x.ld, h, tid, nt, H, xo[h]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) xo[h][i] *= a.scale;
-      if (has_y) {
-        float f[8];
-        read_y(h, f);
-        // y r1 first: the normalised value, which neither factor can overflow
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= r1;
-        if (a.post_norm && token) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= gt;
-        }
-        if (full) {
-          float g[8];
-          if (STAGED)
-            read_staged<TY, G>(at + off_g, h, tid, nt, g);
-          else
-            read_global<TY, G>(gate + t * a.gate.ld, h, tid, nt, H, g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= g[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float c = c1[NCH == 1 ? i : 0];
-          if (NCH > 1) {
-            const int col = col0<G>(h, i, tid, nt);
-            c = col < H ? c1_at(col) : 0.f;
-          }
-          xo[h][i] = fmaf(f[i], c, xo[h][i]);
-        }
+      if (NCH > 1) read_y(h, f);
+      V8 c;
+      read_c(m1, h, c);
+      // y r1 first: the normalised value, which no gate can overflow
+      f = f * r1 * gt;
+      if (full) {
+        V8 g;
+        if (STAGED)
+          read_staged<TY, G>(ay + off_g, h, nt, g);
+        else
+          read_global<TY, G>(gate + t * a.gate.ld, h, tid, nt, H, g);
+        f = f * g;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(xo[h][i], xo[h][i], ss);
-      if (a.x_out.p != nullptr)
-        write_row<TX, G>(static_cast<TX*>(a.x_out.p) + t * a.x_out.ld, h, tid, nt, H, xo[h]);
+      xo[h] = fma8(f, c, xo[h] * a.scale);
+      dot8(xo[h], xo[h], ss);
+      if (a.x_out.p != nullptr) write_row<TX, G>(w_x, h, tid, nt, H, xo[h]);
     }
     if (!has_n) continue;
-    const float r2 = 1.0f / sqrtf(group_sum(ss, red[group], which, tid, nt, group) * inv_h + a.eps);
+    const float r2 = 1.0f / sqrtf(group_sum(ss.x + ss.y, red[group], which, tid, nt, group) * inv_h + a.eps);
     if (tid == 0 && a.rstd_pre != nullptr) a.rstd_pre[t] = r2;
 #pragma unroll
     for (int h = 0; h < NCH; ++h) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float c = c2[NCH == 1 ? i : 0];
-        if (NCH > 1) {
-          const int col = col0<G>(h, i, tid, nt);
-          c = col < H ? gain(a.gamma_pre, col) : 0.f;
-        }
-        xo[h][i] = xo[h][i] * r2 * c;
-      }
-      write_row<TY, G>(static_cast<TY*>(a.n_out.p) + t * a.n_out.ld, h, tid, nt, H, xo[h]);
+      V8 c;
+      read_c(m2, h, c);
+      xo[h] = xo[h] * r2 * c;
+      write_row<TY, G>(w_n, h, tid, nt, H, xo[h]);
     }
   }
 }
@@ -172,8 +187,9 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
 cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t st) {
   const bool full = a.gate_kind == MOE_GATE_FULL;
   const Rows gate = full ? a.gate : Rows{nullptr, 0, MOE_ROW_F32};
-  const NormPlan p = norm_plan(a.T, a.H, row_bytes8(a.x) + row_bytes8(a.y) + row_bytes8(gate), kThreads);
-  const int unit = norm_unit({a.x, a.y, gate, a.x_out, a.n_out});
+  NormPlan p = norm_plan(a.T, a.H, row_bytes8(a.x) + (a.y.type == MOE_ROW_F32 ? 32 : 16) + row_bytes8(gate), kThreads);
+  plan_steps(p, {a.x, a.y, gate, a.x_out, a.n_out});
+  const int unit = norm_unit(a.H, {a.x, a.y, gate, a.x_out, a.n_out});
   return norm_dispatch(a.x.type, a.y.type, unit, p.nch, [&](auto tx, auto ty, auto g, auto n) {
     auto kern = block_norm_kernel<decltype(tx), decltype(ty), decltype(g)::value, decltype(n)::value>;
     static std::atomic<uint64_t> done{0};

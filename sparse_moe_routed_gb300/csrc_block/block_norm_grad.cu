@@ -3,8 +3,8 @@
 // With xh = x_out r2, yh = y r1 (the normalised rows), u = dn c2, c1 = (1 +
 // gamma_post) times a per-channel gate and g the gate where it varies by row:
 //   D  = dx_out + r2 (u - xh mean(u xh)),   dx = scale D
-//   q  = sum D c1 yh g  (per-token dgate: without g)
-//   dy = r1 (D g c1 - yh q / H)
+//   q  = sum D c1 yh,   dy = r1 g (D c1 - yh q / H),   per-token dgate = q
+// (a gate per element goes into D before q instead).
 // Written with normalised rows, so that a small row's large r is never cubed.
 // Per column, A = sum_t D g yh gives dgamma_post = gate_c A as well as a
 // per-channel dgate = (1 + gamma_post) A, and B = sum_t dn xh is dgamma_pre:
@@ -25,20 +25,24 @@ namespace blk {
 
 namespace {
 
-constexpr int kThreads = 640;
+#ifndef GT
+#define GT 640
+#endif
+constexpr int kThreads = GT;
 
 template <typename TX, typename TY, int G, int NCH>
 __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     block_norm_grad_kernel(const NormGradArgs a, const NormPlan p, int want_cols) {
   constexpr bool STAGED = NCH <= kMaxStagedChunks;
-  constexpr int NA = STAGED ? NCH * 8 : 1;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float red[15][2][16];
-  pdl_wait();
-  pdl_trigger();
+  __shared__ __align__(16) float red[15][2][16];
   const int nt = p.nt, H = a.H;
   const int group = threadIdx.x / nt, tid = threadIdx.x - group * nt;
   const bool has_d = a.dx_out.p != nullptr, has_n = a.dn.p != nullptr, has_y = a.y.p != nullptr;
+  // an absent gradient is a row of zeros: its places are never written
+  stage_init(red, smem, !has_d || !has_n ? p.smem : 0);
+  pdl_wait();
+  pdl_trigger();
   const bool full = a.gate_kind == MOE_GATE_FULL, token = a.gate_kind == MOE_GATE_TOKEN;
   const TX *dxo = static_cast<const TX*>(a.dx_out.p), *xo = static_cast<const TX*>(a.x_out.p);
   const TY *dn = static_cast<const TY*>(a.dn.p), *y = static_cast<const TY*>(a.y.p);
@@ -50,46 +54,76 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     if (a.gate_kind == MOE_GATE_CHANNEL) v *= gate_v[c];
     return v;
   };
-  float c1[NCH == 1 ? 8 : 1], c2[NCH == 1 ? 8 : 1];
-  if (NCH == 1) {
+  // c1 and c2 of every column behind the stages, laid out like fp32 rows;
+  // unstaged kernels read them from global memory
+  unsigned char* m1 = smem + static_cast<size_t>(p.groups) * p.stages * p.stage + tid * (G * 4);
+  unsigned char* m2 = m1 + NCH * nt * 32;
+  auto read_c = [&](const unsigned char* m, int h, V8& f) {
+    if (STAGED) {
+      read_staged<float, G>(m, h, nt, f);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = col0<G>(0, i, tid, nt);
-      c1[NCH == 1 ? i : 0] = has_y && c < H ? c1_at(c) : 0.f;
-      c2[NCH == 1 ? i : 0] = c < H ? gain(a.gamma_pre, c) : 0.f;
+      for (int i = 0; i < 8; ++i) {
+        const int c = col0<G>(h, i, tid, nt);
+        el(f, i) = c >= H ? 0.f : m == m1 ? c1_at(c) : gain(a.gamma_pre, c);
+      }
     }
-  }
+  };
   // column sums: registers, or (unstaged, widest rows) the thread's own
   // places in shared memory
-  float accA[NA], accB[NA];
+  constexpr int NA = STAGED ? NCH : 1;
+  V8 accA[NA], accB[NA];
 #pragma unroll
-  for (int i = 0; i < NA; ++i) accA[i] = accB[i] = 0.f;
+  for (int h = 0; h < NA; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) accA[h].v[i] = accB[h].v[i] = splat(0.f);
   float* shA = reinterpret_cast<float*>(smem) + tid;
   float* shB = shA + NCH * 8 * nt;
   if (!STAGED)
     for (int i = 0; i < NCH * 8; ++i) shA[i * nt] = shB[i * nt] = 0.f;
+  // acc += v w for chunk h
+  auto add_cols = [&](V8(&acc)[NA], float* sh, int h, const V8& v, float w) {
+    if (STAGED) {
+      acc[STAGED ? h : 0] = fma8(v, w, acc[STAGED ? h : 0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sh[(h * 8 + i) * nt] = fmaf(el(v, i), w, sh[(h * 8 + i) * nt]);
+    }
+  };
 
   const int bx = NCH * nt * kSlot<TX>, by = NCH * nt * kSlot<TY>;
-  const int off_x = has_d ? bx : 0, off_dn = off_x + (has_n ? bx : 0), off_y = off_dn + (has_n ? by : 0),
-            off_g = off_y + (has_y ? by : 0);
-  unsigned char* mine = smem + static_cast<size_t>(group) * p.stages * p.stage;
+  const int off_x = bx, off_dn = off_x + bx, off_y = off_dn + by, off_g = off_y + (has_y ? by : 0);
   const int64_t step = static_cast<int64_t>(gridDim.x) * p.groups;
   int64_t t = static_cast<int64_t>(blockIdx.x) * p.groups + group;
-  auto stage = [&](int64_t row, int s) {
-    if (row < a.T) {
-      unsigned char* at = mine + static_cast<size_t>(s) * p.stage;
+  // the thread's first place of each operand, in the group's first stage
+  unsigned char* mine = smem + static_cast<size_t>(group) * p.stages * p.stage;
+  unsigned char *mx = mine + tid * (G * sizeof(TX)), *my = mine + tid * (G * sizeof(TY));
+  auto s_dxo = first_column<const TX>(a.dx_out, t, tid * G), s_xo = first_column<const TX>(a.x_out, t, tid * G);
+  auto s_dn = first_column<const TY>(a.dn, t, tid * G), s_y = first_column<const TY>(a.y, t, tid * G),
+       s_g = first_column<const TY>(a.gate, t, tid * G);
+  auto w_dx = first_column<TX>(a.dx, t, tid * G);
+  auto w_dy = first_column<TY>(a.dy, t, tid * G);
+  int64_t ahead = t;  // the row that is staged next
+  auto stage = [&](int at) {
+    if (ahead < a.T) {
+      if (has_d) stage_row<TX, G, NCH>(mx + at, s_dxo, tid, nt, H);
       if (has_n) {
-        stage_row<TX, G, NCH>(at + off_x, xo + row * a.x_out.ld, tid, nt, H);
-        stage_row<TY, G, NCH>(at + off_dn, dn + row * a.dn.ld, tid, nt, H);
+        stage_row<TX, G, NCH>(mx + at + off_x, s_xo, tid, nt, H);
+        stage_row<TY, G, NCH>(my + at + off_dn, s_dn, tid, nt, H);
       }
-      if (has_d) stage_row<TX, G, NCH>(at, dxo + row * a.dx_out.ld, tid, nt, H);
-      if (has_y) stage_row<TY, G, NCH>(at + off_y, y + row * a.y.ld, tid, nt, H);
-      if (full) stage_row<TY, G, NCH>(at + off_g, gate + row * a.gate.ld, tid, nt, H);
+      if (has_y) stage_row<TY, G, NCH>(my + at + off_y, s_y, tid, nt, H);
+      if (full) stage_row<TY, G, NCH>(my + at + off_g, s_g, tid, nt, H);
     }
+    ahead += step;
+    advance(s_dxo, p.by[0]);
+    advance(s_xo, p.by[1]);
+    advance(s_dn, p.by[2]);
+    advance(s_y, p.by[3]);
+    if (full) advance(s_g, p.by[4]);
     copies_commit();
   };
   if (STAGED)
-    for (int s = 0; s < p.stages - 1; ++s) stage(t + s * step, s);
+    for (int s = 0; s < p.stages - 1; ++s) stage(s * p.stage);
   float r1n = 1.f, r2n = 0.f, gtn = 1.f;  // the next row's factors
   auto factors = [&](int64_t row) {
     if (row >= a.T) return;
@@ -98,131 +132,119 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     if (token) gtn = gate_v[row];
   };
   factors(t);
-  int which = 0, slot = 0;
-  for (; t < a.T; t += step) {
-    const unsigned char* at = mine + static_cast<size_t>(slot) * p.stage;
+  // after the first rows' copies are on their way
+  if (STAGED) {
+    // place i holds column i: units of G columns are adjacent
+    float* g = reinterpret_cast<float*>(smem + static_cast<size_t>(p.groups) * p.stages * p.stage);
+    for (int i0 = threadIdx.x; i0 < NCH * 8 * nt; i0 += 8 * blockDim.x) {
+      float v1[8], v2[8];  // eight columns' loads in flight
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * blockDim.x;
+        v1[k] = i < H ? c1_at(i) : 0.f;
+        v2[k] = i < H ? gain(a.gamma_pre, i) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * blockDim.x;
+        if (i < NCH * 8 * nt) g[i] = v1[k], g[NCH * 8 * nt + i] = v2[k];
+      }
+    }
+    __syncthreads();
+  }
+  int which = 0, at = 0;
+  for (; t < a.T; t += step, advance(w_dx, p.by[5]), advance(w_dy, p.by[6])) {
+    const unsigned char *ax = mx + at, *ay = my + at;
     if (STAGED) {
       if (p.stages == 1) {
-        stage(t, 0);
+        stage(0);
         copies_wait(0);
       } else {
         copies_wait(p.stages - 2);
-        stage(t + (p.stages - 1) * step, slot == 0 ? p.stages - 1 : slot - 1);
+        stage(at == 0 ? (p.stages - 1) * p.stage : at - p.stage);
       }
-      slot = slot + 1 == p.stages ? 0 : slot + 1;
+      at = at + p.stage == p.stages * p.stage ? 0 : at + p.stage;
     }
     const float r1 = r1n, r2 = r2n, gt = gtn;
     factors(t + step);
-    auto read_x = [&](int off, const TX* q, int64_t ld, int h, float(&f)[8]) {
+    auto read_x = [&](int off, const TX* q, int64_t ld, int h, V8& f) {
       if (STAGED)
-        read_staged<TX, G>(at + off, h, tid, nt, f);
+        read_staged<TX, G>(ax + off, h, nt, f);
       else
-        read_global<TX, G>(q + t * ld, h, tid, nt, H, f);
+        read_global<TX, G>(q == nullptr ? q : q + t * ld, h, tid, nt, q == nullptr ? 0 : H, f);
     };
-    auto read_y = [&](int off, const TY* q, int64_t ld, int h, float(&f)[8]) {
+    auto read_y = [&](int off, const TY* q, int64_t ld, int h, V8& f) {
       if (STAGED)
-        read_staged<TY, G>(at + off, h, tid, nt, f);
+        read_staged<TY, G>(ay + off, h, nt, f);
       else
-        read_global<TY, G>(q + t * ld, h, tid, nt, H, f);
+        read_global<TY, G>(q == nullptr ? q : q + t * ld, h, tid, nt, q == nullptr ? 0 : H, f);
     };
-    auto c1_of = [&](int h, int i) {
-      if (NCH == 1) return c1[NCH == 1 ? i : 0];
-      const int c = col0<G>(h, i, tid, nt);
-      return c < H ? c1_at(c) : 0.f;
-    };
-    auto c2_of = [&](int h, int i) {
-      if (NCH == 1) return c2[NCH == 1 ? i : 0];
-      const int c = col0<G>(h, i, tid, nt);
-      return c < H ? gain(a.gamma_pre, c) : 0.f;
-    };
-
-    float m = 0.f;
-    if (has_n) {
-      float dot = 0.f;
-#pragma unroll
-      for (int h = 0; h < NCH; ++h) {
-        float xv[8], dv[8];
-        read_x(off_x, xo, a.x_out.ld, h, xv);
-        read_y(off_dn, dn, a.dn.ld, h, dv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xh = xv[i] * r2;
-          if (STAGED)
-            accB[STAGED ? h * 8 + i : 0] = fmaf(dv[i], xh, accB[STAGED ? h * 8 + i : 0]);
-          else
-            shB[(h * 8 + i) * nt] = fmaf(dv[i], xh, shB[(h * 8 + i) * nt]);
-          dot = fmaf(dv[i] * c2_of(h, i), xh, dot);
-        }
-      }
-      m = group_sum(dot, red[group], which, tid, nt, group) * inv_h;
-    }
-
-    float D[NCH][8];
-    float q = 0.f;
+    // where a thread has eight columns, xh, u = dn c2 and yh are held between
+    // the row's steps; wider rows are read again
+    V8 xh, u, yh;
+    float2 dot = splat(0.f);
 #pragma unroll
     for (int h = 0; h < NCH; ++h) {
-      if (has_d) {
-        read_x(0, dxo, a.dx_out.ld, h, D[h]);
-      } else {
+      V8 c;
+      read_c(m2, h, c);
+      read_x(off_x, xo, a.x_out.ld, h, xh);
+      read_y(off_dn, dn, a.dn.ld, h, u);
+      xh = xh * r2;
+      add_cols(accB, shB, h, u * xh, 1.0f);
+      u = u * c;
+      dot8(u, xh, dot);
+    }
+    float m = group_sum(dot.x + dot.y, red[group], which, tid, nt, group) * inv_h;
+
+    V8 D[NCH];
+    float2 qs = splat(0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) D[h][i] = 0.f;
+    for (int h = 0; h < NCH; ++h) {
+      V8 c;
+      if (NCH > 1) {
+        read_c(m2, h, c);
+        read_x(off_x, xo, a.x_out.ld, h, xh);
+        read_y(off_dn, dn, a.dn.ld, h, u);
+        xh = xh * r2;
+        u = u * c;
       }
-      if (has_n) {
-        float xv[8], dv[8];
-        read_x(off_x, xo, a.x_out.ld, h, xv);
-        read_y(off_dn, dn, a.dn.ld, h, dv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          D[h][i] = fmaf(r2, fmaf(dv[i], c2_of(h, i), -(xv[i] * r2) * m), D[h][i]);
-      }
-      float o[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = a.scale * D[h][i];
-      write_row<TX, G>(static_cast<TX*>(a.dx.p) + t * a.dx.ld, h, tid, nt, H, o);
+      read_x(0, dxo, a.dx_out.ld, h, D[h]);
+      D[h] = fma8(fma8(xh, -m, u), r2, D[h]);
+      write_row<TX, G>(w_dx, h, tid, nt, H, D[h] * a.scale);
       if (!has_y) continue;
-      float yv[8], g[8];
-      read_y(off_y, y, a.y.ld, h, yv);
+      read_y(off_y, y, a.y.ld, h, yh);
+      yh = yh * r1;
+      read_c(m1, h, c);
       if (full) {
+        V8 g;
         read_y(off_g, gate, a.gate.ld, h, g);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = gt;
+        if (a.dgate.p != nullptr)
+          write_row<TY, G>(static_cast<TY*>(a.dgate.p) + t * a.dgate.ld + tid * G, h, tid, nt, H, D[h] * c * yh);
+        D[h] = D[h] * g;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float yh = yv[i] * r1;
-        const float dg = D[h][i] * g[i];
-        if (STAGED)
-          accA[STAGED ? h * 8 + i : 0] = fmaf(dg, yh, accA[STAGED ? h * 8 + i : 0]);
-        else
-          shA[(h * 8 + i) * nt] = fmaf(dg, yh, shA[(h * 8 + i) * nt]);
-        const float c = c1_of(h, i);
-        o[i] = D[h][i] * c * yh;  // a full gate's gradient
-        D[h][i] = dg * c;
-        q += token ? o[i] : D[h][i] * yh;
-      }
-      if (full && a.dgate.p != nullptr)
-        write_row<TY, G>(static_cast<TY*>(a.dgate.p) + t * a.dgate.ld, h, tid, nt, H, o);
+      const V8 v = D[h] * yh;
+      add_cols(accA, shA, h, v, gt);
+      dot8(v, c, qs);
+      D[h] = D[h] * c;
     }
     if (!has_y) continue;
-    m = 0.f;
+    float q = qs.x + qs.y;
     if (a.post_norm || token) {
       q = group_sum(q, red[group], which, tid, nt, group);
-      if (token) {
-        if (tid == 0 && a.dgate.p != nullptr) static_cast<float*>(a.dgate.p)[t] = q;
-        q *= gt;
-      }
-      m = q * inv_h;
+      if (token && tid == 0 && a.dgate.p != nullptr) static_cast<float*>(a.dgate.p)[t] = q;
     }
+    m = q * inv_h;
+    const float rg = r1 * gt;
 #pragma unroll
     for (int h = 0; h < NCH; ++h) {
       if (a.post_norm) {
-        float yv[8];
-        read_y(off_y, y, a.y.ld, h, yv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) D[h][i] = r1 * fmaf(-(yv[i] * r1), m, D[h][i]);
+        if (NCH > 1) {
+          read_y(off_y, y, a.y.ld, h, yh);
+          yh = yh * r1;
+        }
+        D[h] = fma8(yh, -m, D[h]);
       }
-      write_row<TY, G>(static_cast<TY*>(a.dy.p) + t * a.dy.ld, h, tid, nt, H, D[h]);
+      write_row<TY, G>(w_dy, h, tid, nt, H, D[h] * rg);
     }
   }
   if (!want_cols) return;
@@ -231,21 +253,21 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     float* sh = reinterpret_cast<float*>(smem);
     __syncthreads();
     if (group > 0) {
-      float* s = sh + static_cast<size_t>(group - 1) * 2 * NA * nt + tid;
+      float* s = sh + static_cast<size_t>(group - 1) * 16 * NA * nt + tid;
 #pragma unroll
-      for (int i = 0; i < NA; ++i) {
-        s[i * nt] = accA[i];
-        s[(NA + i) * nt] = accB[i];
+      for (int i = 0; i < 8 * NA; ++i) {
+        s[i * nt] = el(accA[i / 8], i % 8);
+        s[(8 * NA + i) * nt] = el(accB[i / 8], i % 8);
       }
     }
     __syncthreads();
     if (group > 0) return;
     for (int k = 0; k + 1 < p.groups; ++k) {
-      const float* s = sh + static_cast<size_t>(k) * 2 * NA * nt + tid;
+      const float* s = sh + static_cast<size_t>(k) * 16 * NA * nt + tid;
 #pragma unroll
-      for (int i = 0; i < NA; ++i) {
-        accA[i] += s[i * nt];
-        accB[i] += s[(NA + i) * nt];
+      for (int i = 0; i < 8 * NA; ++i) {
+        el(accA[i / 8], i % 8) += s[i * nt];
+        el(accB[i / 8], i % 8) += s[(8 * NA + i) * nt];
       }
     }
   }
@@ -256,43 +278,40 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     for (int i = 0; i < 8; ++i) {
       const int c = col0<G>(h, i, tid, nt);
       if (c >= H) continue;
-      w[c] = STAGED ? accA[STAGED ? h * 8 + i : 0] : shA[(h * 8 + i) * nt];
-      w[H + c] = STAGED ? accB[STAGED ? h * 8 + i : 0] : shB[(h * 8 + i) * nt];
+      w[c] = STAGED ? el(accA[STAGED ? h : 0], i) : shA[(h * 8 + i) * nt];
+      w[H + c] = STAGED ? el(accB[STAGED ? h : 0], i) : shB[(h * 8 + i) * nt];
     }
 }
 
-// Column sums over the parts, in part order within each of the CTA's 8 rows
-// of threads, then over those.
-__global__ void __launch_bounds__(256) norm_cols_kernel(const float* __restrict__ ws, int parts, int H,
-                                                        const float* gate_c, const float* gamma_post, int post_norm,
-                                                        float* dgate_c, float* dgamma_post, float* dgamma_pre) {
-  __shared__ float sh[2][8][32];
+// Column sums over the parts: 32 columns by 32 threads, each of which adds
+// every 32nd part in order, then these in order.  blockIdx.y 0: A, 1: B.
+__global__ void __launch_bounds__(1024) norm_cols_kernel(const float* __restrict__ ws, int parts, int H,
+                                                         const float* gate_c, const float* gamma_post, int post_norm,
+                                                         float* dgate_c, float* dgamma_post, float* dgamma_pre) {
+  __shared__ float sh[32][33];
   pdl_wait();
-  pdl_trigger();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + tx;
-  float A = 0.f, B = 0.f;
+  const float* w = ws + blockIdx.y * H + col;
+  float v = 0.f;
   if (col < H) {
-#pragma unroll 4
-    for (int p = ty; p < parts; p += 8) {
-      const float* w = ws + static_cast<size_t>(p) * 2 * H;
-      A += w[col];
-      B += w[H + col];
-    }
+#pragma unroll 8
+    for (int p = ty; p < parts; p += 32) v += w[static_cast<size_t>(p) * 2 * H];
   }
-  sh[0][ty][tx] = A;
-  sh[1][ty][tx] = B;
+  sh[ty][tx] = v;
   __syncthreads();
-  if (ty != 0 || col >= H) return;
-  A = B = 0.f;
+  // warp ty adds column ty's 32 sums
+  v = sh[tx][ty];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    A += sh[0][i][tx];
-    B += sh[1][i][tx];
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int c = blockIdx.x * 32 + ty;
+  if (tx != 0 || c >= H) return;
+  if (blockIdx.y == 1) {
+    if (dgamma_pre != nullptr) dgamma_pre[c] = v;
+    return;
   }
-  if (dgamma_post != nullptr) dgamma_post[col] = gate_c != nullptr ? gate_c[col] * A : A;
-  if (dgate_c != nullptr) dgate_c[col] = post_norm ? gain(gamma_post, col) * A : A;
-  if (dgamma_pre != nullptr) dgamma_pre[col] = B;
+  if (dgamma_post != nullptr) dgamma_post[c] = gate_c != nullptr ? gate_c[c] * v : v;
+  if (dgate_c != nullptr) dgate_c[c] = post_norm ? gain(gamma_post, c) * v : v;
 }
 
 }  // namespace
@@ -312,13 +331,15 @@ cudaError_t launch_block_norm_grad(const NormGradArgs& a, cudaStream_t st) {
     const bool full = a.gate_kind == MOE_GATE_FULL;
     const Rows none = {nullptr, 0, MOE_ROW_F32};
     const Rows gate = full ? a.gate : none, dgate = full ? a.dgate : none;
-    const int slot = row_bytes8(a.dx_out) + row_bytes8(a.x_out) + row_bytes8(a.dn) + row_bytes8(a.y) + row_bytes8(gate);
+    const int sx = a.dx.type == MOE_ROW_F32 ? 32 : 16, sy = a.y.type == MOE_ROW_F32 ? 32 : 16;
+    const int slot = 2 * sx + sy + row_bytes8(a.y) + row_bytes8(gate);
     NormPlan p = norm_plan(a.T, a.H, slot, kThreads);
     p.grid = std::min(p.grid, sm_count());
     const int cols = p.nch <= kMaxStagedChunks ? (p.groups - 1) * 2 * p.nch * 8 * p.nt * 4 : 2 * p.nch * 8 * p.nt * 4;
-    p.smem = std::max(p.smem, cols);
+    p.smem = std::max(p.smem, cols);  // the sums' join takes the stages' place
     parts = p.grid;
-    const int unit = norm_unit({a.dx_out, a.x_out, a.dn, a.y, gate, dgate, a.dx, a.dy});
+    plan_steps(p, {a.dx_out, a.x_out, a.dn, a.y, gate, a.dx, a.dy});
+    const int unit = norm_unit(a.H, {a.dx_out, a.x_out, a.dn, a.y, gate, dgate, a.dx, a.dy});
     const cudaError_t e = norm_dispatch(a.dx.type, a.y.type, unit, p.nch, [&](auto tx, auto ty, auto g, auto n) {
       auto kern = block_norm_grad_kernel<decltype(tx), decltype(ty), decltype(g)::value, decltype(n)::value>;
       static std::atomic<uint64_t> done{0};
@@ -329,7 +350,7 @@ cudaError_t launch_block_norm_grad(const NormGradArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   if (!want) return cudaSuccess;
-  return launch_pdl(norm_cols_kernel, dim3((a.H + 31) / 32), dim3(256), 0, st, a.ws, parts, a.H,
+  return launch_pdl(norm_cols_kernel, dim3((a.H + 31) / 32, 2), dim3(1024), 0, st, a.ws, parts, a.H,
                     chan ? static_cast<const float*>(a.gate.p) : nullptr, a.gamma_post, a.post_norm, dgate_c,
                     a.dgamma_post, a.dgamma_pre);
 }

@@ -10,11 +10,12 @@
 // weighted sum follows route-rank order.
 //
 // Bound by HBM: a row of every kept route moves once (spread: written, with dw
-// also read; join: read) and a row of every token once.  One CTA owns a token
-// (spread: up to all of its routes) and its warps share the row's pieces of
-// 256 columns, so the token's row is read once whatever k is, a thread has the
-// loads of eight routes in flight, and dw needs no atomics: each warp reduces
-// its columns' products and the CTA adds the warps in order.
+// also read; join: read) and a row of every token once.  With many tokens one
+// warp owns a token: it walks the row's pieces of 256 columns, each lane with
+// the loads of up to eight routes in flight, and needs no barrier from its
+// slots to its dw.  With few, the warps of a CTA share a token's pieces (and
+// CTAs its routes or columns), and dw adds the warps' sums in order.  dw needs
+// no atomics in either form, and the token's row is read once whatever k is.
 #include <algorithm>
 
 #include "launch.h"
@@ -45,66 +46,82 @@ __device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane) {
   return c;
 }
 
-// A CTA's routes: slots (-1 where there is none) and weights.
+// A token's routes: where the row of each starts (-1: it has none), weights.
 struct Routes {
-  int slot[kMaxK];
+  int64_t at[kMaxK];
   float w[kMaxK];
 };
 
+// Fills the routes with threads 0..n-1 of the token's warps.
 __device__ __forceinline__ void read_routes(Routes& sh, const int32_t* slot_of, const float* w, size_t r0, int n,
-                                            int R, int32_t* status) {
-  if (threadIdx.x < n) {
-    int s = slot_of[r0 + threadIdx.x];
-    if (s < 0 || s >= R) {
-      if (s != -1) set_status(status, MOE_DEV_BAD_EXPERT);
-      s = -1;
-    }
-    sh.slot[threadIdx.x] = s;
-    sh.w[threadIdx.x] = w != nullptr ? w[r0 + threadIdx.x] : 1.0f;
-  }
-  __syncthreads();
+                                            int tid, int R, int64_t ld, int32_t* status) {
+  if (tid >= n) return;
+  const int s = slot_of[r0 + tid];
+  const bool ok = s >= 0 && s < R;
+  if (!ok && s != -1) set_status(status, MOE_DEV_BAD_EXPERT);
+  sh.at[tid] = ok ? s * ld : -1;
+  sh.w[tid] = w != nullptr ? w[r0 + tid] : 1.0f;
 }
 
-// dw of a CTA's n routes: the warps' sums, added in warp order.
-template <int NB>
+// The warps of one token: SOLO, each warp of the CTA has its own token.
+template <bool SOLO>
+__device__ __forceinline__ void token_sync() {
+  if (SOLO)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+
+// dw of a token's n routes: the warps' sums, added in warp order.
+template <bool SOLO, int NB>
 __device__ __forceinline__ void write_dw(const float (&part)[NB][kBatch], float (*red)[kMaxK], const Routes& sh,
-                                         float* dw, int n) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+                                         float* dw, int n, int warp, int warps, int tid) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const float s = warp_sum8(part[b], lane);
     if ((lane & 3) == 0) red[warp][b * kBatch + (lane >> 2)] = s;
   }
-  __syncthreads();
-  if (threadIdx.x < n) {
-    float s = 0.f;
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += red[i][threadIdx.x];
-    dw[threadIdx.x] = sh.slot[threadIdx.x] < 0 ? 0.f : s;
+  token_sync<SOLO>();
+  if (tid < n) {
+    float s = red[SOLO ? warp : 0][tid];
+    if (!SOLO)
+      for (int i = 1; i < warps; ++i) s += red[i][tid];
+    dw[tid] = sh.at[tid] < 0 ? 0.f : s;
   }
 }
 
-// NB: batches of eight routes per CTA.  grid (token, group of jb routes).
-template <typename TT, typename TR, bool VEC, bool DOT, int NB>
-__global__ void __launch_bounds__(kMaxWarps * 32)
+constexpr int kSoloWarps = 4;  // tokens per CTA where a warp owns a token
+
+// NB: batches of eight routes.  SOLO: grid (tokens / kSoloWarps); else grid
+// (token, group of jb routes).
+template <typename TT, typename TR, bool VEC, bool DOT, int NB, bool SOLO>
+__global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
     spread_kernel(const TT* tok, int64_t ld_tok, const TR* dot, int64_t ld_dot, const int32_t* __restrict__ slot_of,
-                  const float* __restrict__ w, int k, int jb, int H, int R, TR* out, int64_t ld_out, float* dw,
+                  const float* __restrict__ w, int T, int k, int jb, int H, int R, TR* out, int64_t ld_out, float* dw,
                   int32_t* status) {
-  __shared__ Routes sh;
-  __shared__ float red[DOT ? kMaxWarps : 1][kMaxK];
+  __shared__ Routes routes[SOLO ? kSoloWarps : 1];
+  __shared__ float red[DOT ? (SOLO ? kSoloWarps : kMaxWarps) : 1][kMaxK];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int j0 = blockIdx.y * jb;
-  const int n = min(jb, k - j0);
-  const size_t r0 = static_cast<size_t>(blockIdx.x) * k + j0;
-  read_routes(sh, slot_of, w, r0, n, R, status);
-  const TT* row = tok + static_cast<int64_t>(blockIdx.x) * ld_tok;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = SOLO ? 1 : blockDim.x >> 5;
+  const int tid = SOLO ? lane : threadIdx.x;
+  const int64_t t = SOLO ? static_cast<int64_t>(blockIdx.x) * kSoloWarps + warp : blockIdx.x;
+  if (SOLO && t >= T) return;
+  const int j0 = SOLO ? 0 : blockIdx.y * jb;
+  const int n = SOLO ? k : min(jb, k - j0);
+  const size_t r0 = static_cast<size_t>(t) * k + j0;
+  Routes& sh = routes[SOLO ? warp : 0];
+  // dot and out have rows at the same slots: their strides differ
+  read_routes(sh, slot_of, w, r0, n, tid, R, 1, status);
+  token_sync<SOLO>();
+  const TT* row = tok + t * ld_tok;
   float part[DOT ? NB : 1][kBatch];
 #pragma unroll
   for (int b = 0; b < (DOT ? NB : 1); ++b)
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) part[b][u] = 0.f;
-  for (int base = warp * 256; base < H; base += warps * 256) {
+  for (int base = (SOLO ? 0 : warp) * 256; base < H; base += warps * 256) {
     const Cols<VEC> c(base, lane, 32);
     Raw8<TT> xr;
     load8<VEC>(row, c, H, xr);
@@ -118,7 +135,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
           const int j = b * kBatch + u;
-          const int s = j < n ? sh.slot[j] : -1;
+          const int64_t s = j < n ? sh.at[j] : -1;
           if (s >= 0)
             load8<VEC>(dot + s * ld_dot, c, H, v[DOT ? u : 0]);
           else
@@ -128,7 +145,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int j = b * kBatch + u;
-        const int s = j < n ? sh.slot[j] : -1;
+        const int64_t s = j < n ? sh.at[j] : -1;
         if (s < 0) continue;
         if (DOT) {
           float y[8];
@@ -143,28 +160,35 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
       }
     }
   }
-  if (DOT) write_dw<DOT ? NB : 1>(part, red, sh, dw + r0, n);
+  if (DOT) write_dw<SOLO, DOT ? NB : 1>(part, red, sh, dw + r0, n, warp, warps, tid);
 }
 
-// grid (token, part of the columns); with DOT a token's columns stay in one CTA.
-template <typename TR, typename TO, bool VEC, bool DOT, int NB>
-__global__ void __launch_bounds__(kMaxWarps * 32)
+// SOLO: grid (tokens / kSoloWarps); else grid (token, part of the columns),
+// one part with DOT.
+template <typename TR, typename TO, bool VEC, bool DOT, int NB, bool SOLO>
+__global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
     join_kernel(const TR* rows, int64_t ld_rows, const TR* dot, int64_t ld_dot, const int32_t* __restrict__ slot_of,
-                const float* __restrict__ w, int k, int H, int R, TO* out, int64_t ld_out, const TO* add,
+                const float* __restrict__ w, int T, int k, int H, int R, TO* out, int64_t ld_out, const TO* add,
                 int64_t ld_add, float* dw, int32_t* status) {
-  __shared__ Routes sh;
-  __shared__ float red[DOT ? kMaxWarps : 1][kMaxK];
+  __shared__ Routes routes[SOLO ? kSoloWarps : 1];
+  __shared__ float red[DOT ? (SOLO ? kSoloWarps : kMaxWarps) : 1][kMaxK];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int64_t t = blockIdx.x;
-  read_routes(sh, slot_of, w, static_cast<size_t>(t) * k, k, R, blockIdx.y == 0 ? status : nullptr);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = SOLO ? 1 : blockDim.x >> 5;
+  const int tid = SOLO ? lane : threadIdx.x;
+  const int64_t t = SOLO ? static_cast<int64_t>(blockIdx.x) * kSoloWarps + warp : blockIdx.x;
+  if (SOLO && t >= T) return;
+  Routes& sh = routes[SOLO ? warp : 0];
+  const size_t r0 = static_cast<size_t>(t) * k;
+  read_routes(sh, slot_of, w, r0, k, tid, R, ld_rows, SOLO || blockIdx.y == 0 ? status : nullptr);
+  token_sync<SOLO>();
   float part[DOT ? NB : 1][kBatch];
 #pragma unroll
   for (int b = 0; b < (DOT ? NB : 1); ++b)
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) part[b][u] = 0.f;
-  for (int base = (blockIdx.y * warps + warp) * 256; base < H; base += gridDim.y * warps * 256) {
+  const int first = SOLO ? 0 : blockIdx.y * warps + warp, stride = SOLO ? 1 : gridDim.y * warps;
+  for (int base = first * 256; base < H; base += stride * 256) {
     const Cols<VEC> c(base, lane, 32);
     float x[8], acc[8];
     if (DOT) {
@@ -181,16 +205,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int j = b * kBatch + u;
-        const int s = j < k ? sh.slot[j] : -1;
+        const int64_t s = j < k ? sh.at[j] : -1;
         if (s >= 0)
-          load8<VEC>(rows + s * ld_rows, c, H, v[u]);
+          load8<VEC>(rows + s, c, H, v[u]);
         else
           raw_zero(v[u]);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int j = b * kBatch + u;
-        if (j >= k || sh.slot[j] < 0) continue;
+        if (j >= k || sh.at[j] < 0) continue;
         float y[8];
         unpack(v[u], y);
         const float wj = sh.w[j];
@@ -211,46 +235,59 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
     }
     store8<VEC>(out + t * ld_out, c, H, acc);
   }
-  if (DOT) write_dw<DOT ? NB : 1>(part, red, sh, dw + static_cast<size_t>(t) * k, k);
+  if (DOT) write_dw<SOLO, DOT ? NB : 1>(part, red, sh, dw + r0, k, warp, warps, tid);
 }
 
-int warps_for(int H) { return std::min(kMaxWarps, (H + 255) / 256); }
+// Warps in flight that keep the memory busy, over the whole GPU.
+inline int warps_wanted() { return 24 * sm_count(); }
 
 template <typename TT, typename TR, bool VEC, bool DOT>
 cudaError_t spread(const Rows& tok, const Rows& dot, const int32_t* slot_of, const float* w, int T, int k, int H,
                    int R, const Rows& out, float* dw, int32_t* status, cudaStream_t st) {
-  const int warps = warps_for(H);
-  // few tokens: a token's routes are spread over several CTAs
-  const int want = 4 * sm_count();
-  const int jb = T >= want ? k : std::max<int64_t>(1, static_cast<int64_t>(k) * T / want);
-  const dim3 grid(T, (k + jb - 1) / jb);
-  auto go = [&](auto kern) {
-    return launch_pdl(kern, grid, dim3(warps * 32), 0, st, static_cast<const TT*>(tok.p), tok.ld,
-                      static_cast<const TR*>(dot.p), dot.ld, slot_of, w, k, jb, H, R, static_cast<TR*>(out.p), out.ld,
-                      dw, status);
+  const int pieces = (H + 255) / 256, want = warps_wanted();
+  // few tokens: more warps per token, then a token's routes over several CTAs
+  const int warps = std::min({kMaxWarps, pieces, (want + T - 1) / T});
+  const int split = static_cast<int>(std::min<int64_t>(k, std::max<int64_t>(1, want / (static_cast<int64_t>(T) * pieces))));
+  const int jb = (k + split - 1) / split;
+  auto go = [&](auto kern, dim3 grid, int threads) {
+    return launch_pdl(kern, grid, dim3(threads), 0, st, static_cast<const TT*>(tok.p), tok.ld,
+                      static_cast<const TR*>(dot.p), dot.ld, slot_of, w, T, k, jb, H, R, static_cast<TR*>(out.p),
+                      out.ld, dw, status);
   };
-  if (jb <= 16) return go(spread_kernel<TT, TR, VEC, DOT, 2>);
-  return go(spread_kernel<TT, TR, VEC, DOT, 4>);
+  if (warps == 1 && split == 1) {
+    const dim3 grid((T + kSoloWarps - 1) / kSoloWarps);
+    return k <= 16 ? go(spread_kernel<TT, TR, VEC, DOT, 2, true>, grid, kSoloWarps * 32)
+                   : go(spread_kernel<TT, TR, VEC, DOT, 4, true>, grid, kSoloWarps * 32);
+  }
+  const dim3 grid(T, (k + jb - 1) / jb);
+  return jb <= 16 ? go(spread_kernel<TT, TR, VEC, DOT, 2, false>, grid, warps * 32)
+                  : go(spread_kernel<TT, TR, VEC, DOT, 4, false>, grid, warps * 32);
 }
 
 template <typename TR, typename TO, bool VEC, bool DOT>
 cudaError_t join(const Rows& rows, const Rows& dot, const int32_t* slot_of, const float* w, int T, int k, int H, int R,
                  const Rows& out, const Rows& add, float* dw, int32_t* status, cudaStream_t st) {
   const int pieces = (H + 255) / 256;
-  int warps = warps_for(H);
+  // few tokens: more warps per token, without dw on SMs of their own
+  int warps = std::min({kMaxWarps, pieces, (warps_wanted() + T - 1) / T});
   int parts = 1;
-  if (!DOT && T < 4 * sm_count()) {  // few tokens: a token's columns are spread over several CTAs
+  if (!DOT && warps > 1 && T < 4 * sm_count()) {
     warps = 1;
-    parts = std::min(pieces, 1024);
+    parts = pieces;
   }
-  const dim3 grid(T, parts);
-  auto go = [&](auto kern) {
-    return launch_pdl(kern, grid, dim3(warps * 32), 0, st, static_cast<const TR*>(rows.p), rows.ld,
-                      static_cast<const TR*>(dot.p), dot.ld, slot_of, w, k, H, R, static_cast<TO*>(out.p), out.ld,
+  auto go = [&](auto kern, dim3 grid, int threads) {
+    return launch_pdl(kern, grid, dim3(threads), 0, st, static_cast<const TR*>(rows.p), rows.ld,
+                      static_cast<const TR*>(dot.p), dot.ld, slot_of, w, T, k, H, R, static_cast<TO*>(out.p), out.ld,
                       static_cast<const TO*>(add.p), add.ld, dw, status);
   };
-  if (k <= 16) return go(join_kernel<TR, TO, VEC, DOT, 2>);
-  return go(join_kernel<TR, TO, VEC, DOT, 4>);
+  if (warps == 1 && parts == 1) {
+    const dim3 grid((T + kSoloWarps - 1) / kSoloWarps);
+    return k <= 16 ? go(join_kernel<TR, TO, VEC, DOT, 2, true>, grid, kSoloWarps * 32)
+                   : go(join_kernel<TR, TO, VEC, DOT, 4, true>, grid, kSoloWarps * 32);
+  }
+  const dim3 grid(T, parts);
+  return k <= 16 ? go(join_kernel<TR, TO, VEC, DOT, 2, false>, grid, warps * 32)
+                 : go(join_kernel<TR, TO, VEC, DOT, 4, false>, grid, warps * 32);
 }
 
 // f(type tag of a, type tag of b)

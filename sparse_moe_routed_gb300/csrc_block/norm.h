@@ -11,14 +11,25 @@ namespace moe {
 namespace blk {
 
 constexpr int kMaxGroupThreads = 512;      // threads of a row's group, 8 * nch columns each
-constexpr int kNormSmem = 220 * 1024;      // shared memory for staged rows per CTA
-constexpr int kMaxStages = 4;              // rows staged per group
+#ifndef MINCH
+#define MINCH 1
+#endif
+#ifndef SMEMK
+#define SMEMK 220
+#endif
+constexpr int kNormSmem = SMEMK * 1024;      // shared memory for staged rows per CTA
+#ifndef MAXST
+#define MAXST 2
+#endif
+constexpr int kMaxStages = MAXST;              // rows staged per group
 constexpr int kMaxStagedChunks = 2;        // wider rows (H > 8192) are read without staging
 
 // How a launch cuts its rows: CTAs of `groups` groups of `nt` threads, each
 // group with `stages` rows of `stage` bytes in shared memory.
 struct NormPlan {
   int nt, nch, groups, stages, stage, grid, smem;
+  int gains;  // bytes of c1 and c2 behind the stages
+  int64_t by[8];  // bytes from a group's row to its next, per operand
 };
 
 // slot: bytes per thread of all operands' eight columns; max_threads: threads
@@ -29,26 +40,34 @@ inline NormPlan norm_plan(int T, int H, int slot, int max_threads) {
   NormPlan p;
   const int chunks = (H + 7) / 8;
   p.nch = chunks <= kMaxGroupThreads ? 1 : chunks <= 2 * kMaxGroupThreads ? 2 : 4;
+  if (p.nch < MINCH && chunks > 32) p.nch = MINCH;
   p.nt = ((chunks + p.nch - 1) / p.nch + 31) / 32 * 32;
   if (p.nch > 1) max_threads = kMaxGroupThreads;
   const int sms = sm_count();
   p.groups = std::max(1, std::min(p.nt == 32 ? 32 : 15, max_threads / p.nt));
   p.groups = std::max(1, std::min(p.groups, (T + sms - 1) / sms));
   p.stage = p.nch <= kMaxStagedChunks ? slot * p.nch * p.nt : 0;
-  while (p.groups > 1 && p.stage * p.groups * 2 > kNormSmem) --p.groups;
-  p.stages = p.stage > 0 ? std::max(1, std::min(kMaxStages, kNormSmem / (p.stage * p.groups))) : 1;
+  p.gains = p.nch <= kMaxStagedChunks ? 2 * 32 * p.nch * p.nt : 0;
+  const int room = kNormSmem - p.gains;
+  while (p.groups > 1 && p.stage * p.groups * 2 > room) --p.groups;
+  p.stages = p.stage > 0 ? std::max(1, std::min(kMaxStages, room / (p.stage * p.groups))) : 1;
   const int per_sm = std::max(1, std::min(max_threads / (p.nt * p.groups),
-                                          p.stage > 0 ? kNormSmem / (p.stage * p.groups * p.stages) : 8));
+                                          p.stage > 0 ? kNormSmem / (p.stage * p.groups * p.stages + p.gains) : 8));
   p.grid = std::max(1, std::min((T + p.groups - 1) / p.groups, sms * per_sm));
   const int rows = (T + p.grid * p.groups - 1) / (p.grid * p.groups);  // per group
   p.stages = std::max(1, std::min(p.stages, rows));
-  p.smem = p.stage * p.groups * p.stages;
+  p.smem = p.stage * p.groups * p.stages + p.gains;
   return p;
 }
 
-// The widest unit of adjacent columns that every row allows.
-inline int norm_unit(std::initializer_list<Rows> all) {
-  int g = 4;
+inline void plan_steps(NormPlan& p, std::initializer_list<Rows> all) {
+  int i = 0;
+  for (const Rows& r : all) p.by[i++] = static_cast<int64_t>(p.grid) * p.groups * r.ld * (r.type == MOE_ROW_F32 ? 4 : 2);
+}
+
+// The widest unit of adjacent columns that the width and every row allow.
+inline int norm_unit(int H, std::initializer_list<Rows> all) {
+  int g = H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
   for (const Rows& r : all) {
     if (r.p == nullptr) continue;
     const int bytes = r.type == MOE_ROW_F32 ? 4 : 2;

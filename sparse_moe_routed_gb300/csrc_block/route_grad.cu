@@ -28,25 +28,38 @@ namespace {
 constexpr int kUnit = 256;         // routes per unit
 constexpr int kPlanThreads = 1024;  // >= kMaxE
 constexpr int kBatch = 8;          // rows whose loads a thread has in flight
-constexpr int kMaxSlab = 256;      // threads per CTA, eight columns each
+constexpr int kRowThreads = 256;   // threads per CTA of the row sums
 
-// Workspace (int32 unless said): [E+1] first unit of each expert, [E] first
-// partial row of each expert, [1] whether the offsets are bad, then, 256-byte
-// aligned, the partial rows [max_partials][H] f32 and their bias sums
-// [max_partials] f32.
+// A unit: n routes of expert e from slot s0 on; part is where its partial row
+// goes, or -1 where it is the expert's only unit and writes the result.
+struct Unit {
+  int32_t e, s0, n, part;
+};
+
+// Workspace, each part 256-byte aligned: the units, each expert's first
+// partial row and how many it has ({first, count}, count 0: written
+// directly), partial rows [..][H] f32, their bias sums f32.
+__host__ __device__ inline int max_units(int R, int E) { return E + R / kUnit; }
 __host__ __device__ inline int max_partials(int R) { return 2 * (R / kUnit) + 1; }
+__host__ __device__ inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 struct Ws {
-  int32_t *unit0, *part0, *bad;
+  Unit* units;
+  int2* parts;
   float *rows, *bias;
+  size_t bytes;
 };
 __host__ __device__ inline Ws ws_layout(void* p, int R, int E, int H) {
+  char* c = static_cast<char*>(p);
+  size_t at = 0;
   Ws w;
-  w.unit0 = static_cast<int32_t*>(p);
-  w.part0 = w.unit0 + E + 1;
-  w.bad = w.part0 + E;
-  const size_t head = (static_cast<size_t>(2 * E + 2) * 4 + 255) / 256 * 256;
-  w.rows = reinterpret_cast<float*>(static_cast<char*>(p) + head);
-  w.bias = w.rows + static_cast<size_t>(max_partials(R)) * H;
+  w.units = reinterpret_cast<Unit*>(c + at);
+  at += round256(sizeof(Unit) * max_units(R, E));
+  w.parts = reinterpret_cast<int2*>(c + at);
+  at += round256(sizeof(int2) * E);
+  w.rows = reinterpret_cast<float*>(c + at);
+  at += round256(sizeof(float) * static_cast<size_t>(max_partials(R)) * H);
+  w.bias = reinterpret_cast<float*>(c + at);
+  w.bytes = at + round256(sizeof(float) * max_partials(R));
   return w;
 }
 
@@ -71,7 +84,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     route_plan_kernel(const float* __restrict__ dw, const float* __restrict__ w, const int32_t* __restrict__ offsets,
                       int T, int k, int E, int H, float* __restrict__ dl, void* ws, int plan, int32_t* status) {
   __shared__ int warp_tot[32];
-  __shared__ int bad;
+  __shared__ int first[kPlanThreads], start[kPlanThreads], count[kPlanThreads], part0[kPlanThreads];
+  __shared__ int bad, total;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31;
@@ -81,25 +95,41 @@ __global__ void __launch_bounds__(kPlanThreads)
     const Ws s = ws_layout(ws, R, E, H);
     if (tid == 0) bad = 0;
     __syncthreads();
-    int n = 0;
+    int n = 0, a = 0;
     if (tid < E && R > 0) {  // no routes: the grouping wrote no offsets
-      const int a = offsets[tid], b = offsets[tid + 1];
+      a = offsets[tid];
+      const int b = offsets[tid + 1];
       if (a < 0 || b < a || b > R || (tid == 0 && a != 0) || (tid == E - 1 && b != R)) bad = 1;
       n = b - a;
     }
     __syncthreads();
+    // bad offsets: every unit is marked as none
     const int units = tid < E && !bad ? max(1, (n + kUnit - 1) / kUnit) : 0;
-    const int u0 = block_scan_excl(units, warp_tot);
     const int p0 = block_scan_excl(units > 1 ? units : 0, warp_tot);
-    if (tid < E) {
-      s.unit0[tid] = u0;
-      s.part0[tid] = p0;
-      if (tid == E - 1) s.unit0[E] = u0 + units;
+    first[tid] = block_scan_excl(units, warp_tot);
+    start[tid] = a;
+    count[tid] = n;
+    part0[tid] = units > 1 ? p0 : -1;
+    if (tid < E) s.parts[tid] = make_int2(p0, units > 1 ? units : 0);
+    if (tid == kPlanThreads - 1) total = first[tid] + units;
+    __syncthreads();
+    for (int u = tid; u < max_units(R, E); u += kPlanThreads) {
+      Unit d = {-1, 0, 0, -1};
+      if (u < total) {
+        int lo = 0, hi = E;  // the expert whose first unit is the last at or before u
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (first[mid] <= u)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        const int i = u - first[lo];
+        d = {lo, start[lo] + i * kUnit, min(kUnit, count[lo] - i * kUnit), part0[lo] < 0 ? -1 : part0[lo] + i};
+      }
+      s.units[u] = d;
     }
-    if (tid == 0) {
-      *s.bad = bad;
-      if (bad) set_status(status, MOE_DEV_BAD_EXPERT);
-    }
+    if (tid == 0 && bad) set_status(status, MOE_DEV_BAD_EXPERT);
     return;
   }
   const int warps = kPlanThreads / 32;
@@ -114,80 +144,86 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// grid (unit, slab of 8 * blockDim.x columns)
+// grid (unit, slab of 8 cw columns).  The CTA's threads are cw columns of
+// eight by kRowThreads / cw row groups; a row group sums every such route of
+// the unit, and the first adds the others in order.
 template <bool VEC>
-__global__ void __launch_bounds__(kMaxSlab)
-    route_rows_kernel(const float* __restrict__ dl, const int32_t* __restrict__ offsets,
-                      const int32_t* __restrict__ perm, const bf16_t* __restrict__ x, int64_t ldx, int T, int k, int E,
-                      int H, float* dwr, int64_t ld_dw, float* dbias, void* ws, int32_t* status) {
-  __shared__ int expert;
-  __shared__ int tok[kUnit];
-  __shared__ float g[kUnit];
+__global__ void __launch_bounds__(kRowThreads)
+    route_rows_kernel(const float* __restrict__ dl, const int32_t* __restrict__ perm, const bf16_t* __restrict__ x,
+                      int64_t ldx, int T, int k, int E, int H, int cw, float* dwr, int64_t ld_dw, float* dbias,
+                      void* ws, int32_t* status) {
+  __shared__ int2 route[kUnit];  // token (-1: none) and the bits of dl
+  __shared__ float red[kRowThreads * 8];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
   const int R = T * k;
   const Ws s = ws_layout(ws, R, E, H);
-  if (*s.bad) return;
-  const int u = blockIdx.x;
-  if (tid == 0) expert = -1;
-  __syncthreads();
-  for (int e = tid; e < E; e += blockDim.x)
-    if (s.unit0[e] <= u && u < s.unit0[e + 1]) expert = e;
-  __syncthreads();
-  const int e = expert;
-  if (e < 0) return;
-  const int part = u - s.unit0[e];
-  const bool direct = s.unit0[e + 1] - s.unit0[e] == 1;
-  const int a = R > 0 ? offsets[e] + part * kUnit : 0;
-  const int n = R > 0 ? min(kUnit, offsets[e + 1] - a) : 0;
-  for (int i = tid; i < n; i += blockDim.x) {
-    const int r = perm[a + i];
+  const Unit un = s.units[blockIdx.x];
+  if (un.e < 0) return;
+  const int n = un.n;
+  for (int i = tid; i < n; i += kRowThreads) {
+    const int r = perm[un.s0 + i];
     const bool ok = r >= 0 && r < R;
     if (!ok) set_status(status, MOE_DEV_BAD_EXPERT);
-    tok[i] = ok ? r / k : -1;
-    g[i] = ok ? dl[r] : 0.f;
+    route[i] = make_int2(ok ? r / k : -1, ok ? __float_as_int(dl[r]) : 0);
   }
   __syncthreads();
   if (dbias != nullptr && blockIdx.y == 0 && tid < 32) {
     float b = 0.f;
-    for (int i = tid; i < n; i += 32) b += g[i];
+    for (int i = tid; i < n; i += 32) b += __int_as_float(route[i].y);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
-    if (tid == 0) (direct ? dbias[e] : s.bias[s.part0[e] + part]) = b;
+    if (tid == 0) (un.part < 0 ? dbias[un.e] : s.bias[un.part]) = b;
   }
   if (dwr == nullptr) return;
-  const Cols<VEC> c(blockIdx.y * blockDim.x * 8, tid, blockDim.x);
+  const int rg = kRowThreads / cw, g = tid / cw, col = tid - g * cw;
+  const Cols<VEC> c(blockIdx.y * cw * 8, col, cw);
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += kBatch) {
+  for (int i0 = g; i0 < n; i0 += kBatch * rg) {
     Raw8<bf16_t> v[kBatch];
+    float w[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int t = i0 + b < n ? tok[i0 + b] : -1;
-      if (t >= 0)
-        load8<VEC>(x + t * ldx, c, H, v[b]);
+      const int i = i0 + b * rg;
+      const int2 rt = i < n ? route[i] : make_int2(-1, 0);
+      w[b] = __int_as_float(rt.y);
+      if (rt.x >= 0)
+        load8<VEC>(x + rt.x * ldx, c, H, v[b]);
       else
         raw_zero(v[b]);
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      if (i0 + b >= n || tok[i0 + b] < 0) continue;
       float f[8];
       unpack(v[b], f);
-      const float w = g[i0 + b];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[b], f[i], acc[i]);
     }
   }
-  if (direct)
-    store8<VEC>(dwr + e * ld_dw, c, H, acc);
-  else
-    // partial rows are packed [H]: whole vectors only where H allows it
-    for (int i = 0; i < 8; ++i)
-      if (c.first + i * c.step < H)
-        s.rows[static_cast<size_t>(s.part0[e] + part) * H + c.first + i * c.step] = acc[i];
+  if (rg > 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[i * kRowThreads + tid] = acc[i];
+    __syncthreads();
+    if (g > 0) return;
+    for (int o = 1; o < rg; ++o)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += red[i * kRowThreads + o * cw + col];
+  }
+  if (un.part < 0) {
+    store8<VEC>(dwr + un.e * ld_dw, c, H, acc);
+  } else {
+    float* out = s.rows + static_cast<size_t>(un.part) * H;  // packed: whole vectors only where H allows it
+    if (VEC && H % 8 == 0) {
+      store8<VEC>(out, c, H, acc);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c.first + i * c.step < H) out[c.first + i * c.step] = acc[i];
+    }
+  }
 }
 
 // grid (expert, 256 columns): the experts of several units.
@@ -196,14 +232,13 @@ __global__ void __launch_bounds__(256) route_join_kernel(int T, int k, int E, in
   pdl_wait();
   pdl_trigger();
   const Ws s = ws_layout(ws, T * k, E, H);
-  if (*s.bad) return;
   const int e = blockIdx.x;
-  const int n = s.unit0[e + 1] - s.unit0[e];
-  if (n <= 1) return;
-  const int p0 = s.part0[e];
+  const int p0 = s.parts[e].x, n = s.parts[e].y;
+  if (n == 0) return;
   const int col = blockIdx.y * 256 + threadIdx.x;
   if (dwr != nullptr && col < H) {
     float a = 0.f;
+#pragma unroll 4
     for (int p = 0; p < n; ++p) a += s.rows[static_cast<size_t>(p0 + p) * H + col];
     dwr[e * ld_dw + col] = a;
   }
@@ -217,9 +252,7 @@ __global__ void __launch_bounds__(256) route_join_kernel(int T, int k, int E, in
 }  // namespace
 
 size_t route_grad_ws_bytes(int T, int k, int E, int H) {
-  const int R = T * k;
-  const size_t head = (static_cast<size_t>(2 * E + 2) * 4 + 255) / 256 * 256;
-  return (head + static_cast<size_t>(max_partials(R)) * (H + 1) * sizeof(float) + 255) / 256 * 256;
+  return ws_layout(nullptr, T * k, E, H).bytes;
 }
 
 cudaError_t launch_route_grad(const RouteGradArgs& a, cudaStream_t st) {
@@ -239,14 +272,14 @@ cudaError_t launch_route_grad(const RouteGradArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   if (!plan) return cudaSuccess;
+  // 64 columns of eight by 4 row groups; narrower rows: fewer columns
   const int chunks = (a.H + 7) / 8;
-  const int slabs = a.dw_router.p != nullptr ? (chunks + kMaxSlab - 1) / kMaxSlab : 1;
-  const int nt = a.dw_router.p != nullptr ? ((chunks + slabs - 1) / slabs + 31) / 32 * 32 : 128;
-  const int units = a.E + R / kUnit;
+  const int cw = chunks > 32 ? 64 : chunks > 16 ? 32 : 16;
+  const int slabs = a.dw_router.p != nullptr ? (chunks + cw - 1) / cw : 1;
   const bool vec = vec_ok(a.x) && vec_ok(a.dw_router);
   auto go = [&](auto kern) {
-    return launch_pdl(kern, dim3(units, slabs), dim3(nt), 0, st, a.dlogits, a.offsets, a.perm,
-                      static_cast<const bf16_t*>(a.x.p), a.x.ld, a.T, a.k, a.E, a.H,
+    return launch_pdl(kern, dim3(max_units(R, a.E), slabs), dim3(kRowThreads), 0, st, a.dlogits, a.perm,
+                      static_cast<const bf16_t*>(a.x.p), a.x.ld, a.T, a.k, a.E, a.H, cw,
                       static_cast<float*>(a.dw_router.p), a.dw_router.ld, a.dbias, a.ws, a.status);
   };
   e = vec ? go(route_rows_kernel<true>) : go(route_rows_kernel<false>);

@@ -2,29 +2,67 @@
 //
 // A group of nt threads owns a row and thread `tid` its columns
 //   col(h, i) = h * 8 nt + ((i / G) * nt + tid) * G + i % G,   i = 0..7
-// for h = 0..NCH-1: G adjacent columns at a time, so that every access of a
-// warp covers whole sectors (G = 4: 16 bytes of fp32, 8 of bf16 a lane; G = 2:
-// rows that start on even columns; G = 1: any).  Each thread copies its own
+// for h = 0..NCH-1: G adjacent columns at a time (G divides H), so that every
+// access of a warp covers whole sectors (G = 4: 16 bytes of fp32, 8 of bf16 a
+// lane; G = 2: even widths; G = 1: any) and no unit of G is partial.  Each thread copies its own
 // columns into its own places in shared memory and reads them back itself:
 // copies of the rows ahead stay in flight while a row is worked on, cost no
 // registers, and need no barrier, only the thread's own wait.
 #pragma once
 
+#include "launch.h"
 #include "rows.cuh"
 
 namespace moe {
 namespace blk {
 
+// Eight columns as four pairs: two fp32 operations per instruction.
+struct V8 {
+  float2 v[4];
+};
+__device__ __forceinline__ float2 splat(float a) { return make_float2(a, a); }
+__device__ __forceinline__ V8 operator*(const V8& a, const V8& b) {
+  V8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], b.v[i]);
+  return r;
+}
+__device__ __forceinline__ V8 operator*(const V8& a, float b) {
+  V8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], splat(b));
+  return r;
+}
+__device__ __forceinline__ V8 fma8(const V8& a, const V8& b, const V8& c) {
+  V8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], b.v[i], c.v[i]);
+  return r;
+}
+__device__ __forceinline__ V8 fma8(const V8& a, float b, const V8& c) {
+  V8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], splat(b), c.v[i]);
+  return r;
+}
+// s += sum a b
+__device__ __forceinline__ void dot8(const V8& a, const V8& b, float2& s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = __ffma2_rn(a.v[i], b.v[i], s);
+}
+
 // Bytes of one thread's eight columns of one array.
 template <typename T>
 constexpr int kSlot = 8 * static_cast<int>(sizeof(T));
 
+// BYTES from src to shared memory; `have` 0: zeros instead, src is not read.
 template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int have) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES < 16 ? BYTES : 8) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(have), "n"(BYTES)
+                 : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most `left` of the thread's committed groups are in flight.
@@ -42,106 +80,117 @@ __device__ __forceinline__ int col0(int h, int i, int tid, int nt) {
   return (h * (8 / G) + i / G) * nt * G + tid * G + i % G;
 }
 
-// Thread's columns of a row into its places; columns past H become zero.
-// The array's region holds NCH * nt * kSlot<T> bytes.
+// Thread's columns of a row into its places, columns past H as zeros.  src:
+// the thread's first column of the row; at: its first place.  The array's
+// region holds NCH * nt * kSlot<T> bytes.
 template <typename T, int G, int NCH>
-__device__ __forceinline__ void stage_row(unsigned char* region, const T* row, int tid, int nt, int H) {
+__device__ __forceinline__ void stage_row(unsigned char* at, const T* src, int tid, int nt, int H) {
   constexpr int UB = G * static_cast<int>(sizeof(T));  // bytes of one unit of G columns
 #pragma unroll
   for (int p = 0; p < NCH * 8 / G; ++p) {
-    const int c = (p * nt + tid) * G;
-    unsigned char* at = region + static_cast<size_t>(p * nt + tid) * UB;
-    if (UB >= 4 && c + G <= H) {
-      copy_async<(UB >= 4 ? UB : 4)>(static_cast<uint32_t>(__cvta_generic_to_shared(at)), row + c);
+    const bool in = (p * nt + tid) * G < H;
+    if constexpr (UB >= 4) {
+      copy_async<UB>(static_cast<uint32_t>(__cvta_generic_to_shared(at)) + p * nt * UB, src + p * nt * G, in ? UB : 0);
     } else {
-#pragma unroll
-      for (int i = 0; i < G; ++i) reinterpret_cast<T*>(at)[i] = c + i < H ? row[c + i] : T(0);
+      reinterpret_cast<T*>(at)[p * nt] = in ? src[p * nt] : T(0);
     }
   }
 }
 
+// Element i of the eight, for the units narrower than a pair.
+__device__ __forceinline__ float& el(V8& f, int i) { return i & 1 ? f.v[i / 2].y : f.v[i / 2].x; }
+__device__ __forceinline__ float el(const V8& f, int i) { return i & 1 ? f.v[i / 2].y : f.v[i / 2].x; }
+__device__ __forceinline__ float2 widen(uint32_t two) {
+  return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+}
+
+// Unit p of G columns.
 template <typename T, int G>
-__device__ __forceinline__ void read_unit(const unsigned char* at, float* f) {
+__device__ __forceinline__ void read_unit(const unsigned char* at, int p, V8& f) {
   if constexpr (sizeof(T) == 4) {
     if constexpr (G == 4) {
       const float4 v = *reinterpret_cast<const float4*>(at);
-      f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+      f.v[2 * p] = make_float2(v.x, v.y);
+      f.v[2 * p + 1] = make_float2(v.z, v.w);
     } else if constexpr (G == 2) {
-      const float2 v = *reinterpret_cast<const float2*>(at);
-      f[0] = v.x, f[1] = v.y;
+      f.v[p] = *reinterpret_cast<const float2*>(at);
     } else {
-      f[0] = *reinterpret_cast<const float*>(at);
+      el(f, p) = *reinterpret_cast<const float*>(at);
     }
   } else {
     if constexpr (G == 4) {
       const uint2 v = *reinterpret_cast<const uint2*>(at);
-      f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xffff0000u);
-      f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xffff0000u);
+      f.v[2 * p] = widen(v.x);
+      f.v[2 * p + 1] = widen(v.y);
     } else if constexpr (G == 2) {
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(at);
-      f[0] = __uint_as_float(v << 16), f[1] = __uint_as_float(v & 0xffff0000u);
+      f.v[p] = widen(*reinterpret_cast<const uint32_t*>(at));
     } else {
-      f[0] = bf16_to_f32(*reinterpret_cast<const bf16_t*>(at));
+      el(f, p) = bf16_to_f32(*reinterpret_cast<const bf16_t*>(at));
     }
   }
 }
 
-// Chunk h of the thread's columns from its places.
+// Chunk h of the thread's columns; at: its first place.
 template <typename T, int G>
-__device__ __forceinline__ void read_staged(const unsigned char* region, int h, int tid, int nt, float (&f)[8]) {
+__device__ __forceinline__ void read_staged(const unsigned char* at, int h, int nt, V8& f) {
   constexpr int UB = G * static_cast<int>(sizeof(T));
 #pragma unroll
-  for (int p = 0; p < 8 / G; ++p)
-    read_unit<T, G>(region + static_cast<size_t>((h * (8 / G) + p) * nt + tid) * UB, f + p * G);
+  for (int p = 0; p < 8 / G; ++p) read_unit<T, G>(at + (h * (8 / G) + p) * nt * UB, p, f);
 }
 
 // The same from global memory; columns past H read as zero.
 template <typename T, int G>
-__device__ __forceinline__ void read_global(const T* row, int h, int tid, int nt, int H, float (&f)[8]) {
+__device__ __forceinline__ void read_global(const T* row, int h, int tid, int nt, int H, V8& f) {
 #pragma unroll
   for (int p = 0; p < 8 / G; ++p) {
     const int c = ((h * (8 / G) + p) * nt + tid) * G;
-    if (c + G <= H) {
-      read_unit<T, G>(reinterpret_cast<const unsigned char*>(row + c), f + p * G);
-    } else {
 #pragma unroll
-      for (int i = 0; i < G; ++i) f[p * G + i] = c + i < H ? as_f32(row[c + i]) : 0.f;
-    }
+    for (int i = 0; i < G; ++i) el(f, p * G + i) = 0.f;
+    if (c < H) read_unit<T, G>(reinterpret_cast<const unsigned char*>(row + c), p, f);
   }
 }
 
+// dst: the thread's first column of the row.
 template <typename T, int G>
-__device__ __forceinline__ void write_row(T* row, int h, int tid, int nt, int H, const float (&f)[8]) {
+__device__ __forceinline__ void write_row(T* dst, int h, int tid, int nt, int H, const V8& f) {
 #pragma unroll
   for (int p = 0; p < 8 / G; ++p) {
-    const int c = ((h * (8 / G) + p) * nt + tid) * G;
-    if (c + G <= H) {
-      if constexpr (sizeof(T) == 4) {
-        if constexpr (G == 4)
-          *reinterpret_cast<float4*>(row + c) = make_float4(f[p * G], f[p * G + 1], f[p * G + 2], f[p * G + 3]);
-        else if constexpr (G == 2)
-          *reinterpret_cast<float2*>(row + c) = make_float2(f[p * G], f[p * G + 1]);
-        else
-          row[c] = f[p];
-      } else {
-        if constexpr (G == 4)
-          *reinterpret_cast<uint2*>(row + c) =
-              make_uint2(pack2(f[p * G], f[p * G + 1]), pack2(f[p * G + 2], f[p * G + 3]));
-        else if constexpr (G == 2)
-          *reinterpret_cast<uint32_t*>(row + c) = pack2(f[p * G], f[p * G + 1]);
-        else
-          row[c] = f32_to_bf16(f[p]);
-      }
+    const int at = (h * (8 / G) + p) * nt * G;
+    if (at + tid * G >= H) continue;
+    if constexpr (sizeof(T) == 4) {
+      if constexpr (G == 4)
+        *reinterpret_cast<float4*>(dst + at) =
+            make_float4(f.v[2 * p].x, f.v[2 * p].y, f.v[2 * p + 1].x, f.v[2 * p + 1].y);
+      else if constexpr (G == 2)
+        *reinterpret_cast<float2*>(dst + at) = f.v[p];
+      else
+        dst[at] = el(f, p);
     } else {
-#pragma unroll
-      for (int i = 0; i < G; ++i)
-        if (c + i < H) put(row + c + i, f[p * G + i]);
+      if constexpr (G == 4)
+        *reinterpret_cast<uint2*>(dst + at) =
+            make_uint2(pack2(f.v[2 * p].x, f.v[2 * p].y), pack2(f.v[2 * p + 1].x, f.v[2 * p + 1].y));
+      else if constexpr (G == 2)
+        *reinterpret_cast<uint32_t*>(dst + at) = pack2(f.v[p].x, f.v[p].y);
+      else
+        dst[at] = f32_to_bf16(el(f, p));
     }
   }
 }
 
-// Sum of v over the group's nt threads.  `buf` alternates between successive
-// sums: a buffer is written again only after the barrier of the sum between.
+// The thread's first column of row `row`; null rows stay null.
+template <typename T>
+__device__ __forceinline__ T* first_column(const Rows& r, int64_t row, int col) {
+  return r.p == nullptr ? nullptr : static_cast<T*>(r.p) + row * r.ld + col;
+}
+// Moves p by a launch constant (bytes), which the instruction itself can hold.
+template <typename T>
+__device__ __forceinline__ void advance(T*& p, int64_t bytes) {
+  p = reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + bytes);
+}
+
+// Sum of v over the group's nt threads, four warps' sums to a read.  `buf`
+// (zeros behind the group's warps) alternates between successive sums: a
+// buffer is written again only after the barrier of the sum between.
 __device__ __forceinline__ float group_sum(float v, float (*buf)[16], int& which, int tid, int nt, int group) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -151,8 +200,19 @@ __device__ __forceinline__ float group_sum(float v, float (*buf)[16], int& which
   if ((tid & 31) == 0) b[tid >> 5] = v;
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(nt) : "memory");
   float s = 0.f;
-  for (int i = 0; i < nt / 32; ++i) s += b[i];
+  for (int i = 0; i < nt; i += 128) {
+    const float4 w = *reinterpret_cast<const float4*>(b + i / 32);
+    s += (w.x + w.y) + (w.z + w.w);
+  }
   return s;
+}
+// Zeros the buffers of every group's sums and the rows' places; the CTA's
+// threads call it together.
+__device__ __forceinline__ void stage_init(float (*buf)[2][16], unsigned char* smem, int bytes) {
+  for (int i = threadIdx.x; i < 15 * 2 * 16; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+  for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
+    *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
+  __syncthreads();
 }
 
 __device__ __forceinline__ float gain(const float* gamma, int c) { return gamma != nullptr ? 1.0f + gamma[c] : 1.0f; }
