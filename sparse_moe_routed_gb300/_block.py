@@ -70,157 +70,155 @@ def load():
         return lib
 
 
-class _Call:
-    """The checks of one call: every tensor on one GPU, of the shape asked."""
-
-    __slots__ = ("fn", "dev")
-
-    def __init__(self, fn, t):
-        self.fn = fn
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise MoEError(fn, MOE_EINVAL, "tensors must be on a GPU")
-        self.dev = t.get_device()
-
-    def no(self, status, what):
-        raise MoEError(self.fn, status, what)
-
-    def _tensor(self, t, name):
-        if not isinstance(t, torch.Tensor) or t.get_device() != self.dev:
-            self.no(MOE_EINVAL, f"{name} is not a tensor on GPU {self.dev}")
-
-    def rows(self, t, name, n, H, dtype=None):
-        """(pointer, row stride) of a [n, H] matrix; (None, 0) for None."""
-        if t is None:
-            return None, 0
-        self._tensor(t, name)
-        if tuple(t.shape) != (n, H):
-            self.no(MOE_ESHAPE, f"{name} has shape {tuple(t.shape)}, expected {(n, H)}")
-        if t.dtype not in _TYPES if dtype is None else t.dtype != dtype:
-            self.no(MOE_EINVAL, f"{name} has type {t.dtype}, expected {dtype or 'float32 or bfloat16'}")
-        ld, step = t.stride()
-        if step != 1 and H > 1:
-            self.no(MOE_EINVAL, f"{name}: the elements of a row must be adjacent")
-        return t.data_ptr(), ld if n > 1 else max(ld, H)
-
-    def flat(self, t, name, shape, dtype=torch.float32):
-        """Pointer of a contiguous array; None for None."""
-        if t is None:
-            return None
-        self._tensor(t, name)
-        if tuple(t.shape) != shape:
-            self.no(MOE_ESHAPE, f"{name} has shape {tuple(t.shape)}, expected {shape}")
-        if t.dtype != dtype:
-            self.no(MOE_EINVAL, f"{name} has type {t.dtype}, expected {dtype}")
-        if not t.is_contiguous():
-            self.no(MOE_EINVAL, f"{name} is not contiguous")
-        return t.data_ptr()
-
-    def bytes(self, t, name):
-        """(pointer, size in bytes) of a workspace; (None, 0) for None."""
-        if t is None:
-            return None, 0
-        self._tensor(t, name)
-        if not t.is_contiguous():
-            self.no(MOE_EINVAL, f"{name} is not contiguous")
-        return t.data_ptr(), t.numel() * t.element_size()
-
-    def matrix(self, t, name):
-        """Rows, width and type of the matrix that the others are measured by."""
-        self._tensor(t, name)
-        if t.dim() != 2:
-            self.no(MOE_ESHAPE, f"{name} must be two-dimensional")
-        if t.dtype not in _TYPES:
-            self.no(MOE_EINVAL, f"{name} has type {t.dtype}, expected float32 or bfloat16")
-        return t.shape[0], t.shape[1], _TYPES[t.dtype]
-
-    def issue(self, stream, *args):
-        """The C call with the GPU of its tensors current, on `stream` or that GPU's current stream."""
-        fn = getattr(load(), self.fn)
-        if self.dev == torch.cuda.current_device():
-            st = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
-        else:
-            with torch.cuda.device(self.dev):
-                st = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
-        if st != MOE_OK:
-            raise MoEError(self.fn, st, _lib.status_str(st))
+# The checks of a call.  ``fn`` is its name, ``dev`` the GPU of its tensors (-1:
+# they are on the CPU).
+def _no(fn, status, what):
+    raise MoEError(fn, status, what)
 
 
-def _routes(c, inv_perm, T, name="inv_perm"):
-    if not isinstance(inv_perm, torch.Tensor) or inv_perm.dim() != 2:
-        c.no(MOE_ESHAPE, f"{name} must be [T, k]")
+def _matrix(fn, t, name):
+    """(rows, width, type, GPU) of the matrix that the others are measured by."""
+    if t.dim() != 2:
+        _no(fn, MOE_ESHAPE, f"{name} must be two-dimensional")
+    ty = _TYPES.get(t.dtype)
+    if ty is None:
+        _no(fn, MOE_EINVAL, f"{name} has type {t.dtype}, expected float32 or bfloat16")
+    n, H = t.shape
+    return n, H, ty, t.get_device()
+
+
+def _tensor_no(fn, dev, t, name, shape, dtype):
+    if t.get_device() != dev or dev < 0:
+        _no(fn, MOE_EINVAL, f"{name} is not on GPU {dev}" if dev >= 0 else "tensors must be on a GPU")
+    if t.shape != shape:
+        _no(fn, MOE_ESHAPE, f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    _no(fn, MOE_EINVAL, f"{name} has type {t.dtype}, expected {dtype}")
+
+
+def _rows(fn, dev, t, name, n, H, dtype):
+    """(pointer, row stride) of a [n, H] matrix; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != (n, H) or dev < 0:
+        _tensor_no(fn, dev, t, name, (n, H), dtype)
+    ld, step = t.stride()
+    if step != 1 and H > 1:
+        _no(fn, MOE_EINVAL, f"{name}: the elements of a row must be adjacent")
+    return t.data_ptr(), ld if n > 1 else max(ld, H)
+
+
+def _flat(fn, dev, t, name, shape, dtype=torch.float32):
+    """Pointer of a contiguous array; None for None."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or dev < 0:
+        _tensor_no(fn, dev, t, name, shape, dtype)
+    if not t.is_contiguous():
+        _no(fn, MOE_EINVAL, f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+def _bytes(fn, dev, t, name):
+    """(pointer, size in bytes) of a workspace; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or dev < 0:
+        _no(fn, MOE_EINVAL, f"{name} is not on GPU {dev}")
+    if not t.is_contiguous():
+        _no(fn, MOE_EINVAL, f"{name} is not contiguous")
+    return t.data_ptr(), t.nbytes
+
+
+def _routes(fn, dev, inv_perm, T, name="inv_perm"):
+    if inv_perm.dim() != 2:
+        _no(fn, MOE_ESHAPE, f"{name} must be [T, k]")
     k = inv_perm.shape[1]
-    return k, c.flat(inv_perm, name, (T, k), torch.int32)
+    return k, _flat(fn, dev, inv_perm, name, (T, k), torch.int32)
+
+
+def _issue(fn, dev, stream, args):
+    """The C call with the GPU of its tensors current, on `stream` or that GPU's current stream."""
+    f = getattr(load(), fn)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        st = f(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, raw)
+    if st != MOE_OK:
+        raise MoEError(fn, st, _lib.status_str(st))
 
 
 def moe_dispatch(x, inv_perm, x_perm, w=None, dev_status=None, stream=None):
     """x_perm[inv_perm[t,j]] = w[t,j] * x[t] (w None: 1); routes of slot -1 and rows without a route are left out."""
-    c = _Call("moe_dispatch", x)
-    T, H, ty = c.matrix(x, "x")
-    k, inv = _routes(c, inv_perm, T)
-    R = c.matrix(x_perm, "x_perm")[0]
-    px, ldx = c.rows(x, "x", T, H)
-    pp, ldp = c.rows(x_perm, "x_perm", R, H, x.dtype)
-    c.issue(stream, px, ldx, ty, inv, c.flat(w, "w", (T, k)), T, k, H, R, pp, ldp,
-            c.flat(dev_status, "dev_status", (1,), torch.int32))
+    fn = "moe_dispatch"
+    T, H, ty, dev = _matrix(fn, x, "x")
+    k, inv = _routes(fn, dev, inv_perm, T)
+    R = _matrix(fn, x_perm, "x_perm")[0]
+    px, ldx = _rows(fn, dev, x, "x", T, H, x.dtype)
+    pp, ldp = _rows(fn, dev, x_perm, "x_perm", R, H, x.dtype)
+    _issue(fn, dev, stream, (px, ldx, ty, inv, _flat(fn, dev, w, "w", (T, k)), T, k, H, R, pp, ldp,
+                             _flat(fn, dev, dev_status, "dev_status", (1,), torch.int32)))
 
 
 def moe_dispatch_backward(dx_perm, inv_perm, dx, w=None, x=None, dw=None, add=None, dev_status=None, stream=None):
     """dx = add + sum_j w * dx_perm[inv_perm]; with dw (and x), dw[t,j] = <dx_perm[inv_perm[t,j]], x[t]>."""
-    c = _Call("moe_dispatch_backward", dx)
-    T, H, dty = c.matrix(dx, "dx")
-    k, inv = _routes(c, inv_perm, T)
-    R, _, ty = c.matrix(dx_perm, "dx_perm")
-    pp, ldp = c.rows(dx_perm, "dx_perm", R, H)
-    px, ldx = c.rows(x, "x", T, H, dx_perm.dtype)
-    pd, ldd = c.rows(dx, "dx", T, H)
-    pa, lda = c.rows(add, "add", T, H, dx.dtype)
-    c.issue(stream, pp, ldp, ty, inv, c.flat(w, "w", (T, k)), px, ldx, T, k, H, R, pd, ldd, dty, pa, lda,
-            c.flat(dw, "dw", (T, k)), c.flat(dev_status, "dev_status", (1,), torch.int32))
+    fn = "moe_dispatch_backward"
+    T, H, dty, dev = _matrix(fn, dx, "dx")
+    k, inv = _routes(fn, dev, inv_perm, T)
+    R, _, ty, _ = _matrix(fn, dx_perm, "dx_perm")
+    pp, ldp = _rows(fn, dev, dx_perm, "dx_perm", R, H, dx_perm.dtype)
+    px, ldx = _rows(fn, dev, x, "x", T, H, dx_perm.dtype)
+    pd, ldd = _rows(fn, dev, dx, "dx", T, H, dx.dtype)
+    pa, lda = _rows(fn, dev, add, "add", T, H, dx.dtype)
+    _issue(fn, dev, stream, (pp, ldp, ty, inv, _flat(fn, dev, w, "w", (T, k)), px, ldx, T, k, H, R, pd, ldd, dty, pa, lda,
+                             _flat(fn, dev, dw, "dw", (T, k)),
+                             _flat(fn, dev, dev_status, "dev_status", (1,), torch.int32)))
 
 
 def moe_collect(y_perm, inv_perm, w, out, add=None, dev_status=None, stream=None):
     """out = add + sum_j w * y_perm[inv_perm] in rank order (w None: 1)."""
-    c = _Call("moe_collect", out)
-    T, H, oty = c.matrix(out, "out")
-    k, inv = _routes(c, inv_perm, T)
-    R, _, ty = c.matrix(y_perm, "y_perm")
-    pp, ldp = c.rows(y_perm, "y_perm", R, H)
-    po, ldo = c.rows(out, "out", T, H)
-    pa, lda = c.rows(add, "add", T, H, out.dtype)
-    c.issue(stream, pp, ldp, ty, inv, c.flat(w, "w", (T, k)), T, k, H, R, po, ldo, oty, pa, lda,
-            c.flat(dev_status, "dev_status", (1,), torch.int32))
+    fn = "moe_collect"
+    T, H, oty, dev = _matrix(fn, out, "out")
+    k, inv = _routes(fn, dev, inv_perm, T)
+    R, _, ty, _ = _matrix(fn, y_perm, "y_perm")
+    pp, ldp = _rows(fn, dev, y_perm, "y_perm", R, H, y_perm.dtype)
+    po, ldo = _rows(fn, dev, out, "out", T, H, out.dtype)
+    pa, lda = _rows(fn, dev, add, "add", T, H, out.dtype)
+    _issue(fn, dev, stream, (pp, ldp, ty, inv, _flat(fn, dev, w, "w", (T, k)), T, k, H, R, po, ldo, oty, pa, lda,
+                             _flat(fn, dev, dev_status, "dev_status", (1,), torch.int32)))
 
 
 def moe_collect_backward(dout, y_perm, inv_perm, w, dy_perm, dw=None, dev_status=None, stream=None):
     """dy_perm[inv_perm[t,j]] = w[t,j] * dout[t]; with dw (and y_perm), dw[t,j] = <dout[t], y_perm[inv_perm[t,j]]>."""
-    c = _Call("moe_collect_backward", dout)
-    T, H, oty = c.matrix(dout, "dout")
-    k, inv = _routes(c, inv_perm, T)
-    R, _, ty = c.matrix(dy_perm, "dy_perm")
-    po, ldo = c.rows(dout, "dout", T, H)
-    py, ldy = c.rows(y_perm, "y_perm", R, H, dy_perm.dtype)
-    pd, ldd = c.rows(dy_perm, "dy_perm", R, H)
-    c.issue(stream, po, ldo, oty, py, ldy, ty, inv, c.flat(w, "w", (T, k)), T, k, H, R, pd, ldd,
-            c.flat(dw, "dw", (T, k)), c.flat(dev_status, "dev_status", (1,), torch.int32))
+    fn = "moe_collect_backward"
+    T, H, oty, dev = _matrix(fn, dout, "dout")
+    k, inv = _routes(fn, dev, inv_perm, T)
+    R, _, ty, _ = _matrix(fn, dy_perm, "dy_perm")
+    po, ldo = _rows(fn, dev, dout, "dout", T, H, dout.dtype)
+    py, ldy = _rows(fn, dev, y_perm, "y_perm", R, H, dy_perm.dtype)
+    pd, ldd = _rows(fn, dev, dy_perm, "dy_perm", R, H, dy_perm.dtype)
+    _issue(fn, dev, stream, (po, ldo, oty, py, ldy, ty, inv, _flat(fn, dev, w, "w", (T, k)), T, k, H, R, pd, ldd,
+                             _flat(fn, dev, dw, "dw", (T, k)),
+                             _flat(fn, dev, dev_status, "dev_status", (1,), torch.int32)))
 
 
-def _gate(c, gate, name, T, H, dtype, kind=None):
+def _gate(fn, dev, gate, name, T, H, dtype, kind=None):
     """(kind, pointer, row stride): [H] per channel, [T, 1] per token, [T, H] elementwise (of y's type)."""
     if gate is None:
         return MOE_GATE_NONE, None, 0
-    if not isinstance(gate, torch.Tensor):
-        c.no(MOE_EINVAL, f"{name} is not a tensor on GPU {c.dev}")
     if kind is None:
         if gate.dim() == 1:
             kind = MOE_GATE_CHANNEL
+        elif gate.dim() == 2 and gate.shape[1] == 1 and gate.dtype is torch.float32:
+            kind = MOE_GATE_TOKEN
         else:
-            kind = MOE_GATE_TOKEN if gate.dim() == 2 and gate.shape[1] == 1 and gate.dtype == torch.float32 \
-                else MOE_GATE_FULL
+            kind = MOE_GATE_FULL
     if kind == MOE_GATE_CHANNEL:
-        return kind, c.flat(gate, name, (H,)), 0
+        return kind, _flat(fn, dev, gate, name, (H,)), 0
     if kind == MOE_GATE_TOKEN:
-        return kind, c.flat(gate, name, (T, 1)), 0
-    return (kind,) + c.rows(gate, name, T, H, dtype)
+        return kind, _flat(fn, dev, gate, name, (T, 1)), 0
+    return (kind,) + _rows(fn, dev, gate, name, T, H, dtype)
 
 
 def moe_block_norm(x, y, x_out, n_out, gamma_post=None, gamma_pre=None, gate=None, scale=1.0, eps=1e-6,
@@ -231,21 +229,21 @@ def moe_block_norm(x, y, x_out, n_out, gamma_post=None, gamma_pre=None, gate=Non
     wanted.  gate: [H], [T, 1] (both fp32) or [T, H] of y's type.  The norms'
     gain is 1 + gamma; post_norm=False leaves y as it is.
     """
-    c = _Call("moe_block_norm", x)
-    T, H, xty = c.matrix(x, "x")
+    fn = "moe_block_norm"
+    T, H, xty, dev = _matrix(fn, x, "x")
     act = y if y is not None else n_out
     if act is None:
-        c.no(MOE_EINVAL, "y and n_out are both None")
-    yty = c.matrix(act, "y" if y is not None else "n_out")[2]
-    post_norm = bool(post_norm) and y is not None
-    px, ldx = c.rows(x, "x", T, H)
-    py, ldy = c.rows(y, "y", T, H)
-    kind, pg, ldg = _gate(c, gate, "gate", T, H, act.dtype)
-    po, ldo = c.rows(x_out, "x_out", T, H, x.dtype)
-    pn, ldn = c.rows(n_out, "n_out", T, H, act.dtype)
-    c.issue(stream, px, ldx, xty, py, ldy, yty, pg, kind, ldg, c.flat(gamma_post, "gamma_post", (H,)),
-            c.flat(gamma_pre, "gamma_pre", (H,)), post_norm, scale, eps, T, H, po, ldo, pn, ldn,
-            c.flat(rstd_post, "rstd_post", (T,)), c.flat(rstd_pre, "rstd_pre", (T,)))
+        _no(fn, MOE_EINVAL, "y and n_out are both None")
+    yty, yt = _matrix(fn, act, "y" if y is not None else "n_out")[2], act.dtype
+    px, ldx = _rows(fn, dev, x, "x", T, H, x.dtype)
+    py, ldy = _rows(fn, dev, y, "y", T, H, yt)
+    kind, pg, ldg = _gate(fn, dev, gate, "gate", T, H, yt)
+    po, ldo = _rows(fn, dev, x_out, "x_out", T, H, x.dtype)
+    pn, ldn = _rows(fn, dev, n_out, "n_out", T, H, yt)
+    _issue(fn, dev, stream, (px, ldx, xty, py, ldy, yty, pg, kind, ldg, _flat(fn, dev, gamma_post, "gamma_post", (H,)),
+                             _flat(fn, dev, gamma_pre, "gamma_pre", (H,)), post_norm and y is not None, scale, eps, T,
+                             H, po, ldo, pn, ldn, _flat(fn, dev, rstd_post, "rstd_post", (T,)),
+                             _flat(fn, dev, rstd_pre, "rstd_pre", (T,))))
 
 
 def moe_block_norm_workspace_size(T, H):
@@ -260,28 +258,29 @@ def moe_block_norm_backward(dx_out, dn, x_out, y, dx, dy, workspace, gamma_post=
     x_out, rstd_post and rstd_pre are what the forward call wrote.  dgate has
     gate's shape and type; dgate, dgamma_post and dgamma_pre may be None.
     """
-    c = _Call("moe_block_norm_backward", dx)
-    T, H, xty = c.matrix(dx, "dx")
+    fn = "moe_block_norm_backward"
+    T, H, xty, dev = _matrix(fn, dx, "dx")
     act = y if y is not None else dn
     if act is None:
-        c.no(MOE_EINVAL, "y and dn are both None")
-    yty = c.matrix(act, "y" if y is not None else "dn")[2]
-    post_norm = bool(post_norm) and y is not None
-    pdo, lddo = c.rows(dx_out, "dx_out", T, H, dx.dtype)
-    pdn, lddn = c.rows(dn, "dn", T, H, act.dtype)
-    px, ldx = c.rows(x_out, "x_out", T, H, dx.dtype)
-    py, ldy = c.rows(y, "y", T, H)
-    kind, pg, ldg = _gate(c, gate, "gate", T, H, act.dtype)
-    pdx, lddx = c.rows(dx, "dx", T, H)
-    pdy, lddy = c.rows(dy, "dy", T, H, act.dtype)
+        _no(fn, MOE_EINVAL, "y and dn are both None")
+    xt, yty, yt = dx.dtype, _matrix(fn, act, "y" if y is not None else "dn")[2], act.dtype
+    pdo, lddo = _rows(fn, dev, dx_out, "dx_out", T, H, xt)
+    pdn, lddn = _rows(fn, dev, dn, "dn", T, H, yt)
+    px, ldx = _rows(fn, dev, x_out, "x_out", T, H, xt)
+    py, ldy = _rows(fn, dev, y, "y", T, H, yt)
+    kind, pg, ldg = _gate(fn, dev, gate, "gate", T, H, yt)
+    pdx, lddx = _rows(fn, dev, dx, "dx", T, H, xt)
+    pdy, lddy = _rows(fn, dev, dy, "dy", T, H, yt)
     if dgate is not None and gate is None:
-        c.no(MOE_EINVAL, "dgate without gate")
-    _, pdg, lddg = _gate(c, dgate, "dgate", T, H, act.dtype, kind)
-    ws, nbytes = c.bytes(workspace, "workspace")
-    c.issue(stream, pdo, lddo, pdn, lddn, px, ldx, xty, py, ldy, yty, pg, kind, ldg,
-            c.flat(gamma_post, "gamma_post", (H,)), c.flat(gamma_pre, "gamma_pre", (H,)), post_norm, scale,
-            c.flat(rstd_post, "rstd_post", (T,)), c.flat(rstd_pre, "rstd_pre", (T,)), T, H, pdx, lddx, pdy, lddy,
-            pdg, lddg, c.flat(dgamma_post, "dgamma_post", (H,)), c.flat(dgamma_pre, "dgamma_pre", (H,)), ws, nbytes)
+        _no(fn, MOE_EINVAL, "dgate without gate")
+    _, pdg, lddg = _gate(fn, dev, dgate, "dgate", T, H, yt, kind)
+    ws, nbytes = _bytes(fn, dev, workspace, "workspace")
+    _issue(fn, dev, stream,
+           (pdo, lddo, pdn, lddn, px, ldx, xty, py, ldy, yty, pg, kind, ldg,
+            _flat(fn, dev, gamma_post, "gamma_post", (H,)), _flat(fn, dev, gamma_pre, "gamma_pre", (H,)),
+            post_norm and y is not None, scale, _flat(fn, dev, rstd_post, "rstd_post", (T,)),
+            _flat(fn, dev, rstd_pre, "rstd_pre", (T,)), T, H, pdx, lddx, pdy, lddy, pdg, lddg,
+            _flat(fn, dev, dgamma_post, "dgamma_post", (H,)), _flat(fn, dev, dgamma_pre, "dgamma_pre", (H,)), ws, nbytes))
 
 
 def moe_route_backward_workspace_size(T, k, E, H):
@@ -293,20 +292,24 @@ def moe_route_backward(dw, topk_w, topk_ids, x, w_router, offsets, perm, dlogits
     """Gradient of moe_route: from the gradient of the top-k weights to the
     selected logits (dlogits), the tokens (dx, plus add), the router matrix
     and its bias.  dx, dw_router and dbias may be None."""
-    c = _Call("moe_route_backward", x)
-    T, H, _ = c.matrix(x, "x")
-    E = c.matrix(w_router, "w_router")[0]
-    k, ids = _routes(c, topk_ids, T, "topk_ids")
-    px, ldx = c.rows(x, "x", T, H, torch.bfloat16)
-    pr, ldr = c.rows(w_router, "w_router", E, H, torch.bfloat16)
-    dty = MOE_ROW_F32 if dx is None else c.matrix(dx, "dx")[2]
-    pd, ldd = c.rows(dx, "dx", T, H)
-    if add is not None and dx is None:
-        c.no(MOE_EINVAL, "add without dx")
-    pa, lda = c.rows(add, "add", T, H, None if dx is None else dx.dtype)
-    pw, ldw = c.rows(dw_router, "dw_router", E, H, torch.float32)
-    ws, nbytes = c.bytes(workspace, "workspace")
-    c.issue(stream, c.flat(dw, "dw", (T, k)), c.flat(topk_w, "topk_w", (T, k)), ids, px, ldx, pr, ldr,
-            c.flat(offsets, "offsets", (E + 1,), torch.int32), c.flat(perm, "perm", (T * k,), torch.int32), T, k, E, H,
-            c.flat(dlogits, "dlogits", (T, k)), pd, ldd, dty, pa, lda, pw, ldw, c.flat(dbias, "dbias", (E,)), ws, nbytes,
-            c.flat(dev_status, "dev_status", (1,), torch.int32))
+    fn = "moe_route_backward"
+    i32 = torch.int32
+    T, H, _, dev = _matrix(fn, x, "x")
+    E = _matrix(fn, w_router, "w_router")[0]
+    k, ids = _routes(fn, dev, topk_ids, T, "topk_ids")
+    px, ldx = _rows(fn, dev, x, "x", T, H, torch.bfloat16)
+    pr, ldr = _rows(fn, dev, w_router, "w_router", E, H, torch.bfloat16)
+    dty, pd, ldd, pa, lda = MOE_ROW_F32, None, 0, None, 0
+    if dx is not None:
+        dty = _matrix(fn, dx, "dx")[2]
+        pd, ldd = _rows(fn, dev, dx, "dx", T, H, dx.dtype)
+        pa, lda = _rows(fn, dev, add, "add", T, H, dx.dtype)
+    elif add is not None:
+        _no(fn, MOE_EINVAL, "add without dx")
+    pw, ldw = _rows(fn, dev, dw_router, "dw_router", E, H, torch.float32)
+    ws, nbytes = _bytes(fn, dev, workspace, "workspace")
+    _issue(fn, dev, stream,
+           (_flat(fn, dev, dw, "dw", (T, k)), _flat(fn, dev, topk_w, "topk_w", (T, k)), ids, px, ldx, pr, ldr,
+            _flat(fn, dev, offsets, "offsets", (E + 1,), i32), _flat(fn, dev, perm, "perm", (T * k,), i32), T, k, E, H,
+            _flat(fn, dev, dlogits, "dlogits", (T, k)), pd, ldd, dty, pa, lda, pw, ldw,
+            _flat(fn, dev, dbias, "dbias", (E,)), ws, nbytes, _flat(fn, dev, dev_status, "dev_status", (1,), i32)))

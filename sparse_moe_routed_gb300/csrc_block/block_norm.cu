@@ -20,10 +20,7 @@ namespace blk {
 
 namespace {
 
-#ifndef FT
-#define FT 1024
-#endif
-constexpr int kThreads = FT;
+constexpr int kThreads = 1024;
 
 template <typename TX, typename TY, int G, int NCH>
 __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)

@@ -25,10 +25,7 @@ namespace blk {
 
 namespace {
 
-#ifndef GT
-#define GT 640
-#endif
-constexpr int kThreads = GT;
+constexpr int kThreads = 640;  // 96 registers a thread: no spills, which would miss the small L1 that the stages leave
 
 template <typename TX, typename TY, int G, int NCH>
 __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)

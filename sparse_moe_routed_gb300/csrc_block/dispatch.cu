@@ -26,7 +26,12 @@ namespace blk {
 
 namespace {
 
-constexpr int kBatch = 8;      // routes whose loads a thread has in flight
+// Routes whose loads a thread has in flight: a lone warp per token wants eight
+// (collect's gradient at 16,384 tokens: 269 us against 273 with four), CTAs of
+// several warps are better off with four and twice the CTAs per SM (dispatch's
+// gradient at 2,048 tokens: 24.7 against 33.2 us, 1,024: 14.9 against 20.0).
+template <bool SOLO>
+constexpr int kBatch = SOLO ? 8 : 4;
 constexpr int kMaxWarps = 16;  // warps per CTA
 
 // Sums of eight values over the warp, each lane giving its eight: lane l
@@ -74,13 +79,13 @@ __device__ __forceinline__ void token_sync() {
 
 // dw of a token's n routes: the warps' sums, added in warp order.
 template <bool SOLO, int NB>
-__device__ __forceinline__ void write_dw(const float (&part)[NB][kBatch], float (*red)[kMaxK], const Routes& sh,
+__device__ __forceinline__ void write_dw(const float (&part)[NB][8], float (*red)[kMaxK], const Routes& sh,
                                          float* dw, int n, int warp, int warps, int tid) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const float s = warp_sum8(part[b], lane);
-    if ((lane & 3) == 0) red[warp][b * kBatch + (lane >> 2)] = s;
+    if ((lane & 3) == 0) red[warp][b * 8 + (lane >> 2)] = s;
   }
   token_sync<SOLO>();
   if (tid < n) {
@@ -93,10 +98,10 @@ __device__ __forceinline__ void write_dw(const float (&part)[NB][kBatch], float 
 
 constexpr int kSoloWarps = 4;  // tokens per CTA where a warp owns a token
 
-// NB: batches of eight routes.  SOLO: grid (tokens / kSoloWarps); else grid
+// NK: routes per CTA at most.  SOLO: grid (tokens / kSoloWarps); else grid
 // (token, group of jb routes).
-template <typename TT, typename TR, bool VEC, bool DOT, int NB, bool SOLO>
-__global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
+template <typename TT, typename TR, bool VEC, bool DOT, int NK, bool SOLO>
+__global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO ? 7 : 2)
     spread_kernel(const TT* tok, int64_t ld_tok, const TR* dot, int64_t ld_dot, const int32_t* __restrict__ slot_of,
                   const float* __restrict__ w, int T, int k, int jb, int H, int R, TR* out, int64_t ld_out, float* dw,
                   int32_t* status) {
@@ -116,11 +121,11 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
   read_routes(sh, slot_of, w, r0, n, tid, R, 1, status);
   token_sync<SOLO>();
   const TT* row = tok + t * ld_tok;
-  float part[DOT ? NB : 1][kBatch];
+  float part[DOT ? NK / 8 : 1][8];  // this lane's share of each route's product
 #pragma unroll
-  for (int b = 0; b < (DOT ? NB : 1); ++b)
+  for (int b = 0; b < (DOT ? NK / 8 : 1); ++b)
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) part[b][u] = 0.f;
+    for (int u = 0; u < 8; ++u) part[b][u] = 0.f;
   for (int base = (SOLO ? 0 : warp) * 256; base < H; base += warps * 256) {
     const Cols<VEC> c(base, lane, 32);
     Raw8<TT> xr;
@@ -128,13 +133,13 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
     float x[8];
     unpack(xr, x);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      if (b * kBatch >= n) break;
-      Raw8<TR> v[DOT ? kBatch : 1];
+    for (int b = 0; b < NK / kBatch<SOLO>; ++b) {
+      if (b * kBatch<SOLO> >= n) break;
+      Raw8<TR> v[DOT ? kBatch<SOLO> : 1];
       if (DOT) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int j = b * kBatch + u;
+        for (int u = 0; u < kBatch<SOLO>; ++u) {
+          const int j = b * kBatch<SOLO> + u;
           const int64_t s = j < n ? sh.at[j] : -1;
           if (s >= 0)
             load8<VEC>(dot + s * ld_dot, c, H, v[DOT ? u : 0]);
@@ -143,15 +148,16 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
         }
       }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int j = b * kBatch + u;
+      for (int u = 0; u < kBatch<SOLO>; ++u) {
+        const int j = b * kBatch<SOLO> + u;
         const int64_t s = j < n ? sh.at[j] : -1;
         if (s < 0) continue;
         if (DOT) {
           float y[8];
           unpack(v[DOT ? u : 0], y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) part[DOT ? b : 0][u] = fmaf(x[i], y[i], part[DOT ? b : 0][u]);
+          for (int i = 0; i < 8; ++i) part[DOT ? (b * kBatch<SOLO> + u) / 8 : 0][(b * kBatch<SOLO> + u) % 8] =
+              fmaf(x[i], y[i], part[DOT ? (b * kBatch<SOLO> + u) / 8 : 0][(b * kBatch<SOLO> + u) % 8]);
         }
         float o[8];
 #pragma unroll
@@ -160,13 +166,13 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
       }
     }
   }
-  if (DOT) write_dw<SOLO, DOT ? NB : 1>(part, red, sh, dw + r0, n, warp, warps, tid);
+  if (DOT) write_dw<SOLO, DOT ? NK / 8 : 1>(part, red, sh, dw + r0, n, warp, warps, tid);
 }
 
 // SOLO: grid (tokens / kSoloWarps); else grid (token, part of the columns),
 // one part with DOT.
-template <typename TR, typename TO, bool VEC, bool DOT, int NB, bool SOLO>
-__global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
+template <typename TR, typename TO, bool VEC, bool DOT, int NK, bool SOLO>
+__global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO ? 7 : 2)
     join_kernel(const TR* rows, int64_t ld_rows, const TR* dot, int64_t ld_dot, const int32_t* __restrict__ slot_of,
                 const float* __restrict__ w, int T, int k, int H, int R, TO* out, int64_t ld_out, const TO* add,
                 int64_t ld_add, float* dw, int32_t* status) {
@@ -182,11 +188,11 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
   const size_t r0 = static_cast<size_t>(t) * k;
   read_routes(sh, slot_of, w, r0, k, tid, R, ld_rows, SOLO || blockIdx.y == 0 ? status : nullptr);
   token_sync<SOLO>();
-  float part[DOT ? NB : 1][kBatch];
+  float part[DOT ? NK / 8 : 1][8];  // this lane's share of each route's product
 #pragma unroll
-  for (int b = 0; b < (DOT ? NB : 1); ++b)
+  for (int b = 0; b < (DOT ? NK / 8 : 1); ++b)
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) part[b][u] = 0.f;
+    for (int u = 0; u < 8; ++u) part[b][u] = 0.f;
   const int first = SOLO ? 0 : blockIdx.y * warps + warp, stride = SOLO ? 1 : gridDim.y * warps;
   for (int base = first * 256; base < H; base += stride * 256) {
     const Cols<VEC> c(base, lane, 32);
@@ -199,12 +205,12 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      if (b * kBatch >= k) break;
-      Raw8<TR> v[kBatch];
+    for (int b = 0; b < NK / kBatch<SOLO>; ++b) {
+      if (b * kBatch<SOLO> >= k) break;
+      Raw8<TR> v[kBatch<SOLO>];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int j = b * kBatch + u;
+      for (int u = 0; u < kBatch<SOLO>; ++u) {
+        const int j = b * kBatch<SOLO> + u;
         const int64_t s = j < k ? sh.at[j] : -1;
         if (s >= 0)
           load8<VEC>(rows + s, c, H, v[u]);
@@ -212,8 +218,8 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
           raw_zero(v[u]);
       }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int j = b * kBatch + u;
+      for (int u = 0; u < kBatch<SOLO>; ++u) {
+        const int j = b * kBatch<SOLO> + u;
         if (j >= k || sh.at[j] < 0) continue;
         float y[8];
         unpack(v[u], y);
@@ -221,7 +227,8 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           acc[i] = fmaf(wj, y[i], acc[i]);
-          if (DOT) part[DOT ? b : 0][u] = fmaf(x[i], y[i], part[DOT ? b : 0][u]);
+          if (DOT) part[DOT ? (b * kBatch<SOLO> + u) / 8 : 0][(b * kBatch<SOLO> + u) % 8] =
+              fmaf(x[i], y[i], part[DOT ? (b * kBatch<SOLO> + u) / 8 : 0][(b * kBatch<SOLO> + u) % 8]);
         }
       }
     }
@@ -235,16 +242,20 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32)
     }
     store8<VEC>(out + t * ld_out, c, H, acc);
   }
-  if (DOT) write_dw<SOLO, DOT ? NB : 1>(part, red, sh, dw + r0, k, warp, warps, tid);
+  if (DOT) write_dw<SOLO, DOT ? NK / 8 : 1>(part, red, sh, dw + r0, k, warp, warps, tid);
 }
 
-// Warps in flight that keep the memory busy, over the whole GPU.
+// Warps that keep the memory busy, over the whole GPU.  28 fit on an SM with
+// one per token (launch bounds: 4,096 tokens are then one wave; with five CTAs
+// instead of seven dispatch's gradient took 73 us there, not 52).  Spread
+// without dw waits for one load and then only stores: it wants more (4,096
+// tokens: 47 us with 24 warps per SM, 36 with 120).
 inline int warps_wanted() { return 24 * sm_count(); }
 
 template <typename TT, typename TR, bool VEC, bool DOT>
 cudaError_t spread(const Rows& tok, const Rows& dot, const int32_t* slot_of, const float* w, int T, int k, int H,
                    int R, const Rows& out, float* dw, int32_t* status, cudaStream_t st) {
-  const int pieces = (H + 255) / 256, want = warps_wanted();
+  const int pieces = (H + 255) / 256, want = DOT ? warps_wanted() : 5 * warps_wanted();
   // few tokens: more warps per token, then a token's routes over several CTAs
   const int warps = std::min({kMaxWarps, pieces, (want + T - 1) / T});
   const int split = static_cast<int>(std::min<int64_t>(k, std::max<int64_t>(1, want / (static_cast<int64_t>(T) * pieces))));
@@ -256,12 +267,12 @@ cudaError_t spread(const Rows& tok, const Rows& dot, const int32_t* slot_of, con
   };
   if (warps == 1 && split == 1) {
     const dim3 grid((T + kSoloWarps - 1) / kSoloWarps);
-    return k <= 16 ? go(spread_kernel<TT, TR, VEC, DOT, 2, true>, grid, kSoloWarps * 32)
-                   : go(spread_kernel<TT, TR, VEC, DOT, 4, true>, grid, kSoloWarps * 32);
+    return k <= 16 ? go(spread_kernel<TT, TR, VEC, DOT, 16, true>, grid, kSoloWarps * 32)
+                   : go(spread_kernel<TT, TR, VEC, DOT, 32, true>, grid, kSoloWarps * 32);
   }
   const dim3 grid(T, (k + jb - 1) / jb);
-  return jb <= 16 ? go(spread_kernel<TT, TR, VEC, DOT, 2, false>, grid, warps * 32)
-                  : go(spread_kernel<TT, TR, VEC, DOT, 4, false>, grid, warps * 32);
+  return jb <= 16 ? go(spread_kernel<TT, TR, VEC, DOT, 16, false>, grid, warps * 32)
+                  : go(spread_kernel<TT, TR, VEC, DOT, 32, false>, grid, warps * 32);
 }
 
 template <typename TR, typename TO, bool VEC, bool DOT>
@@ -282,12 +293,12 @@ cudaError_t join(const Rows& rows, const Rows& dot, const int32_t* slot_of, cons
   };
   if (warps == 1 && parts == 1) {
     const dim3 grid((T + kSoloWarps - 1) / kSoloWarps);
-    return k <= 16 ? go(join_kernel<TR, TO, VEC, DOT, 2, true>, grid, kSoloWarps * 32)
-                   : go(join_kernel<TR, TO, VEC, DOT, 4, true>, grid, kSoloWarps * 32);
+    return k <= 16 ? go(join_kernel<TR, TO, VEC, DOT, 16, true>, grid, kSoloWarps * 32)
+                   : go(join_kernel<TR, TO, VEC, DOT, 32, true>, grid, kSoloWarps * 32);
   }
   const dim3 grid(T, parts);
-  return k <= 16 ? go(join_kernel<TR, TO, VEC, DOT, 2, false>, grid, warps * 32)
-                 : go(join_kernel<TR, TO, VEC, DOT, 4, false>, grid, warps * 32);
+  return k <= 16 ? go(join_kernel<TR, TO, VEC, DOT, 16, false>, grid, warps * 32)
+                 : go(join_kernel<TR, TO, VEC, DOT, 32, false>, grid, warps * 32);
 }
 
 // f(type tag of a, type tag of b)

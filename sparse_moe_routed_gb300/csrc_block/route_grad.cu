@@ -2,120 +2,145 @@
 //
 // The weights are the softmax over a token's k selected logits, so
 //   dl_j = w_j (dw_j - sum_i w_i dw_i),
-// the gradient of x is the dl-weighted sum of k router rows (the join of
-// dispatch.cu, with the router as its rows and the expert IDs as its slots)
-// and that of the router sums dl x over the routes of each expert, which the
-// grouping has put side by side.
+// the gradient of x is the dl-weighted sum of k router rows, and that of the
+// router sums dl x over the routes of each expert, which the grouping has put
+// side by side.
 //
-// A sparse sum, not a matrix product over all experts: k of E logits carry a
+// Sparse sums, not a matrix product over all experts: k of E logits carry a
 // gradient, so the dense form computes E / k times the work (and would have
-// to hold dl in bf16 to use the tensor cores).  Bound by L2: x and the router
-// stay there, and each of their rows is read once per route.
+// to split dl into several bf16 terms to use the tensor cores).  x and the
+// router stay in L2; what bounds both sums is reading each of their rows once
+// per route through the SMs.
 //
-// An expert's routes are cut into units of at most kUnit, so that a popular
-// expert is shared by many CTAs; an expert of one unit is written directly,
-// the units of others leave partial rows that a last launch adds in order.
+// dx: with many tokens a CTA keeps a slab of the router's columns in shared
+// memory and reads every route's row from there; with few, or rows that are
+// not aligned, it is the join of dispatch.cu with the router as its rows and
+// the expert IDs as its slots.
+// dw_router: one warp per unit of at most kUnit routes and 256 columns.  An
+// expert of one unit is written directly; the units of a popular expert leave
+// partial rows that a last launch adds in order.
 #include <algorithm>
 
-#include "launch.h"
-#include "rows.cuh"
+#include "norm.h"
+#include "stage.cuh"
 
 namespace moe {
 namespace blk {
 
 namespace {
 
-constexpr int kUnit = 256;         // routes per unit
+constexpr int kUnit = 128;          // routes per unit
 constexpr int kPlanThreads = 1024;  // >= kMaxE
-constexpr int kBatch = 8;          // rows whose loads a thread has in flight
-constexpr int kRowThreads = 256;   // threads per CTA of the row sums
+constexpr int kBatch = 8;           // rows whose loads a thread has in flight
+constexpr int kRowWarps = 4;        // warps per CTA of the row sums
 
-// A unit: n routes of expert e from slot s0 on; part is where its partial row
-// goes, or -1 where it is the expert's only unit and writes the result.
+// A unit: n routes of expert e (-1: no unit) from slot s0 on; part is where
+// its partial row goes, or -1 where it is the expert's only unit and writes
+// the result.
 struct Unit {
   int32_t e, s0, n, part;
 };
 
-// Workspace, each part 256-byte aligned: the units, each expert's first
-// partial row and how many it has ({first, count}, count 0: written
-// directly), partial rows [..][H] f32, their bias sums f32.
-__host__ __device__ inline int max_units(int R, int E) { return E + R / kUnit; }
-__host__ __device__ inline int max_partials(int R) { return 2 * (R / kUnit) + 1; }
-__host__ __device__ inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+// An expert of n > 1 units (0: none): partial rows part0 .. part0 + n - 1.
+struct Multi {
+  int32_t e, part0, n, pad;
+};
+
+inline int max_units(int R, int E) { return E + R / kUnit; }
+inline int max_multi(int R) { return R / kUnit; }
+inline int max_partials(int R) { return 2 * (R / kUnit) + 1; }
+
+// The workspace's parts, 256-byte aligned: the units, the experts of several
+// units, partial rows [..][H], their bias sums.
 struct Ws {
   Unit* units;
-  int2* parts;
+  Multi* multi;
   float *rows, *bias;
   size_t bytes;
 };
-__host__ __device__ inline Ws ws_layout(void* p, int R, int E, int H) {
+Ws ws_layout(void* p, int R, int E, int H) {
   char* c = static_cast<char*>(p);
   size_t at = 0;
+  auto take = [&](size_t n) {
+    char* q = c + at;
+    at += (n + 255) / 256 * 256;
+    return q;
+  };
   Ws w;
-  w.units = reinterpret_cast<Unit*>(c + at);
-  at += round256(sizeof(Unit) * max_units(R, E));
-  w.parts = reinterpret_cast<int2*>(c + at);
-  at += round256(sizeof(int2) * E);
-  w.rows = reinterpret_cast<float*>(c + at);
-  at += round256(sizeof(float) * static_cast<size_t>(max_partials(R)) * H);
-  w.bias = reinterpret_cast<float*>(c + at);
-  w.bytes = at + round256(sizeof(float) * max_partials(R));
+  w.units = reinterpret_cast<Unit*>(take(sizeof(Unit) * max_units(R, E)));
+  w.multi = reinterpret_cast<Multi*>(take(sizeof(Multi) * max_multi(R)));
+  w.rows = reinterpret_cast<float*>(take(sizeof(float) * static_cast<size_t>(max_partials(R)) * H));
+  w.bias = reinterpret_cast<float*>(take(sizeof(float) * max_partials(R)));
+  w.bytes = at;
   return w;
 }
 
-__device__ __forceinline__ int block_scan_excl(int v, int* warp_tot) {
+// Up to this many tokens an expert is one unit (n <= T where a token's experts
+// are distinct): no plan and no join.
+constexpr int kDirectTokens = kUnit;
+
+// Do a thread's offsets rise from 0 to R?
+__device__ __forceinline__ bool offsets_bad(const int32_t* offsets, int e, int E, int R, int& a, int& n) {
+  a = offsets[e];
+  const int b = offsets[e + 1];
+  n = b - a;
+  return a < 0 || b < a || b > R || (e == 0 && a != 0) || (e == E - 1 && b != R);
+}
+
+// Exclusive sum over the CTA's threads; returns the total in `total`.
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_tot, uint64_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
+  uint64_t incl = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, d);
+    const uint64_t y = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += y;
   }
   if (lane == 31) warp_tot[warp] = incl;
   __syncthreads();
-  int before = 0;
-  for (int i = 0; i < warp; ++i) before += warp_tot[i];
-  __syncthreads();
+  uint64_t before = lane < warp ? warp_tot[lane] : 0, all = warp_tot[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  total = all;
   return before + incl - v;
 }
 
-// CTA 0: the units of every expert.  The others: dl, one warp per token.
+// dl, one warp per token, and with `plan` CTA 0 the units of every expert.
 __global__ void __launch_bounds__(kPlanThreads)
     route_plan_kernel(const float* __restrict__ dw, const float* __restrict__ w, const int32_t* __restrict__ offsets,
-                      int T, int k, int E, int H, float* __restrict__ dl, void* ws, int plan, int32_t* status) {
-  __shared__ int warp_tot[32];
+                      int T, int k, int E, float* __restrict__ dl, Unit* units_out, Multi* multi_out, int units_max,
+                      int multi_max, int plan, int32_t* status) {
+  __shared__ uint64_t warp_tot[32];
   __shared__ int first[kPlanThreads], start[kPlanThreads], count[kPlanThreads], part0[kPlanThreads];
-  __shared__ int bad, total;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31;
-  if (blockIdx.x == 0) {
-    if (!plan) return;
-    const int R = T * k;
-    const Ws s = ws_layout(ws, R, E, H);
-    if (tid == 0) bad = 0;
-    __syncthreads();
+  if (plan && blockIdx.x == 0) {
     int n = 0, a = 0;
-    if (tid < E && R > 0) {  // no routes: the grouping wrote no offsets
-      a = offsets[tid];
-      const int b = offsets[tid + 1];
-      if (a < 0 || b < a || b > R || (tid == 0 && a != 0) || (tid == E - 1 && b != R)) bad = 1;
-      n = b - a;
-    }
-    __syncthreads();
-    // bad offsets: every unit is marked as none
+    const bool bad = __syncthreads_or(tid < E && offsets_bad(offsets, tid, E, T * k, a, n)) != 0;
+    // bad offsets: no unit at all.  One sum of three: units (26 bits), partial
+    // rows (27), experts of several units (11).
     const int units = tid < E && !bad ? max(1, (n + kUnit - 1) / kUnit) : 0;
-    const int p0 = block_scan_excl(units > 1 ? units : 0, warp_tot);
-    first[tid] = block_scan_excl(units, warp_tot);
+    const bool several = units > 1;
+    uint64_t total;
+    const uint64_t at = block_scan(static_cast<uint64_t>(units) |
+                                       (several ? static_cast<uint64_t>(units) << 26 | 1ull << 53 : 0ull),
+                                   warp_tot, total);
+    const int p0 = static_cast<int>(at >> 26 & 0x7ffffff), m0 = static_cast<int>(at >> 53);
+    first[tid] = static_cast<int>(at & 0x3ffffff);
     start[tid] = a;
     count[tid] = n;
-    part0[tid] = units > 1 ? p0 : -1;
-    if (tid < E) s.parts[tid] = make_int2(p0, units > 1 ? units : 0);
-    if (tid == kPlanThreads - 1) total = first[tid] + units;
+    part0[tid] = several ? p0 : -1;
+    if (several) multi_out[m0] = {tid, p0, units, 0};
+    for (int i = static_cast<int>(total >> 53) + tid; i < multi_max; i += kPlanThreads) multi_out[i] = {0, 0, 0, 0};
     __syncthreads();
-    for (int u = tid; u < max_units(R, E); u += kPlanThreads) {
+    const int units_all = static_cast<int>(total & 0x3ffffff);
+    for (int u = tid; u < units_max; u += kPlanThreads) {
       Unit d = {-1, 0, 0, -1};
-      if (u < total) {
+      if (u < units_all) {
         int lo = 0, hi = E;  // the expert whose first unit is the last at or before u
         while (hi - lo > 1) {
           const int mid = (lo + hi) / 2;
@@ -127,14 +152,14 @@ __global__ void __launch_bounds__(kPlanThreads)
         const int i = u - first[lo];
         d = {lo, start[lo] + i * kUnit, min(kUnit, count[lo] - i * kUnit), part0[lo] < 0 ? -1 : part0[lo] + i};
       }
-      s.units[u] = d;
+      units_out[u] = d;
     }
     if (tid == 0 && bad) set_status(status, MOE_DEV_BAD_EXPERT);
     return;
   }
   const int warps = kPlanThreads / 32;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x - 1) * warps + (tid >> 5); t < T;
-       t += static_cast<int64_t>(gridDim.x - 1) * warps) {
+  for (int64_t t = static_cast<int64_t>(blockIdx.x - plan) * warps + (tid >> 5); t < T;
+       t += static_cast<int64_t>(gridDim.x - plan) * warps) {
     const float wj = lane < k ? w[t * k + lane] : 0.f;
     const float gj = lane < k ? dw[t * k + lane] : 0.f;
     float m = lane < k ? wj * gj : 0.f;
@@ -144,148 +169,303 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// grid (unit, slab of 8 cw columns).  The CTA's threads are cw columns of
-// eight by kRowThreads / cw row groups; a row group sums every such route of
-// the unit, and the first adds the others in order.
-template <bool VEC>
-__global__ void __launch_bounds__(kRowThreads)
-    route_rows_kernel(const float* __restrict__ dl, const int32_t* __restrict__ perm, const bf16_t* __restrict__ x,
-                      int64_t ldx, int T, int k, int E, int H, int cw, float* dwr, int64_t ld_dw, float* dbias,
-                      void* ws, int32_t* status) {
-  __shared__ int2 route[kUnit];  // token (-1: none) and the bits of dl
-  __shared__ float red[kRowThreads * 8];
+// acc += w times eight bf16 columns
+__device__ __forceinline__ void add_row(float2 (&acc)[4], float w, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t two[4] = {a, b, c, d};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = __ffma2_rn(splat(w), widen(two[i]), acc[i]);
+}
+
+// One warp per unit and piece of 256 columns: it needs no other, so that the
+// chain of loads in front of its rows (unit, route, dl) overlaps the rows of
+// the SM's other warps.  grid (units / kRowWarps, pieces).  DIRECT: the units
+// are the experts.
+template <bool VEC, bool DIRECT>
+__global__ void __launch_bounds__(kRowWarps * 32)
+    route_rows_kernel(const float* __restrict__ dl, const int32_t* __restrict__ offsets,
+                      const int32_t* __restrict__ perm, const bf16_t* __restrict__ x, int64_t ldx, int R, int k, int E,
+                      int H, const Unit* units, int units_max, float* dwr, int64_t ld_dw, float* dbias, float* part_rows,
+                      float* part_bias, int32_t* status) {
+  __shared__ int2 routes[kRowWarps][32];  // token (-1: none) and the bits of dl
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x;
-  const int R = T * k;
-  const Ws s = ws_layout(ws, R, E, H);
-  const Unit un = s.units[blockIdx.x];
-  if (un.e < 0) return;
-  const int n = un.n;
-  for (int i = tid; i < n; i += kRowThreads) {
-    const int r = perm[un.s0 + i];
-    const bool ok = r >= 0 && r < R;
-    if (!ok) set_status(status, MOE_DEV_BAD_EXPERT);
-    route[i] = make_int2(ok ? r / k : -1, ok ? __float_as_int(dl[r]) : 0);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int unit = blockIdx.x * kRowWarps + warp;
+  Unit un = {-1, 0, 0, -1};
+  if (DIRECT) {
+    int a = 0, n = 0;
+    bool bad = false;
+    if (R > 0)  // no routes: the grouping wrote no offsets
+      for (int e = threadIdx.x; e < E; e += kRowWarps * 32) bad |= offsets_bad(offsets, e, E, R, a, n);
+    if (__syncthreads_or(bad)) {
+      if (threadIdx.x == 0) set_status(status, MOE_DEV_BAD_EXPERT);
+      return;
+    }
+    if (unit < E) {
+      const int s0 = R > 0 ? offsets[unit] : 0;
+      un = {unit, s0, R > 0 ? offsets[unit + 1] - s0 : 0, -1};
+    }
+  } else if (unit < units_max) {
+    un = units[unit];
   }
-  __syncthreads();
-  if (dbias != nullptr && blockIdx.y == 0 && tid < 32) {
-    float b = 0.f;
-    for (int i = tid; i < n; i += 32) b += __int_as_float(route[i].y);
+  if (un.e < 0) return;
+  auto fetch = [&](int i) {
+    if (i >= un.n) return make_int2(-1, 0);
+    const int r = perm[un.s0 + i];
+    if (r >= 0 && r < R) return make_int2(r / k, __float_as_int(dl[r]));
+    set_status(status, MOE_DEV_BAD_EXPERT);
+    return make_int2(-1, 0);
+  };
+  const Cols<VEC> c(blockIdx.y * 256, lane, 32);
+  const bool whole = VEC && c.first + 8 <= H;
+  float2 acc[4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
-    if (tid == 0) (un.part < 0 ? dbias[un.e] : s.bias[un.part]) = b;
+  for (int i = 0; i < 4; ++i) acc[i] = splat(0.f);
+  float bias = 0.f;
+  int2 next = fetch(lane);
+  for (int i0 = 0; i0 < un.n; i0 += 32) {
+    __syncwarp();
+    routes[warp][lane] = next;
+    bias += __int_as_float(next.y);
+    const unsigned valid = __ballot_sync(0xffffffffu, next.x >= 0);
+    __syncwarp();
+    next = fetch(i0 + 32 + lane);
+    if (dwr == nullptr) continue;
+#pragma unroll 1
+    for (int j0 = 0; j0 < 32 && valid >> j0 != 0; j0 += kBatch) {
+      Raw8<bf16_t> v[kBatch];
+      float w[kBatch];
+      if (whole && (valid >> j0 & 0xff) == 0xff) {  // the usual batch: nothing to test per row
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int2 rt = routes[warp][j0 + b];
+          w[b] = __int_as_float(rt.y);
+          load_vec(x + rt.x * ldx + c.first, v[b]);
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int2 rt = routes[warp][j0 + b];
+          w[b] = __int_as_float(rt.y);
+          if (rt.x >= 0)
+            load8<VEC>(x + rt.x * ldx, c, H, v[b]);
+          else
+            raw_zero(v[b]);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) add_row(acc, w[b], v[b].v[0], v[b].v[1], v[b].v[2], v[b].v[3]);
+    }
+  }
+  if (dbias != nullptr && blockIdx.y == 0) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) bias += __shfl_xor_sync(0xffffffffu, bias, o);
+    if (lane == 0) (un.part < 0 ? dbias[un.e] : part_bias[un.part]) = bias;
   }
   if (dwr == nullptr) return;
-  const int rg = kRowThreads / cw, g = tid / cw, col = tid - g * cw;
-  const Cols<VEC> c(blockIdx.y * cw * 8, col, cw);
-  float acc[8];
+  float o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  for (int i0 = g; i0 < n; i0 += kBatch * rg) {
-    Raw8<bf16_t> v[kBatch];
-    float w[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + b * rg;
-      const int2 rt = i < n ? route[i] : make_int2(-1, 0);
-      w[b] = __int_as_float(rt.y);
-      if (rt.x >= 0)
-        load8<VEC>(x + rt.x * ldx, c, H, v[b]);
-      else
-        raw_zero(v[b]);
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      float f[8];
-      unpack(v[b], f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[b], f[i], acc[i]);
-    }
-  }
-  if (rg > 1) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) red[i * kRowThreads + tid] = acc[i];
-    __syncthreads();
-    if (g > 0) return;
-    for (int o = 1; o < rg; ++o)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += red[i * kRowThreads + o * cw + col];
-  }
+  for (int i = 0; i < 4; ++i) o[2 * i] = acc[i].x, o[2 * i + 1] = acc[i].y;
   if (un.part < 0) {
-    store8<VEC>(dwr + un.e * ld_dw, c, H, acc);
+    store8<VEC>(dwr + un.e * ld_dw, c, H, o);
   } else {
-    float* out = s.rows + static_cast<size_t>(un.part) * H;  // packed: whole vectors only where H allows it
+    float* out = part_rows + static_cast<size_t>(un.part) * H;  // packed: whole vectors only where H allows it
     if (VEC && H % 8 == 0) {
-      store8<VEC>(out, c, H, acc);
+      store8<VEC>(out, c, H, o);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c.first + i * c.step < H) out[c.first + i * c.step] = acc[i];
+        if (c.first + i * c.step < H) out[c.first + i * c.step] = o[i];
     }
   }
 }
 
-// grid (expert, 256 columns): the experts of several units.
-__global__ void __launch_bounds__(256) route_join_kernel(int T, int k, int E, int H, float* dwr, int64_t ld_dw,
-                                                         float* dbias, void* ws) {
+// grid (expert of several units, 1,024 columns): the partial rows in order.
+__global__ void __launch_bounds__(256) route_join_kernel(const Multi* multi, const float* rows, const float* bias,
+                                                         int H, float* dwr, int64_t ld_dw, float* dbias) {
   pdl_wait();
   pdl_trigger();
-  const Ws s = ws_layout(ws, T * k, E, H);
-  const int e = blockIdx.x;
-  const int p0 = s.parts[e].x, n = s.parts[e].y;
-  if (n == 0) return;
-  const int col = blockIdx.y * 256 + threadIdx.x;
-  if (dwr != nullptr && col < H) {
-    float a = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < n; ++p) a += s.rows[static_cast<size_t>(p0 + p) * H + col];
-    dwr[e * ld_dw + col] = a;
+  const Multi m = multi[blockIdx.x];
+  if (m.n == 0) return;
+  if (dwr != nullptr) {
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    const int col = blockIdx.y * 1024 + threadIdx.x;
+    const float* src = rows + static_cast<size_t>(m.part0) * H + col;
+#pragma unroll 2
+    for (int p = 0; p < m.n; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i * 256 < H) a[i] += src[static_cast<size_t>(p) * H + i * 256];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i * 256 < H) dwr[m.e * ld_dw + col + i * 256] = a[i];
   }
   if (dbias != nullptr && blockIdx.y == 0 && threadIdx.x == 0) {
     float b = 0.f;
-    for (int p = 0; p < n; ++p) b += s.bias[p0 + p];
-    dbias[e] = b;
+    for (int p = 0; p < m.n; ++p) b += bias[m.part0 + p];
+    dbias[m.e] = b;
   }
+}
+
+// dx with a slab of the router's columns in shared memory: CTA (slab, part of
+// the tokens) copies its columns of all E rows once and then reads every
+// route's row from there; row E is zeros, for routes that are none.  Sixteen
+// lanes of eight columns work on a token, two tokens per warp.
+constexpr int kSlabColumns = 128;
+constexpr int kSlabThreads = 1024;
+constexpr int kSlabBatch = 2;  // rows whose reads a thread has in flight (1, 4: 28.7 and 29.0 us, 2: 26.9)
+// From this many elements of routed rows on (and where E + 1 rows of 128
+// columns fit): 26.9 us against the join's 32.5 at 4,096 tokens, top 10 of 512
+// experts, width 2,560, and 82 against 107 at 16,384; 17.3 against 18.5 at
+// 2,048, but 14.8 against 13.2 at 2,048 with top 4 of 64.
+constexpr int64_t kSlabElements = 50'000'000;
+
+template <typename TO>
+__global__ void __launch_bounds__(kSlabThreads)
+    route_dx_kernel(const bf16_t* __restrict__ wr, int64_t ld_wr, const int32_t* __restrict__ ids,
+                    const float* __restrict__ dl, int T, int k, int E, int H, TO* dx, int64_t ld_dx, const TO* add,
+                    int64_t ld_add, int32_t* status) {
+  extern __shared__ __align__(16) unsigned char slab[];  // [E + 1][C] bf16
+  constexpr int C = kSlabColumns, kLanes = C / 8, kTokens = 32 / kLanes;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int col = blockIdx.x * C;
+  for (int i = tid; i < (E + 1) * kLanes; i += kSlabThreads) {
+    const int e = i / kLanes, c = col + (i % kLanes) * 8;
+    const int n = e < E ? max(0, min(8, H - c)) : 0;  // columns of the vector that exist; the rest become zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(slab)) + i * 16),
+                 "l"(n > 0 ? wr + e * ld_wr + c : wr), "r"(n * 2)
+                 : "memory");
+  }
+  copies_commit();
+  copies_wait(0);
+  __syncthreads();
+  const int sub = lane / kLanes, l = lane % kLanes;
+  const Cols<true> c(col, l, kLanes);
+  const unsigned char* mine = slab + l * 16;
+  const int64_t step = static_cast<int64_t>(gridDim.y) * (kSlabThreads / 32) * kTokens;
+  // lane l of the token's lanes reads routes l, l + kLanes, ...
+  auto route = [&](int64_t t, int j, int& id, float& g) {
+    id = E;
+    g = 0.f;
+    if (t < T && j < k) {
+      id = ids[t * k + j];
+      g = dl[t * k + j];
+      if (id == E) id = -1;  // E is this kernel's own name for no route
+    }
+  };
+  auto check = [&](int& id, float& g) {
+    if (id >= 0 && id <= E) return;
+    if (blockIdx.x == 0) set_status(status, MOE_DEV_BAD_EXPERT);
+    id = E;
+    g = 0.f;
+  };
+  int64_t t = (static_cast<int64_t>(blockIdx.y) * (kSlabThreads / 32) + warp) * kTokens + sub;
+  // the next token's first routes and add are loaded while this one's rows are summed
+  int id_next;
+  float g_next;
+  Raw8<TO> a_next;
+  auto ahead = [&](int64_t at) {
+    route(at, l, id_next, g_next);
+    raw_zero(a_next);
+    if (at < T && add != nullptr) load8<true>(add + at * ld_add, c, H, a_next);
+  };
+  ahead(t);
+  for (; t - sub < T; t += step) {
+    int id = id_next;
+    float g = g_next;
+    const Raw8<TO> ar = a_next;
+    ahead(t + step);
+    float2 acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = splat(0.f);
+    for (int j0 = 0;;) {
+      check(id, g);
+      id *= C * 2;  // bytes to the row
+      const int n = min(kLanes, k - j0);
+#pragma unroll 1
+      for (int b = 0; b < n; b += kSlabBatch) {
+        uint4 q[kSlabBatch];
+        float w[kSlabBatch];
+#pragma unroll
+        for (int u = 0; u < kSlabBatch; ++u) {
+          // a place past k - j0 (and within the token's lanes) holds row E
+          q[u] = *reinterpret_cast<const uint4*>(mine + __shfl_sync(0xffffffffu, id, b + u, kLanes));
+          w[u] = __shfl_sync(0xffffffffu, g, b + u, kLanes);
+        }
+#pragma unroll
+        for (int u = 0; u < kSlabBatch; ++u) add_row(acc, w[u], q[u].x, q[u].y, q[u].z, q[u].w);
+      }
+      j0 += kLanes;
+      if (j0 >= k) break;
+      route(t, j0 + l, id, g);
+    }
+    if (t >= T) continue;
+    float a[8];
+    unpack(ar, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[2 * i] += acc[i].x, a[2 * i + 1] += acc[i].y;
+    store8<true>(dx + t * ld_dx, c, H, a);
+  }
+}
+
+template <typename TO>
+cudaError_t launch_route_dx(const RouteGradArgs& a, cudaStream_t st) {
+  constexpr int C = kSlabColumns;
+  auto kern = route_dx_kernel<TO>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kern, done);
+  if (e != cudaSuccess) return e;
+  const int slabs = (a.H + C - 1) / C, smem = (a.E + 1) * C * 2;
+  const int per_sm = std::max(1, std::min(2048 / kSlabThreads, kNormSmem / smem));
+  const int tokens = kSlabThreads / 32 * (256 / C);  // per CTA at a time
+  const int parts = std::max(1, std::min(per_sm * sm_count() / slabs, (a.T + tokens - 1) / tokens));
+  return launch_pdl(kern, dim3(slabs, parts), dim3(kSlabThreads), smem, st,
+                    static_cast<const bf16_t*>(a.w_router.p), a.w_router.ld, a.ids, a.dlogits, a.T, a.k, a.E, a.H,
+                    static_cast<TO*>(a.dx.p), a.dx.ld, static_cast<const TO*>(a.add.p), a.add.ld, a.status);
 }
 
 }  // namespace
 
-size_t route_grad_ws_bytes(int T, int k, int E, int H) {
-  return ws_layout(nullptr, T * k, E, H).bytes;
-}
+size_t route_grad_ws_bytes(int T, int k, int E, int H) { return ws_layout(nullptr, T * k, E, H).bytes; }
 
 cudaError_t launch_route_grad(const RouteGradArgs& a, cudaStream_t st) {
   const int R = a.T * a.k;
-  const int plan = a.dw_router.p != nullptr || a.dbias != nullptr;
-  const int warps = kPlanThreads / 32;
-  const int dl_ctas = std::min((a.T + warps - 1) / warps, 4 * sm_count());
+  const bool rows = a.dw_router.p != nullptr || a.dbias != nullptr, direct = a.T <= kDirectTokens;
+  const int plan = rows && !direct;
+  const Ws ws = ws_layout(a.ws, R, a.E, a.H);
+  const int units = direct ? a.E : max_units(R, a.E), multi = direct ? 0 : max_multi(R);
   cudaError_t e = cudaSuccess;
-  if (plan || dl_ctas > 0) {
-    e = launch_pdl(route_plan_kernel, dim3(1 + dl_ctas), dim3(kPlanThreads), 0, st, a.dw, a.w, a.offsets, a.T, a.k,
-                   a.E, a.H, a.dlogits, a.ws, plan, a.status);
+  if (a.T > 0) {
+    const int warps = kPlanThreads / 32, ctas = std::min((a.T + warps - 1) / warps, 4 * sm_count());
+    e = launch_pdl(route_plan_kernel, dim3(ctas + plan), dim3(kPlanThreads), 0, st, a.dw, a.w, a.offsets, a.T, a.k,
+                   a.E, a.dlogits, ws.units, ws.multi, units, multi, plan, a.status);
     if (e != cudaSuccess) return e;
   }
   if (a.dx.p != nullptr && a.T > 0) {
     const Rows none = {nullptr, 0, MOE_ROW_BF16};
-    e = launch_join(a.w_router, none, a.ids, a.dlogits, a.T, a.k, a.H, a.E, a.dx, a.add, nullptr, a.status, st);
+    if (static_cast<int64_t>(R) * a.H >= kSlabElements && (a.E + 1) * kSlabColumns * 2 <= kNormSmem &&
+        vec_ok(a.w_router) && vec_ok(a.dx) && vec_ok(a.add))
+      e = a.dx.type == MOE_ROW_F32 ? launch_route_dx<float>(a, st) : launch_route_dx<bf16_t>(a, st);
+    else
+      e = launch_join(a.w_router, none, a.ids, a.dlogits, a.T, a.k, a.H, a.E, a.dx, a.add, nullptr, a.status, st);
     if (e != cudaSuccess) return e;
   }
-  if (!plan) return cudaSuccess;
-  // 64 columns of eight by 4 row groups; narrower rows: fewer columns
-  const int chunks = (a.H + 7) / 8;
-  const int cw = chunks > 32 ? 64 : chunks > 16 ? 32 : 16;
-  const int slabs = a.dw_router.p != nullptr ? (chunks + cw - 1) / cw : 1;
+  if (!rows) return cudaSuccess;
+  const int pieces = a.dw_router.p != nullptr ? (a.H + 255) / 256 : 1;
   const bool vec = vec_ok(a.x) && vec_ok(a.dw_router);
   auto go = [&](auto kern) {
-    return launch_pdl(kern, dim3(max_units(R, a.E), slabs), dim3(kRowThreads), 0, st, a.dlogits, a.perm,
-                      static_cast<const bf16_t*>(a.x.p), a.x.ld, a.T, a.k, a.E, a.H, cw,
-                      static_cast<float*>(a.dw_router.p), a.dw_router.ld, a.dbias, a.ws, a.status);
+    return launch_pdl(kern, dim3((units + kRowWarps - 1) / kRowWarps, pieces), dim3(kRowWarps * 32), 0, st, a.dlogits,
+                      a.offsets, a.perm, static_cast<const bf16_t*>(a.x.p), a.x.ld, R, a.k, a.E, a.H, ws.units, units,
+                      static_cast<float*>(a.dw_router.p), a.dw_router.ld, a.dbias, ws.rows, ws.bias, a.status);
   };
-  e = vec ? go(route_rows_kernel<true>) : go(route_rows_kernel<false>);
-  if (e != cudaSuccess || R <= kUnit) return e;
-  return launch_pdl(route_join_kernel, dim3(a.E, (a.H + 255) / 256), dim3(256), 0, st, a.T, a.k, a.E, a.H,
-                    static_cast<float*>(a.dw_router.p), a.dw_router.ld, a.dbias, a.ws);
+  e = direct ? (vec ? go(route_rows_kernel<true, true>) : go(route_rows_kernel<false, true>))
+             : (vec ? go(route_rows_kernel<true, false>) : go(route_rows_kernel<false, false>));
+  if (e != cudaSuccess || multi == 0) return e;
+  return launch_pdl(route_join_kernel, dim3(multi, (a.H + 1023) / 1024), dim3(256), 0, st, ws.multi, ws.rows, ws.bias,
+                    a.H, static_cast<float*>(a.dw_router.p), a.dw_router.ld, a.dbias);
 }
 
 }  // namespace blk

@@ -28,7 +28,7 @@ import ctypes as C
 
 import torch
 
-from . import _lib
+from . import _block, _lib
 
 
 class MoELayer:
@@ -468,16 +468,31 @@ class MoEStack:
     x is an fp32 residual stream [T,H] updated in place; each layer runs
     moe_rmsnorm (fp32 -> bf16, zero-centred gain 1 + gamma) and the five layer
     calls, the combine adding the residual and writing fp32 back into x.
+
+    With ``post_gammas`` (one [H] fp32 vector or None per layer), ``gates``
+    (one [H] fp32, [T_max,1] fp32 or None per layer) or a ``scale`` of the
+    residual stream, a layer's output is normalised and gated before it joins
+    the stream, x <- scale * x + gate_l * RMSNorm(MoE_l(RMSNorm(x))): the
+    combine writes the output (bf16) alone, and moe_block_norm does everything
+    between it and the next layer's router in one launch, so that a layer
+    issues as many launches as without.
     """
 
-    def __init__(self, layers, T_max: int, eps: float = 1e-6, gammas=None):
+    def __init__(self, layers, T_max: int, eps: float = 1e-6, gammas=None, post_gammas=None, gates=None,
+                 scale: float = 1.0):
         self.layers = list(layers)
         self.eps = eps
         self.gammas = gammas
+        self.post_gammas, self.gates, self.scale = post_gammas, gates, float(scale)
         H = self.layers[0].H
         dev = self.layers[0].w_router.device
         self.T_max = T_max
         self.n = torch.empty((T_max, H), dtype=torch.bfloat16, device=dev)
+        self.post_norm = post_gammas is not None or gates is not None or self.scale != 1.0
+        for vectors in (post_gammas, gates):
+            for v in vectors or ():
+                assert v is None or (v.is_cuda and v.is_contiguous() and v.dtype == torch.float32)
+                assert v is None or v.shape == (H,) or (vectors is gates and v.shape == (T_max, 1))
         self._norm_bound = {}
 
     def _norm_call(self, x, l, s, raw=None):
@@ -495,20 +510,51 @@ class MoEStack:
             self._norm_bound[key] = c
         return c
 
-    def layer_calls(self, x, l, stream=None, route=True, raw=None):
+    def _block_norm_call(self, x, l, nxt, s):
+        """moe_block_norm after layer l: its output into x, and the norm before
+        layer nxt (None: none) into n."""
+        key = ("block", x.data_ptr(), x.shape[0], l, nxt, s.cuda_stream)
+        c = self._norm_bound.get(key)
+        if c is None:
+            P = _lib._ptr
+            T, H = x.shape
+            post = None if self.post_gammas is None else self.post_gammas[l]
+            gate = None if self.gates is None else self.gates[l]
+            kind = _block.MOE_GATE_NONE if gate is None else \
+                _block.MOE_GATE_CHANNEL if gate.dim() == 1 else _block.MOE_GATE_TOKEN
+            pre = None if nxt is None or self.gammas is None else self.gammas[nxt]
+            f32, bf16 = _block.MOE_ROW_F32, _block.MOE_ROW_BF16
+            c = ("moe_block_norm", _block.load().moe_block_norm,
+                 (P(x), H, f32, P(self.layers[l].out), H, bf16, P(gate), kind, 0, P(post), P(pre), 1,
+                  C.c_float(self.scale), C.c_float(self.eps), T, H, P(x), H, None if nxt is None else P(self.n), H,
+                  None, None, C.c_void_p(s.cuda_stream)))
+            if len(self._norm_bound) > 4096:
+                self._norm_bound.clear()
+            self._norm_bound[key] = c
+        return c
+
+    def layer_calls(self, x, l, stream=None, route=True, raw=None, first=True, nxt=None):
         """Calls of layer l on the residual stream x; raw (optional, [T,H]
-        bf16) receives x rounded to bf16 before normalisation."""
+        bf16) receives x rounded to bf16 before normalisation.  With norms
+        after the layers, first=False leaves out the norm before the layer
+        (the call of the layer before it made it) and nxt names the layer
+        whose norm this layer's last call makes."""
         s = torch.cuda.current_stream() if stream is None else stream
         T = x.shape[0]
         L = self.layers[l]
-        return [self._norm_call(x, l, s, raw)] + L.bound_calls(self.n[:T], T, stream=s, residual=x, out_f32=x,
-                                                              route=route)
+        if not self.post_norm:
+            return [self._norm_call(x, l, s, raw)] + L.bound_calls(self.n[:T], T, stream=s, residual=x, out_f32=x,
+                                                                  route=route)
+        return ([self._norm_call(x, l, s, raw)] if first else []) + \
+            L.bound_calls(self.n[:T], T, stream=s, route=route) + [self._block_norm_call(x, l, nxt, s)]
 
     def forward(self, x, stream=None, layers=None):
         """x [T,H] fp32 on the GPU, updated in place through the layers."""
         assert x.dtype == torch.float32 and x.is_contiguous()
-        for l in (range(len(self.layers)) if layers is None else layers):
-            for call in self.layer_calls(x, l, stream):
+        order = list(range(len(self.layers)) if layers is None else layers)
+        for i, l in enumerate(order):
+            nxt = order[i + 1] if self.post_norm and i + 1 < len(order) else None
+            for call in self.layer_calls(x, l, stream, first=i == 0, nxt=nxt):
                 MoELayer.issue(call)
         return x
 

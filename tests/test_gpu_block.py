@@ -599,6 +599,48 @@ def test_explicit_stream_and_two_calls_at_once():
     near(a["xp"], ref.spread(a["x"], a["inv"], None, torch.zeros_like(a["xp"])))
 
 
+@pytest.mark.parametrize("gates", ["none", "channel", "token"])
+def test_stack_with_norms_after_the_layers(gates):
+    """MoEStack with post norms: each layer's output as MoELayer gives it, then
+    the definition of the norms, rounded to the stream's and the router's types
+    at the same places."""
+    import workloads as wl
+
+    cfg, L, T, eps, scale = wl.TINY, 3, 16, 1e-6, 0.5
+    g = gen(91)
+    H = cfg.H
+    data = [wl.layer_inputs(cfg, DEV, layer=l) for l in range(L)]
+    vec = lambda: [0.2 * torch.randn(H, generator=g, device=DEV) for _ in range(L)]
+    gammas, post = vec(), vec()
+    gate = {"none": None, "channel": [1 + v for v in vec()],
+            "token": [torch.rand((T, 1), generator=g, device=DEV) for _ in range(L)]}[gates]
+    layers = [M.MoELayer(d["w_router"], d["bias"], d["w_gateup"], d["w_down"], cfg.k, T) for d in data]
+    x0 = torch.randn((T, H), generator=g, device=DEV)
+    stack = M.MoEStack(layers, T, eps, gammas, post_gammas=post, gates=gate, scale=scale)
+    x = stack.forward(x0.clone())
+    # the same layers, one call at a time
+    want, n = x0.clone(), torch.empty((T, H), dtype=BF16, device=DEV)
+    _lib.moe_rmsnorm(want, gammas[0], eps, n)
+    for l in range(L):
+        y = layers[l].forward(n).clone()
+        ref_l = ref.norm(want, y, None if gate is None else gate[l], post[l], gammas[l + 1] if l + 1 < L else None,
+                         scale, eps, True, F32, BF16)
+        nxt = torch.empty_like(want)
+        M.moe_block_norm(want, y, nxt, n, gamma_post=post[l], gamma_pre=gammas[l + 1] if l + 1 < L else None,
+                         gate=None if gate is None else gate[l], scale=scale, eps=eps)
+        near(nxt, ref_l["x_out"], f"layer {l}")
+        near(n, ref_l["n_out"], f"layer {l}")
+        want = nxt
+    assert torch.equal(x, want)
+    # standing alone, a layer makes its own norms
+    y1 = x0.clone()
+    for l in range(L):
+        for call in stack.layer_calls(y1, l):
+            M.MoELayer.issue(call)
+    assert float((y1 - x).abs().max()) <= 2 ** -6 * float(x.abs().max())  # another bf16 rounding of n per layer
+    assert all(m.read_status() == 0 for m in layers)
+
+
 def test_a_block_forward_and_backward_against_autograd():
     """norm -> router -> dispatch -> one linear map per expert -> collect -> norms, and its gradients, chained as
     a training step chains them, against torch.autograd of the definition in 64 bits.
