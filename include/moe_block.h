@@ -14,16 +14,22 @@
  *  - Any width 1 <= H <= 65536 (the norms: 16384) and any alignment that the
  *    element type has by itself.  Rows that start on 8-element boundaries
  *    (bf16: pointer % 16 == 0, fp32: pointer % 32 == 0, ld % 8 == 0) move in
- *    16 and 32 byte pieces; others element by element.
+ *    16 and 32 byte pieces, others element by element; the norms also take
+ *    units of 4 and 2 elements, where these divide H and all rows allow it.
  *  - Every sum, norm factor, product and gradient is computed in fp32 in a
  *    fixed order: the same bits on every call.  A bf16 output is rounded once.
  *  - Outputs must not overlap inputs or one another, except where a call
  *    says so.
  *  - T == 0 is accepted: outputs per token are empty, and outputs per column
  *    or expert (the sum of nothing) are written as zeros.
- *  - k <= 32, E <= 1024, T * k < 2^31; anything else is MOE_ENOTSUP.
+ *  - k <= 32, E <= 1024, T <= 2^30, T * k < 2^31; anything else is
+ *    MOE_ENOTSUP.
  *  - Values are not checked: infinities and NaN go where the formulas take
- *    them.  Rows that no route names are never read.
+ *    them.  Rows that no route names are never read.  Sums of squares are
+ *    fp32: a norm's rows stay below about 1e18 in size.
+ *  - A call may be captured into a CUDA graph; make one call of its kind on
+ *    the device before, which loads the library's device code.  Captured calls
+ *    that share a workspace must not be replayed at the same time.
  */
 #ifndef MOE_BLOCK_H_
 #define MOE_BLOCK_H_

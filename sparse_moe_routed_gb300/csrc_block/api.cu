@@ -36,6 +36,7 @@ using moe::blk::Rows;
 
 constexpr int kMaxH = 65536;      // the row movements
 constexpr int kMaxNormH = 16384;  // the norms
+constexpr int kMaxT = 1 << 30;    // tokens: launch sizes are computed in int
 
 inline bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool a4(const void* p) { return aligned(p, 4); }
@@ -63,7 +64,7 @@ inline moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK 
 
 moe_status check_routes(int T, int k, int H, int R, const int32_t* slots, const float* w, const int32_t* status) {
   if (T < 0 || k <= 0 || H <= 0 || R < 0) return MOE_ESHAPE;
-  if (k > moe::kMaxK || H > kMaxH || static_cast<long long>(T) * k >= (1LL << 31)) return MOE_ENOTSUP;
+  if (k > moe::kMaxK || H > kMaxH || T > kMaxT || static_cast<long long>(T) * k >= (1LL << 31)) return MOE_ENOTSUP;
   if (T > 0 && !slots) return MOE_EINVAL;
   if (!a4(slots) || !a4(w) || !a4(status)) return MOE_EINVAL;
   return MOE_OK;
@@ -145,7 +146,7 @@ static moe_status check_norm(int x_type, const void* y, int y_type, const void* 
                              const float* gamma_post, const float* gamma_pre, int post_norm, float scale, int T,
                              int H) {
   if (T < 0 || H <= 0) return MOE_ESHAPE;
-  if (H > kMaxNormH) return MOE_ENOTSUP;
+  if (H > kMaxNormH || T > kMaxT) return MOE_ENOTSUP;
   if (!type_ok(x_type) || !type_ok(y_type)) return MOE_EINVAL;
   if (gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_FULL) return MOE_EINVAL;
   if ((gate_kind == MOE_GATE_NONE) != (gate == nullptr) && !(T == 0 && gate_kind >= MOE_GATE_TOKEN))
@@ -198,7 +199,7 @@ moe_status moe_block_norm(const void* x, int64_t ldx, int x_type, const void* y,
 }
 
 size_t moe_block_norm_workspace_size(int T, int H) {
-  if (T < 0 || H <= 0 || H > kMaxNormH) return 0;
+  if (T < 0 || H <= 0 || H > kMaxNormH || T > kMaxT) return 0;
   return moe::blk::block_norm_ws_bytes(T, H);
 }
 
@@ -264,7 +265,7 @@ moe_status moe_block_norm_backward(const void* dx_out, int64_t ld_dxo, const voi
 }
 
 size_t moe_route_backward_workspace_size(int T, int k, int E, int H) {
-  if (T < 0 || k <= 0 || E <= 0 || H <= 0 || k > moe::kMaxK || E > moe::kMaxE || H > kMaxH ||
+  if (T < 0 || k <= 0 || E <= 0 || H <= 0 || k > moe::kMaxK || E > moe::kMaxE || H > kMaxH || T > kMaxT ||
       static_cast<long long>(T) * k >= (1LL << 31))
     return 0;
   return moe::blk::route_grad_ws_bytes(T, k, E, H);
@@ -277,7 +278,7 @@ moe_status moe_route_backward(const float* dw, const float* topk_w, const int32_
                               int64_t ld_dw, float* dbias, void* workspace, size_t workspace_bytes,
                               int32_t* dev_status, void* stream) {
   if (T < 0 || k <= 0 || E <= 0 || H <= 0) return MOE_ESHAPE;
-  if (k > moe::kMaxK || k > E || E > moe::kMaxE || H > kMaxH) return MOE_ENOTSUP;
+  if (k > moe::kMaxK || k > E || E > moe::kMaxE || H > kMaxH || T > kMaxT) return MOE_ENOTSUP;
   if (static_cast<long long>(T) * k >= (1LL << 31)) return MOE_ENOTSUP;
   if (!type_ok(dx_type)) return MOE_EINVAL;
   moe::blk::RouteGradArgs a{};

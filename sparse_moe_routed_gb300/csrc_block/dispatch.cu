@@ -130,8 +130,7 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
     const Cols<VEC> c(base, lane, 32);
     Raw8<TT> xr;
     load8<VEC>(row, c, H, xr);
-    float x[8];
-    unpack(xr, x);
+    const V8 x = unpack(xr);
 #pragma unroll
     for (int b = 0; b < NK / kBatch<SOLO>; ++b) {
       if (b * kBatch<SOLO> >= n) break;
@@ -153,16 +152,11 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
         const int64_t s = j < n ? sh.at[j] : -1;
         if (s < 0) continue;
         if (DOT) {
-          float y[8];
-          unpack(v[DOT ? u : 0], y);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) part[DOT ? (b * kBatch<SOLO> + u) / 8 : 0][(b * kBatch<SOLO> + u) % 8] =
-              fmaf(x[i], y[i], part[DOT ? (b * kBatch<SOLO> + u) / 8 : 0][(b * kBatch<SOLO> + u) % 8]);
+          float2 p = splat(0.f);
+          dot8(x, unpack(v[DOT ? u : 0]), p);
+          part[DOT ? j / 8 : 0][j % 8] += p.x + p.y;
         }
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = sh.w[j] * x[i];
-        store8<VEC>(out + s * ld_out, c, H, o);
+        store8<VEC>(out + s * ld_out, c, H, x * sh.w[j]);
       }
     }
   }
@@ -196,14 +190,12 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
   const int first = SOLO ? 0 : blockIdx.y * warps + warp, stride = SOLO ? 1 : gridDim.y * warps;
   for (int base = first * 256; base < H; base += stride * 256) {
     const Cols<VEC> c(base, lane, 32);
-    float x[8], acc[8];
+    V8 x = zero8(), acc = zero8();
     if (DOT) {
       Raw8<TR> xr;
       load8<VEC>(dot + t * ld_dot, c, H, xr);
-      unpack(xr, x);
+      x = unpack(xr);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
 #pragma unroll
     for (int b = 0; b < NK / kBatch<SOLO>; ++b) {
       if (b * kBatch<SOLO> >= k) break;
@@ -221,24 +213,19 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
       for (int u = 0; u < kBatch<SOLO>; ++u) {
         const int j = b * kBatch<SOLO> + u;
         if (j >= k || sh.at[j] < 0) continue;
-        float y[8];
-        unpack(v[u], y);
-        const float wj = sh.w[j];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          acc[i] = fmaf(wj, y[i], acc[i]);
-          if (DOT) part[DOT ? (b * kBatch<SOLO> + u) / 8 : 0][(b * kBatch<SOLO> + u) % 8] =
-              fmaf(x[i], y[i], part[DOT ? (b * kBatch<SOLO> + u) / 8 : 0][(b * kBatch<SOLO> + u) % 8]);
+        const V8 y = unpack(v[u]);
+        acc = fma8(y, sh.w[j], acc);
+        if (DOT) {
+          float2 p = splat(0.f);
+          dot8(x, y, p);
+          part[DOT ? j / 8 : 0][j % 8] += p.x + p.y;
         }
       }
     }
     if (add != nullptr) {
       Raw8<TO> ar;
       load8<VEC>(add + t * ld_add, c, H, ar);
-      float a[8];
-      unpack(ar, a);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += a[i];
+      acc = acc + unpack(ar);
     }
     store8<VEC>(out + t * ld_out, c, H, acc);
   }

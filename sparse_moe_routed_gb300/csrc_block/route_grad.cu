@@ -16,7 +16,7 @@
 // memory and reads every route's row from there; with few, or rows that are
 // not aligned, it is the join of dispatch.cu with the router as its rows and
 // the expert IDs as its slots.
-// dw_router: one warp per unit of at most kUnit routes and 256 columns.  An
+// dw_router: one warp per unit of some routes of one expert and 256 columns.  An
 // expert of one unit is written directly; the units of a popular expert leave
 // partial rows that a last launch adds in order.
 #include <algorithm>
@@ -29,7 +29,12 @@ namespace blk {
 
 namespace {
 
-constexpr int kUnit = 128;          // routes per unit
+// Routes per unit: short units keep few routes from waiting on one warp's
+// long chain, long ones save partial rows.  Per call with dx NULL, top 10 of
+// 512 experts, width 2,560, zipf 1 popularity: 512 tokens 13.7 us with units
+// of 64, 16.1 with 128; 4,096 tokens 37.1 with 128, 40.7 with 64 and with
+// 256; 16,384 tokens 101 with 256, 120 with 128.
+inline int unit_for(int R) { return R <= 10000 ? 64 : R <= 100000 ? 128 : 256; }
 constexpr int kPlanThreads = 1024;  // >= kMaxE
 constexpr int kBatch = 8;           // rows whose loads a thread has in flight
 constexpr int kRowWarps = 4;        // warps per CTA of the row sums
@@ -46,9 +51,9 @@ struct Multi {
   int32_t e, part0, n, pad;
 };
 
-inline int max_units(int R, int E) { return E + R / kUnit; }
-inline int max_multi(int R) { return R / kUnit; }
-inline int max_partials(int R) { return 2 * (R / kUnit) + 1; }
+inline int max_units(int R, int E) { return E + R / unit_for(R); }
+inline int max_multi(int R) { return R / unit_for(R); }
+inline int max_partials(int R) { return 2 * (R / unit_for(R)) + 1; }
 
 // The workspace's parts, 256-byte aligned: the units, the experts of several
 // units, partial rows [..][H], their bias sums.
@@ -76,8 +81,9 @@ Ws ws_layout(void* p, int R, int E, int H) {
 }
 
 // Up to this many tokens an expert is one unit (n <= T where a token's experts
-// are distinct): no plan and no join.
-constexpr int kDirectTokens = kUnit;
+// are distinct): no plan and no join (16 tokens, top 4 of 64 experts: 5.4 us
+// against 7.8; at 128 tokens one warp's chain costs more, 13.8 against 12.8).
+constexpr int kDirectTokens = 64;
 
 // Do a thread's offsets rise from 0 to R?
 __device__ __forceinline__ bool offsets_bad(const int32_t* offsets, int e, int E, int R, int& a, int& n) {
@@ -108,11 +114,12 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_tot, u
   return before + incl - v;
 }
 
-// dl, one warp per token, and with `plan` CTA 0 the units of every expert.
+// dl (and a look at the expert IDs), one warp per token, and with `plan` CTA 0
+// the units of every expert.
 __global__ void __launch_bounds__(kPlanThreads)
-    route_plan_kernel(const float* __restrict__ dw, const float* __restrict__ w, const int32_t* __restrict__ offsets,
-                      int T, int k, int E, float* __restrict__ dl, Unit* units_out, Multi* multi_out, int units_max,
-                      int multi_max, int plan, int32_t* status) {
+    route_plan_kernel(const float* __restrict__ dw, const float* __restrict__ w, const int32_t* __restrict__ ids,
+                      const int32_t* __restrict__ offsets, int T, int k, int E, float* __restrict__ dl, Unit* units_out, Multi* multi_out, int units_max,
+                      int multi_max, int plan, int unit, int32_t* status) {
   __shared__ uint64_t warp_tot[32];
   __shared__ int first[kPlanThreads], start[kPlanThreads], count[kPlanThreads], part0[kPlanThreads];
   pdl_wait();
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     const bool bad = __syncthreads_or(tid < E && offsets_bad(offsets, tid, E, T * k, a, n)) != 0;
     // bad offsets: no unit at all.  One sum of three: units (26 bits), partial
     // rows (27), experts of several units (11).
-    const int units = tid < E && !bad ? max(1, (n + kUnit - 1) / kUnit) : 0;
+    const int units = tid < E && !bad ? max(1, (n + unit - 1) / unit) : 0;
     const bool several = units > 1;
     uint64_t total;
     const uint64_t at = block_scan(static_cast<uint64_t>(units) |
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads)
             hi = mid;
         }
         const int i = u - first[lo];
-        d = {lo, start[lo] + i * kUnit, min(kUnit, count[lo] - i * kUnit), part0[lo] < 0 ? -1 : part0[lo] + i};
+        d = {lo, start[lo] + i * unit, min(unit, count[lo] - i * unit), part0[lo] < 0 ? -1 : part0[lo] + i};
       }
       units_out[u] = d;
     }
@@ -162,18 +169,15 @@ __global__ void __launch_bounds__(kPlanThreads)
        t += static_cast<int64_t>(gridDim.x - plan) * warps) {
     const float wj = lane < k ? w[t * k + lane] : 0.f;
     const float gj = lane < k ? dw[t * k + lane] : 0.f;
+    if (lane < k) {
+      const int e = ids[t * k + lane];
+      if (e < 0 || e >= E) set_status(status, MOE_DEV_BAD_EXPERT);
+    }
     float m = lane < k ? wj * gj : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
     if (lane < k) dl[t * k + lane] = wj * (gj - m);
   }
-}
-
-// acc += w times eight bf16 columns
-__device__ __forceinline__ void add_row(float2 (&acc)[4], float w, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  const uint32_t two[4] = {a, b, c, d};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = __ffma2_rn(splat(w), widen(two[i]), acc[i]);
 }
 
 // One warp per unit and piece of 256 columns: it needs no other, so that the
@@ -218,9 +222,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
   };
   const Cols<VEC> c(blockIdx.y * 256, lane, 32);
   const bool whole = VEC && c.first + 8 <= H;
-  float2 acc[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = splat(0.f);
+  V8 acc = zero8();
   float bias = 0.f;
   int2 next = fetch(lane);
   for (int i0 = 0; i0 < un.n; i0 += 32) {
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     for (int j0 = 0; j0 < 32 && valid >> j0 != 0; j0 += kBatch) {
       Raw8<bf16_t> v[kBatch];
       float w[kBatch];
-      if (whole && (valid >> j0 & 0xff) == 0xff) {  // the usual batch: nothing to test per row
+      if (whole && (~(valid >> j0) & ((1u << kBatch) - 1)) == 0) {  // the usual batch: nothing to test per row
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
           const int2 rt = routes[warp][j0 + b];
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
         }
       }
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) add_row(acc, w[b], v[b].v[0], v[b].v[1], v[b].v[2], v[b].v[3]);
+      for (int b = 0; b < kBatch; ++b) acc = fma8(unpack(v[b]), w[b], acc);
     }
   }
   if (dbias != nullptr && blockIdx.y == 0) {
@@ -263,19 +265,16 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     if (lane == 0) (un.part < 0 ? dbias[un.e] : part_bias[un.part]) = bias;
   }
   if (dwr == nullptr) return;
-  float o[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[2 * i] = acc[i].x, o[2 * i + 1] = acc[i].y;
   if (un.part < 0) {
-    store8<VEC>(dwr + un.e * ld_dw, c, H, o);
+    store8<VEC>(dwr + un.e * ld_dw, c, H, acc);
   } else {
     float* out = part_rows + static_cast<size_t>(un.part) * H;  // packed: whole vectors only where H allows it
     if (VEC && H % 8 == 0) {
-      store8<VEC>(out, c, H, o);
+      store8<VEC>(out, c, H, acc);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c.first + i * c.step < H) out[c.first + i * c.step] = o[i];
+        if (c.first + i * c.step < H) out[c.first + i * c.step] = el(acc, i);
     }
   }
 }
@@ -324,7 +323,7 @@ template <typename TO>
 __global__ void __launch_bounds__(kSlabThreads)
     route_dx_kernel(const bf16_t* __restrict__ wr, int64_t ld_wr, const int32_t* __restrict__ ids,
                     const float* __restrict__ dl, int T, int k, int E, int H, TO* dx, int64_t ld_dx, const TO* add,
-                    int64_t ld_add, int32_t* status) {
+                    int64_t ld_add) {
   extern __shared__ __align__(16) unsigned char slab[];  // [E + 1][C] bf16
   constexpr int C = kSlabColumns, kLanes = C / 8, kTokens = 32 / kLanes;
   pdl_wait();
@@ -353,14 +352,8 @@ __global__ void __launch_bounds__(kSlabThreads)
     if (t < T && j < k) {
       id = ids[t * k + j];
       g = dl[t * k + j];
-      if (id == E) id = -1;  // E is this kernel's own name for no route
+      if (id < 0 || id >= E) id = E, g = 0.f;  // flagged where dl was computed
     }
-  };
-  auto check = [&](int& id, float& g) {
-    if (id >= 0 && id <= E) return;
-    if (blockIdx.x == 0) set_status(status, MOE_DEV_BAD_EXPERT);
-    id = E;
-    g = 0.f;
   };
   int64_t t = (static_cast<int64_t>(blockIdx.y) * (kSlabThreads / 32) + warp) * kTokens + sub;
   // the next token's first routes and add are loaded while this one's rows are summed
@@ -378,36 +371,30 @@ __global__ void __launch_bounds__(kSlabThreads)
     float g = g_next;
     const Raw8<TO> ar = a_next;
     ahead(t + step);
-    float2 acc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = splat(0.f);
+    V8 acc = zero8();
     for (int j0 = 0;;) {
-      check(id, g);
       id *= C * 2;  // bytes to the row
       const int n = min(kLanes, k - j0);
 #pragma unroll 1
       for (int b = 0; b < n; b += kSlabBatch) {
-        uint4 q[kSlabBatch];
+        Raw8<bf16_t> q[kSlabBatch];
         float w[kSlabBatch];
 #pragma unroll
         for (int u = 0; u < kSlabBatch; ++u) {
           // a place past k - j0 (and within the token's lanes) holds row E
-          q[u] = *reinterpret_cast<const uint4*>(mine + __shfl_sync(0xffffffffu, id, b + u, kLanes));
+          const uint4 row = *reinterpret_cast<const uint4*>(mine + __shfl_sync(0xffffffffu, id, b + u, kLanes));
+          q[u].v[0] = row.x, q[u].v[1] = row.y, q[u].v[2] = row.z, q[u].v[3] = row.w;
           w[u] = __shfl_sync(0xffffffffu, g, b + u, kLanes);
         }
 #pragma unroll
-        for (int u = 0; u < kSlabBatch; ++u) add_row(acc, w[u], q[u].x, q[u].y, q[u].z, q[u].w);
+        for (int u = 0; u < kSlabBatch; ++u) acc = fma8(unpack(q[u]), w[u], acc);
       }
       j0 += kLanes;
       if (j0 >= k) break;
       route(t, j0 + l, id, g);
     }
     if (t >= T) continue;
-    float a[8];
-    unpack(ar, a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[2 * i] += acc[i].x, a[2 * i + 1] += acc[i].y;
-    store8<true>(dx + t * ld_dx, c, H, a);
+    store8<true>(dx + t * ld_dx, c, H, acc + unpack(ar));
   }
 }
 
@@ -424,7 +411,7 @@ cudaError_t launch_route_dx(const RouteGradArgs& a, cudaStream_t st) {
   const int parts = std::max(1, std::min(per_sm * sm_count() / slabs, (a.T + tokens - 1) / tokens));
   return launch_pdl(kern, dim3(slabs, parts), dim3(kSlabThreads), smem, st,
                     static_cast<const bf16_t*>(a.w_router.p), a.w_router.ld, a.ids, a.dlogits, a.T, a.k, a.E, a.H,
-                    static_cast<TO*>(a.dx.p), a.dx.ld, static_cast<const TO*>(a.add.p), a.add.ld, a.status);
+                    static_cast<TO*>(a.dx.p), a.dx.ld, static_cast<const TO*>(a.add.p), a.add.ld);
 }
 
 }  // namespace
@@ -440,8 +427,8 @@ cudaError_t launch_route_grad(const RouteGradArgs& a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (a.T > 0) {
     const int warps = kPlanThreads / 32, ctas = std::min((a.T + warps - 1) / warps, 4 * sm_count());
-    e = launch_pdl(route_plan_kernel, dim3(ctas + plan), dim3(kPlanThreads), 0, st, a.dw, a.w, a.offsets, a.T, a.k,
-                   a.E, a.dlogits, ws.units, ws.multi, units, multi, plan, a.status);
+    e = launch_pdl(route_plan_kernel, dim3(ctas + plan), dim3(kPlanThreads), 0, st, a.dw, a.w, a.ids, a.offsets, a.T, a.k,
+                   a.E, a.dlogits, ws.units, ws.multi, units, multi, plan, unit_for(R), a.status);
     if (e != cudaSuccess) return e;
   }
   if (a.dx.p != nullptr && a.T > 0) {

@@ -29,16 +29,70 @@ struct Raw8<bf16_t> {
   uint32_t v[4];
 };
 
-__device__ __forceinline__ void unpack(const Raw8<float>& r, float (&f)[8]) {
+// Eight columns as four pairs: two fp32 operations per instruction.
+struct V8 {
+  float2 v[4];
+};
+__device__ __forceinline__ float& el(V8& f, int i) { return i & 1 ? f.v[i / 2].y : f.v[i / 2].x; }
+__device__ __forceinline__ float el(const V8& f, int i) { return i & 1 ? f.v[i / 2].y : f.v[i / 2].x; }
+__device__ __forceinline__ float2 splat(float a) { return make_float2(a, a); }
+__device__ __forceinline__ V8 operator*(const V8& a, const V8& b) {
+  V8 r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = r.v[i];
+  for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], b.v[i]);
+  return r;
 }
-__device__ __forceinline__ void unpack(const Raw8<bf16_t>& r, float (&f)[8]) {
+__device__ __forceinline__ V8 operator*(const V8& a, float b) {
+  V8 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(r.v[i] << 16);
-    f[2 * i + 1] = __uint_as_float(r.v[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], splat(b));
+  return r;
+}
+__device__ __forceinline__ V8 fma8(const V8& a, const V8& b, const V8& c) {
+  V8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], b.v[i], c.v[i]);
+  return r;
+}
+__device__ __forceinline__ V8 fma8(const V8& a, float b, const V8& c) {
+  V8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], splat(b), c.v[i]);
+  return r;
+}
+__device__ __forceinline__ V8 operator+(const V8& a, const V8& b) {
+  V8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __fadd2_rn(a.v[i], b.v[i]);
+  return r;
+}
+__device__ __forceinline__ V8 zero8() {
+  V8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = splat(0.f);
+  return r;
+}
+// s += sum a b
+__device__ __forceinline__ void dot8(const V8& a, const V8& b, float2& s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = __ffma2_rn(a.v[i], b.v[i], s);
+}
+
+__device__ __forceinline__ float2 widen(uint32_t two) {
+  return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+}
+
+__device__ __forceinline__ V8 unpack(const Raw8<float>& r) {
+  V8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.v[i] = make_float2(r.v[2 * i], r.v[2 * i + 1]);
+  return f;
+}
+__device__ __forceinline__ V8 unpack(const Raw8<bf16_t>& r) {
+  V8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.v[i] = widen(r.v[i]);
+  return f;
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -46,13 +100,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ void pack(const float (&f)[8], Raw8<float>& r) {
+__device__ __forceinline__ void pack(const V8& f, Raw8<float>& r) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r.v[i] = f[i];
+  for (int i = 0; i < 4; ++i) r.v[2 * i] = f.v[i].x, r.v[2 * i + 1] = f.v[i].y;
 }
-__device__ __forceinline__ void pack(const float (&f)[8], Raw8<bf16_t>& r) {
+__device__ __forceinline__ void pack(const V8& f, Raw8<bf16_t>& r) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r.v[i] = pack2(f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) r.v[i] = pack2(f.v[i].x, f.v[i].y);
 }
 
 // Whole pieces.  Plain (coherent) loads: an output may be its own input.
@@ -121,7 +175,7 @@ __device__ __forceinline__ void load8(const T* row, const Cols<VEC>& c, int H, R
   }
 }
 template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* row, const Cols<VEC>& c, int H, const float (&f)[8]) {
+__device__ __forceinline__ void store8(T* row, const Cols<VEC>& c, int H, const V8& f) {
   if (VEC && c.first + 8 <= H) {
     Raw8<T> r;
     pack(f, r);
@@ -129,7 +183,7 @@ __device__ __forceinline__ void store8(T* row, const Cols<VEC>& c, int H, const 
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c.first + i * c.step < H) put(row + c.first + i * c.step, f[i]);
+      if (c.first + i * c.step < H) put(row + c.first + i * c.step, el(f, i));
   }
 }
 

@@ -16,41 +16,6 @@
 namespace moe {
 namespace blk {
 
-// Eight columns as four pairs: two fp32 operations per instruction.
-struct V8 {
-  float2 v[4];
-};
-__device__ __forceinline__ float2 splat(float a) { return make_float2(a, a); }
-__device__ __forceinline__ V8 operator*(const V8& a, const V8& b) {
-  V8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], b.v[i]);
-  return r;
-}
-__device__ __forceinline__ V8 operator*(const V8& a, float b) {
-  V8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], splat(b));
-  return r;
-}
-__device__ __forceinline__ V8 fma8(const V8& a, const V8& b, const V8& c) {
-  V8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], b.v[i], c.v[i]);
-  return r;
-}
-__device__ __forceinline__ V8 fma8(const V8& a, float b, const V8& c) {
-  V8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], splat(b), c.v[i]);
-  return r;
-}
-// s += sum a b
-__device__ __forceinline__ void dot8(const V8& a, const V8& b, float2& s) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s = __ffma2_rn(a.v[i], b.v[i], s);
-}
-
 // Bytes of one thread's eight columns of one array.
 template <typename T>
 constexpr int kSlot = 8 * static_cast<int>(sizeof(T));
@@ -95,13 +60,6 @@ __device__ __forceinline__ void stage_row(unsigned char* at, const T* src, int t
       reinterpret_cast<T*>(at)[p * nt] = in ? src[p * nt] : T(0);
     }
   }
-}
-
-// Element i of the eight, for the units narrower than a pair.
-__device__ __forceinline__ float& el(V8& f, int i) { return i & 1 ? f.v[i / 2].y : f.v[i / 2].x; }
-__device__ __forceinline__ float el(const V8& f, int i) { return i & 1 ? f.v[i / 2].y : f.v[i / 2].x; }
-__device__ __forceinline__ float2 widen(uint32_t two) {
-  return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
 }
 
 // Unit p of G columns.

@@ -67,7 +67,8 @@ REFUSALS = [
     ("moe_dispatch", dict(R=-1), ESHAPE), ("moe_dispatch", dict(ldx=63), ESHAPE), ("moe_dispatch", dict(ldp=0), ESHAPE),
     ("moe_dispatch", dict(ldx=-64), ESHAPE), ("moe_dispatch", dict(k=33), ENOTSUP),
     ("moe_dispatch", dict(H=65537, ldx=1 << 17, ldp=1 << 17), ENOTSUP), ("moe_dispatch", dict(T=1 << 29), ENOTSUP),
-    ("moe_dispatch", dict(ldx=1 << 60), ENOTSUP),
+    ("moe_dispatch", dict(ldx=1 << 60), ENOTSUP), ("moe_dispatch", dict(T=(1 << 30) + 1, k=1), ENOTSUP),
+    ("moe_block_norm", dict(T=(1 << 30) + 1), ENOTSUP), ("moe_route_backward", dict(T=(1 << 30) + 1, k=1), ENOTSUP),
     ("moe_dispatch_backward", dict(dxp=None), EINVAL), ("moe_dispatch_backward", dict(dx=None), EINVAL),
     ("moe_dispatch_backward", dict(x=None), EINVAL), ("moe_dispatch_backward", dict(dx=A[0]), EINVAL),
     ("moe_dispatch_backward", dict(dx=A[3]), EINVAL), ("moe_dispatch_backward", dict(add=A[4], lda=128), EINVAL),

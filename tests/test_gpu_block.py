@@ -295,7 +295,7 @@ def test_block_norm_sizes(T, H, types, pad, shift):
 @pytest.mark.parametrize("gate", GATES)
 @pytest.mark.parametrize("post", [True, False])
 @pytest.mark.parametrize("types", TYPES, ids=str)
-@pytest.mark.parametrize("T,H", [(40, 264), (40, 333), (6, 5000), (5, 9000)])
+@pytest.mark.parametrize("T,H", [(40, 264), (40, 333), (6, 5000), (5, 9000), (160, 8192)])
 def test_block_norm_gates(gate, post, types, T, H):
     norm_case(T, H, (types[1], types[0]), gate, post, 0, 0, seed=T + H, scale=1.0, gammas=H % 2 == 0)
 
@@ -432,6 +432,26 @@ def test_route_gradient(T, H, k, E, hot, dtype, pad, shift):
     route_case(T, H, k, E, dtype, pad, shift, seed=T + H + k + E, hot=hot)
 
 
+def test_route_gradient_through_column_slabs():
+    """Enough routed elements for dx to read the router from shared memory: a ragged last slab, one and several
+    chunks of routes per token, more experts than fit, and an ID out of range."""
+    for T, H, k, E, dtype in ((6000, 1000, 9, 77, F32), (2100, 1544, 17, 64, BF16), (6000, 1000, 9, 1000, F32)):
+        assert T * H * k >= 50_000_000
+        route_case(T, H, k, E, dtype, 0, 0, seed=T)
+    T, H, k, E = 6000, 1000, 9, 77
+    g = gen(5)
+    ids = torch.rand((T, E), generator=g, device=DEV).topk(k, 1)[1].to(torch.int32).contiguous()
+    bad = ids.clone()
+    bad[17, 3], bad[5999, 8] = E, -1
+    w = dw = torch.rand((T, k), generator=g, device=DEV)
+    x, wr, status = rand(g, T, H, BF16), rand(g, E, H, BF16), torch.zeros(1, dtype=torch.int32, device=DEV)
+    offsets, perm = group(ids, E)
+    dl, dx = torch.empty((T, k), device=DEV), torch.empty((T, H), device=DEV)
+    M.moe_route_backward(dw, w, bad, x, wr, offsets, perm, dl, dx, None, None, None, dev_status=status)
+    assert int(status) == _lib.MOE_DEV_BAD_EXPERT
+    near(dx, ref.join(wr, torch.where(bad == E, torch.full_like(bad, -1), bad), dl, None, F32))
+
+
 def test_route_gradient_same_expert_in_every_place():
     route_case(200, 96, 6, 7, F32, 0, 0, seed=3, same=True)
 
@@ -480,12 +500,15 @@ def test_route_gradient_bad_grouping_is_flagged():
     status.zero_()
     M.moe_route_backward(dw, w, ids, x, wr, offsets, bad, dl, None, dwr, db, ws, dev_status=status)
     assert int(status) == _lib.MOE_DEV_BAD_EXPERT and bool((dwr != 5).all())
-    bad = ids.clone()
-    bad[0, 0], bad[4, 1] = E, -3
-    status.zero_()
-    M.moe_route_backward(dw, w, bad, x, wr, offsets, perm, dl, torch.empty((T, H), device=DEV), None, None, None,
-                         dev_status=status)
-    assert int(status) == _lib.MOE_DEV_BAD_EXPERT
+    for v in (E, -1, -3):
+        bad = ids.clone()
+        bad[4, 1] = v
+        status.zero_()
+        dx = torch.empty((T, H), device=DEV)
+        M.moe_route_backward(dw, w, bad, x, wr, offsets, perm, dl, dx, None, None, None, dev_status=status)
+        assert int(status) == _lib.MOE_DEV_BAD_EXPERT
+        one = torch.tensor([[int(ids[4, 0]), -1]], dtype=torch.int32, device=DEV)  # the other route is left out
+        near(dx[4:5], ref.join(wr, one, dl[4:5], None, F32))
 
 
 # -- how calls are made ------------------------------------------------------
