@@ -25,7 +25,7 @@ constexpr int kThreads = 1024;
 template <typename TX, typename TY, int G, int NCH>
 __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     block_norm_kernel(const NormArgs a, const NormPlan p) {
-  constexpr bool STAGED = NCH <= kMaxStagedChunks;
+  constexpr bool STAGED = NCH <= kMaxStagedChunks, BY_WORDS = kByWords<TX, G> || kByWords<TY, G>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) float red[15][2][16];
   const int nt = p.nt, H = a.H;
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
   unsigned char* m2 = m1 + NCH * nt * 32;
   auto read_c = [&](const unsigned char* m, int h, V8& f) {
     if (STAGED) {
-      read_staged<float, G>(m, h, nt, f);
+      read_staged<float, G>(m, nullptr, h, tid, nt, H, f);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
       }
     }
   };
-  const int off_y = NCH * nt * kSlot<TX>, off_g = off_y + NCH * nt * kSlot<TY>;
+  const int off_y = region<TX, G, NCH>(nt), off_g = off_y + region<TY, G, NCH>(nt);
   const int64_t step = static_cast<int64_t>(gridDim.x) * p.groups;
   int64_t t = static_cast<int64_t>(blockIdx.x) * p.groups + group;
   // the thread's first place of each operand, in the group's first stage
@@ -112,10 +112,13 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     const unsigned char *ax = mx + at, *ay = my + at;
     if (STAGED) {
       if (p.stages == 1) {
+        if (BY_WORDS) group_sync(nt, group);  // the row before has been read
         stage(0);
         copies_wait(0);
+        if (BY_WORDS) group_sync(nt, group);
       } else {
         copies_wait(p.stages - 2);
+        if (BY_WORDS) group_sync(nt, group);  // this row is there, the one before has been read
         stage(at == 0 ? (p.stages - 1) * p.stage : at - p.stage);
       }
       at = at + p.stage == p.stages * p.stage ? 0 : at + p.stage;
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     if (token && t + step < a.T) gt_next = gate_v[t + step];
     auto read_y = [&](int h, V8& f) {
       if (STAGED)
-        read_staged<TY, G>(ay + off_y, h, nt, f);
+        read_staged<TY, G>(ay + off_y, y + t * a.y.ld, h, tid, nt, H, f);
       else
         read_global<TY, G>(has_y ? y + t * a.y.ld : y, h, tid, nt, has_y ? H : 0, f);
     };
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
 #pragma unroll
     for (int h = 0; h < NCH; ++h) {
       if (STAGED)
-        read_staged<TX, G>(ax, h, nt, xo[h]);
+        read_staged<TX, G>(ax, x + t * a.x.ld, h, tid, nt, H, xo[h]);
       else
         read_global<TX, G>(x + t * a.x.ld, h, tid, nt, H, xo[h]);
       if (NCH > 1) read_y(h, f);
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
       if (full) {
         V8 g;
         if (STAGED)
-          read_staged<TY, G>(ay + off_g, h, nt, g);
+          read_staged<TY, G>(ay + off_g, gate + t * a.gate.ld, h, tid, nt, H, g);
         else
           read_global<TY, G>(gate + t * a.gate.ld, h, tid, nt, H, g);
         f = f * g;
@@ -184,9 +187,10 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
 cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t st) {
   const bool full = a.gate_kind == MOE_GATE_FULL;
   const Rows gate = full ? a.gate : Rows{nullptr, 0, MOE_ROW_F32};
-  NormPlan p = norm_plan(a.T, a.H, row_bytes8(a.x) + (a.y.type == MOE_ROW_F32 ? 32 : 16) + row_bytes8(gate), kThreads);
-  plan_steps(p, {a.x, a.y, gate, a.x_out, a.n_out});
   const int unit = norm_unit(a.H, {a.x, a.y, gate, a.x_out, a.n_out});
+  NormPlan p = norm_plan(a.T, a.H, row_bytes8(a.x) + (a.y.type == MOE_ROW_F32 ? 32 : 16) + row_bytes8(gate),
+                         unit == 1 && (a.x.type == MOE_ROW_BF16 || a.y.type == MOE_ROW_BF16) ? 3 : 0, kThreads);
+  plan_steps(p, {a.x, a.y, gate, a.x_out, a.n_out});
   return norm_dispatch(a.x.type, a.y.type, unit, p.nch, [&](auto tx, auto ty, auto g, auto n) {
     auto kern = block_norm_kernel<decltype(tx), decltype(ty), decltype(g)::value, decltype(n)::value>;
     static std::atomic<uint64_t> done{0};

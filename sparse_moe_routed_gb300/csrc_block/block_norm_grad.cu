@@ -30,7 +30,7 @@ constexpr int kThreads = 640;  // 96 registers a thread: no spills, which would 
 template <typename TX, typename TY, int G, int NCH>
 __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     block_norm_grad_kernel(const NormGradArgs a, const NormPlan p, int want_cols) {
-  constexpr bool STAGED = NCH <= kMaxStagedChunks;
+  constexpr bool STAGED = NCH <= kMaxStagedChunks, BY_WORDS = kByWords<TX, G> || kByWords<TY, G>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) float red[15][2][16];
   const int nt = p.nt, H = a.H;
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
   unsigned char* m2 = m1 + NCH * nt * 32;
   auto read_c = [&](const unsigned char* m, int h, V8& f) {
     if (STAGED) {
-      read_staged<float, G>(m, h, nt, f);
+      read_staged<float, G>(m, nullptr, h, tid, nt, H, f);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     }
   };
 
-  const int bx = NCH * nt * kSlot<TX>, by = NCH * nt * kSlot<TY>;
+  const int bx = region<TX, G, NCH>(nt), by = region<TY, G, NCH>(nt);
   const int off_x = bx, off_dn = off_x + bx, off_y = off_dn + by, off_g = off_y + (has_y ? by : 0);
   const int64_t step = static_cast<int64_t>(gridDim.x) * p.groups;
   int64_t t = static_cast<int64_t>(blockIdx.x) * p.groups + group;
@@ -154,10 +154,13 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     const unsigned char *ax = mx + at, *ay = my + at;
     if (STAGED) {
       if (p.stages == 1) {
+        if (BY_WORDS) group_sync(nt, group);  // the row before has been read
         stage(0);
         copies_wait(0);
+        if (BY_WORDS) group_sync(nt, group);
       } else {
         copies_wait(p.stages - 2);
+        if (BY_WORDS) group_sync(nt, group);  // this row is there, the one before has been read
         stage(at == 0 ? (p.stages - 1) * p.stage : at - p.stage);
       }
       at = at + p.stage == p.stages * p.stage ? 0 : at + p.stage;
@@ -166,13 +169,13 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     factors(t + step);
     auto read_x = [&](int off, const TX* q, int64_t ld, int h, V8& f) {
       if (STAGED)
-        read_staged<TX, G>(ax + off, h, nt, f);
+        read_staged<TX, G>(ax + off, q + t * ld, h, tid, nt, H, f);
       else
         read_global<TX, G>(q == nullptr ? q : q + t * ld, h, tid, nt, q == nullptr ? 0 : H, f);
     };
     auto read_y = [&](int off, const TY* q, int64_t ld, int h, V8& f) {
       if (STAGED)
-        read_staged<TY, G>(ay + off, h, nt, f);
+        read_staged<TY, G>(ay + off, q + t * ld, h, tid, nt, H, f);
       else
         read_global<TY, G>(q == nullptr ? q : q + t * ld, h, tid, nt, q == nullptr ? 0 : H, f);
     };
@@ -330,13 +333,14 @@ cudaError_t launch_block_norm_grad(const NormGradArgs& a, cudaStream_t st) {
     const Rows gate = full ? a.gate : none, dgate = full ? a.dgate : none;
     const int sx = a.dx.type == MOE_ROW_F32 ? 32 : 16, sy = a.y.type == MOE_ROW_F32 ? 32 : 16;
     const int slot = 2 * sx + sy + row_bytes8(a.y) + row_bytes8(gate);
-    NormPlan p = norm_plan(a.T, a.H, slot, kThreads);
+    const int unit = norm_unit(a.H, {a.dx_out, a.x_out, a.dn, a.y, gate, dgate, a.dx, a.dy});
+    const bool bf16 = a.dx.type == MOE_ROW_BF16 || a.y.type == MOE_ROW_BF16;
+    NormPlan p = norm_plan(a.T, a.H, slot, unit == 1 && bf16 ? 5 : 0, kThreads);
     p.grid = std::min(p.grid, sm_count());
     const int cols = p.nch <= kMaxStagedChunks ? (p.groups - 1) * 2 * p.nch * 8 * p.nt * 4 : 2 * p.nch * 8 * p.nt * 4;
     p.smem = std::max(p.smem, cols);  // the sums' join takes the stages' place
     parts = p.grid;
     plan_steps(p, {a.dx_out, a.x_out, a.dn, a.y, gate, a.dx, a.dy});
-    const int unit = norm_unit(a.H, {a.dx_out, a.x_out, a.dn, a.y, gate, dgate, a.dx, a.dy});
     const cudaError_t e = norm_dispatch(a.dx.type, a.y.type, unit, p.nch, [&](auto tx, auto ty, auto g, auto n) {
       auto kern = block_norm_grad_kernel<decltype(tx), decltype(ty), decltype(g)::value, decltype(n)::value>;
       static std::atomic<uint64_t> done{0};

@@ -17,6 +17,7 @@
 // CTAs its routes or columns), and dw adds the warps' sums in order.  dw needs
 // no atomics in either form, and the token's row is read once whatever k is.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "rows.cuh"
@@ -98,9 +99,9 @@ __device__ __forceinline__ void write_dw(const float (&part)[NB][8], float (*red
 
 constexpr int kSoloWarps = 4;  // tokens per CTA where a warp owns a token
 
-// NK: routes per CTA at most.  SOLO: grid (tokens / kSoloWarps); else grid
+// NK: routes per CTA at most (with DOT each has a register).  SOLO: grid (tokens / kSoloWarps); else grid
 // (token, group of jb routes).
-template <typename TT, typename TR, bool VEC, bool DOT, int NK, bool SOLO>
+template <typename TT, typename TR, int U, bool DOT, int NK, bool SOLO>
 __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO ? 7 : 2)
     spread_kernel(const TT* tok, int64_t ld_tok, const TR* dot, int64_t ld_dot, const int32_t* __restrict__ slot_of,
                   const float* __restrict__ w, int T, int k, int jb, int H, int R, TR* out, int64_t ld_out, float* dw,
@@ -127,9 +128,9 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
 #pragma unroll
     for (int u = 0; u < 8; ++u) part[b][u] = 0.f;
   for (int base = (SOLO ? 0 : warp) * 256; base < H; base += warps * 256) {
-    const Cols<VEC> c(base, lane, 32);
+    const Cols<U> c(base, lane, 32);
     Raw8<TT> xr;
-    load8<VEC>(row, c, H, xr);
+    load8<U>(row, c, H, xr);
     const V8 x = unpack(xr);
 #pragma unroll
     for (int b = 0; b < NK / kBatch<SOLO>; ++b) {
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
           const int j = b * kBatch<SOLO> + u;
           const int64_t s = j < n ? sh.at[j] : -1;
           if (s >= 0)
-            load8<VEC>(dot + s * ld_dot, c, H, v[DOT ? u : 0]);
+            load8<U>(dot + s * ld_dot, c, H, v[DOT ? u : 0]);
           else
             raw_zero(v[DOT ? u : 0]);
         }
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
           dot8(x, unpack(v[DOT ? u : 0]), p);
           part[DOT ? j / 8 : 0][j % 8] += p.x + p.y;
         }
-        store8<VEC>(out + s * ld_out, c, H, x * sh.w[j]);
+        store8<U>(out + s * ld_out, c, H, x * sh.w[j]);
       }
     }
   }
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
 
 // SOLO: grid (tokens / kSoloWarps); else grid (token, part of the columns),
 // one part with DOT.
-template <typename TR, typename TO, bool VEC, bool DOT, int NK, bool SOLO>
+template <typename TR, typename TO, int U, bool DOT, int NK, bool SOLO>
 __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO ? 7 : 2)
     join_kernel(const TR* rows, int64_t ld_rows, const TR* dot, int64_t ld_dot, const int32_t* __restrict__ slot_of,
                 const float* __restrict__ w, int T, int k, int H, int R, TO* out, int64_t ld_out, const TO* add,
@@ -189,11 +190,11 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
     for (int u = 0; u < 8; ++u) part[b][u] = 0.f;
   const int first = SOLO ? 0 : blockIdx.y * warps + warp, stride = SOLO ? 1 : gridDim.y * warps;
   for (int base = first * 256; base < H; base += stride * 256) {
-    const Cols<VEC> c(base, lane, 32);
+    const Cols<U> c(base, lane, 32);
     V8 x = zero8(), acc = zero8();
     if (DOT) {
       Raw8<TR> xr;
-      load8<VEC>(dot + t * ld_dot, c, H, xr);
+      load8<U>(dot + t * ld_dot, c, H, xr);
       x = unpack(xr);
     }
 #pragma unroll
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
         const int j = b * kBatch<SOLO> + u;
         const int64_t s = j < k ? sh.at[j] : -1;
         if (s >= 0)
-          load8<VEC>(rows + s, c, H, v[u]);
+          load8<U>(rows + s, c, H, v[u]);
         else
           raw_zero(v[u]);
       }
@@ -224,10 +225,10 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
     }
     if (add != nullptr) {
       Raw8<TO> ar;
-      load8<VEC>(add + t * ld_add, c, H, ar);
+      load8<U>(add + t * ld_add, c, H, ar);
       acc = acc + unpack(ar);
     }
-    store8<VEC>(out + t * ld_out, c, H, acc);
+    store8<U>(out + t * ld_out, c, H, acc);
   }
   if (DOT) write_dw<SOLO, DOT ? NK / 8 : 1>(part, red, sh, dw + r0, k, warp, warps, tid);
 }
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
 // tokens: 47 us with 24 warps per SM, 36 with 120).
 inline int warps_wanted() { return 24 * sm_count(); }
 
-template <typename TT, typename TR, bool VEC, bool DOT>
+template <typename TT, typename TR, int U, bool DOT>
 cudaError_t spread(const Rows& tok, const Rows& dot, const int32_t* slot_of, const float* w, int T, int k, int H,
                    int R, const Rows& out, float* dw, int32_t* status, cudaStream_t st) {
   const int pieces = (H + 255) / 256, want = DOT ? warps_wanted() : 5 * warps_wanted();
@@ -254,15 +255,15 @@ cudaError_t spread(const Rows& tok, const Rows& dot, const int32_t* slot_of, con
   };
   if (warps == 1 && split == 1) {
     const dim3 grid((T + kSoloWarps - 1) / kSoloWarps);
-    return k <= 16 ? go(spread_kernel<TT, TR, VEC, DOT, 16, true>, grid, kSoloWarps * 32)
-                   : go(spread_kernel<TT, TR, VEC, DOT, 32, true>, grid, kSoloWarps * 32);
+    return DOT && k <= 16 ? go(spread_kernel<TT, TR, U, DOT, DOT ? 16 : 32, true>, grid, kSoloWarps * 32)
+                   : go(spread_kernel<TT, TR, U, DOT, 32, true>, grid, kSoloWarps * 32);
   }
   const dim3 grid(T, (k + jb - 1) / jb);
-  return jb <= 16 ? go(spread_kernel<TT, TR, VEC, DOT, 16, false>, grid, warps * 32)
-                  : go(spread_kernel<TT, TR, VEC, DOT, 32, false>, grid, warps * 32);
+  return DOT && jb <= 16 ? go(spread_kernel<TT, TR, U, DOT, DOT ? 16 : 32, false>, grid, warps * 32)
+                  : go(spread_kernel<TT, TR, U, DOT, 32, false>, grid, warps * 32);
 }
 
-template <typename TR, typename TO, bool VEC, bool DOT>
+template <typename TR, typename TO, int U, bool DOT>
 cudaError_t join(const Rows& rows, const Rows& dot, const int32_t* slot_of, const float* w, int T, int k, int H, int R,
                  const Rows& out, const Rows& add, float* dw, int32_t* status, cudaStream_t st) {
   const int pieces = (H + 255) / 256;
@@ -280,48 +281,47 @@ cudaError_t join(const Rows& rows, const Rows& dot, const int32_t* slot_of, cons
   };
   if (warps == 1 && parts == 1) {
     const dim3 grid((T + kSoloWarps - 1) / kSoloWarps);
-    return k <= 16 ? go(join_kernel<TR, TO, VEC, DOT, 16, true>, grid, kSoloWarps * 32)
-                   : go(join_kernel<TR, TO, VEC, DOT, 32, true>, grid, kSoloWarps * 32);
+    return DOT && k <= 16 ? go(join_kernel<TR, TO, U, DOT, DOT ? 16 : 32, true>, grid, kSoloWarps * 32)
+                   : go(join_kernel<TR, TO, U, DOT, 32, true>, grid, kSoloWarps * 32);
   }
   const dim3 grid(T, parts);
-  return k <= 16 ? go(join_kernel<TR, TO, VEC, DOT, 16, false>, grid, warps * 32)
-                 : go(join_kernel<TR, TO, VEC, DOT, 32, false>, grid, warps * 32);
+  return DOT && k <= 16 ? go(join_kernel<TR, TO, U, DOT, DOT ? 16 : 32, false>, grid, warps * 32)
+                 : go(join_kernel<TR, TO, U, DOT, 32, false>, grid, warps * 32);
 }
 
-// f(type tag of a, type tag of b)
+// f(type tag of a, type tag of b, the unit as an integral constant)
 template <typename F>
-cudaError_t by_types(int a, int b, F&& f) {
-  if (a == MOE_ROW_F32) return b == MOE_ROW_F32 ? f(float(), float()) : f(float(), bf16_t());
-  return b == MOE_ROW_F32 ? f(bf16_t(), float()) : f(bf16_t(), bf16_t());
+cudaError_t by_types(int a, int b, int unit, F&& f) {
+  auto g = [&](auto ta, auto tb) {
+    if (unit == 8) return f(ta, tb, std::integral_constant<int, 8>());
+    if (unit == 2) return f(ta, tb, std::integral_constant<int, 2>());
+    return f(ta, tb, std::integral_constant<int, 1>());
+  };
+  if (a == MOE_ROW_F32) return b == MOE_ROW_F32 ? g(float(), float()) : g(float(), bf16_t());
+  return b == MOE_ROW_F32 ? g(bf16_t(), float()) : g(bf16_t(), bf16_t());
 }
 
 }  // namespace
 
 cudaError_t launch_spread(const Rows& tok, const Rows& dot, const int32_t* slot_of, const float* w, int T, int k,
                           int H, int R, const Rows& out, float* dw, int32_t* status, cudaStream_t st) {
-  const bool vec = vec_ok(tok) && vec_ok(out) && (dw == nullptr || vec_ok(dot));
-  return by_types(tok.type, out.type, [&](auto tt, auto tr) {
+  return by_types(tok.type, out.type, row_unit({tok, out, dot}), [&](auto tt, auto tr, auto u) {
     using TT = decltype(tt);
     using TR = decltype(tr);
-    if (dw != nullptr)
-      return vec ? spread<TT, TR, true, true>(tok, dot, slot_of, w, T, k, H, R, out, dw, status, st)
-                 : spread<TT, TR, false, true>(tok, dot, slot_of, w, T, k, H, R, out, dw, status, st);
-    return vec ? spread<TT, TR, true, false>(tok, dot, slot_of, w, T, k, H, R, out, dw, status, st)
-               : spread<TT, TR, false, false>(tok, dot, slot_of, w, T, k, H, R, out, dw, status, st);
+    constexpr int U = decltype(u)::value;
+    return dw != nullptr ? spread<TT, TR, U, true>(tok, dot, slot_of, w, T, k, H, R, out, dw, status, st)
+                         : spread<TT, TR, U, false>(tok, dot, slot_of, w, T, k, H, R, out, dw, status, st);
   });
 }
 
 cudaError_t launch_join(const Rows& rows, const Rows& dot, const int32_t* slot_of, const float* w, int T, int k,
                         int H, int R, const Rows& out, const Rows& add, float* dw, int32_t* status, cudaStream_t st) {
-  const bool vec = vec_ok(rows) && vec_ok(out) && vec_ok(add) && (dw == nullptr || vec_ok(dot));
-  return by_types(rows.type, out.type, [&](auto tr, auto to) {
+  return by_types(rows.type, out.type, row_unit({rows, out, add, dot}), [&](auto tr, auto to, auto u) {
     using TR = decltype(tr);
     using TO = decltype(to);
-    if (dw != nullptr)
-      return vec ? join<TR, TO, true, true>(rows, dot, slot_of, w, T, k, H, R, out, add, dw, status, st)
-                 : join<TR, TO, false, true>(rows, dot, slot_of, w, T, k, H, R, out, add, dw, status, st);
-    return vec ? join<TR, TO, true, false>(rows, dot, slot_of, w, T, k, H, R, out, add, dw, status, st)
-               : join<TR, TO, false, false>(rows, dot, slot_of, w, T, k, H, R, out, add, dw, status, st);
+    constexpr int U = decltype(u)::value;
+    return dw != nullptr ? join<TR, TO, U, true>(rows, dot, slot_of, w, T, k, H, R, out, add, dw, status, st)
+                         : join<TR, TO, U, false>(rows, dot, slot_of, w, T, k, H, R, out, add, dw, status, st);
   });
 }
 

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/moe_block.h"
 
 namespace moe {
@@ -40,10 +42,19 @@ struct Rows {
   int type;
 };
 
-// Rows that start on 8-element boundaries move in whole vectors.
-inline bool vec_ok(const Rows& r) {
+// Rows that start on u-element boundaries (null rows do).
+inline bool starts_on(const Rows& r, int u) {
   return r.p == nullptr ||
-         (r.ld % 8 == 0 && reinterpret_cast<uintptr_t>(r.p) % (r.type == MOE_ROW_F32 ? 32 : 16) == 0);
+         (r.ld % u == 0 && reinterpret_cast<uintptr_t>(r.p) % (u * (r.type == MOE_ROW_F32 ? 4 : 2)) == 0);
+}
+// The unit (rows.cuh) that all of these rows allow: 8, 2 or 1.
+inline int row_unit(std::initializer_list<Rows> all) {
+  int u = 8;
+  for (const Rows& r : all) {
+    if (u == 8 && !starts_on(r, 8)) u = 2;
+    if (u == 2 && !starts_on(r, 2)) u = 1;
+  }
+  return u;
 }
 
 // dispatch.cu.  slot_of [T,k]; weights or NULL.

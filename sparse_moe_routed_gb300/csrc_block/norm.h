@@ -23,11 +23,13 @@ struct NormPlan {
   int64_t by[8];  // bytes from a group's row to its next, per operand
 };
 
-// slot: bytes per thread of all operands' eight columns; max_threads: threads
-// per CTA where a thread has eight columns.  One CTA per SM walks the rows (more where CTAs are small): a row's
-// two sums put two barriers between its reads and its writes, so the copies
-// of the rows ahead, not more threads, keep the memory busy.
-inline NormPlan norm_plan(int T, int H, int slot, int max_threads) {
+// slot: bytes per thread of all operands' eight columns; words: how many
+// operands are staged by words at most (kByWords); max_threads: threads per CTA
+// where a thread has eight columns.  One CTA per SM walks the rows (more where
+// CTAs are small): a row's two sums put two barriers between its reads and its
+// writes, so the copies of the rows ahead, not more threads, keep the memory
+// busy.
+inline NormPlan norm_plan(int T, int H, int slot, int words, int max_threads) {
   NormPlan p;
   const int chunks = (H + 7) / 8;
   p.nch = chunks <= kMaxGroupThreads ? 1 : chunks <= 2 * kMaxGroupThreads ? 2 : 4;
@@ -36,7 +38,7 @@ inline NormPlan norm_plan(int T, int H, int slot, int max_threads) {
   const int sms = sm_count();
   p.groups = std::max(1, std::min(p.nt == 32 ? 32 : 15, max_threads / p.nt));
   p.groups = std::max(1, std::min(p.groups, (T + sms - 1) / sms));
-  p.stage = p.nch <= kMaxStagedChunks ? slot * p.nch * p.nt : 0;
+  p.stage = p.nch <= kMaxStagedChunks ? slot * p.nch * p.nt + 16 * words : 0;
   p.gains = p.nch <= kMaxStagedChunks ? 2 * 32 * p.nch * p.nt : 0;
   const int room = kNormSmem - p.gains;
   while (p.groups > 1 && p.stage * p.groups * 2 > room) --p.groups;
@@ -58,11 +60,8 @@ inline void plan_steps(NormPlan& p, std::initializer_list<Rows> all) {
 // The widest unit of adjacent columns that the width and every row allow.
 inline int norm_unit(int H, std::initializer_list<Rows> all) {
   int g = H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
-  for (const Rows& r : all) {
-    if (r.p == nullptr) continue;
-    const int bytes = r.type == MOE_ROW_F32 ? 4 : 2;
-    while (g > 1 && (r.ld % g != 0 || reinterpret_cast<uintptr_t>(r.p) % (g * bytes) != 0)) g /= 2;
-  }
+  for (const Rows& r : all)
+    while (g > 1 && !starts_on(r, g)) g /= 2;
   return g;
 }
 

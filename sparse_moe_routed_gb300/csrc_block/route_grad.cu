@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 // chain of loads in front of its rows (unit, route, dl) overlaps the rows of
 // the SM's other warps.  grid (units / kRowWarps, pieces).  DIRECT: the units
 // are the experts.
-template <bool VEC, bool DIRECT>
+template <int U, bool DIRECT>
 __global__ void __launch_bounds__(kRowWarps * 32)
     route_rows_kernel(const float* __restrict__ dl, const int32_t* __restrict__ offsets,
                       const int32_t* __restrict__ perm, const bf16_t* __restrict__ x, int64_t ldx, int R, int k, int E,
@@ -220,8 +220,8 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     set_status(status, MOE_DEV_BAD_EXPERT);
     return make_int2(-1, 0);
   };
-  const Cols<VEC> c(blockIdx.y * 256, lane, 32);
-  const bool whole = VEC && c.first + 8 <= H;
+  const Cols<U> c(blockIdx.y * 256, lane, 32);
+  const bool whole = U == 8 && c.first + 8 <= H;
   V8 acc = zero8();
   float bias = 0.f;
   int2 next = fetch(lane);
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
           const int2 rt = routes[warp][j0 + b];
           w[b] = __int_as_float(rt.y);
           if (rt.x >= 0)
-            load8<VEC>(x + rt.x * ldx, c, H, v[b]);
+            load8<U>(x + rt.x * ldx, c, H, v[b]);
           else
             raw_zero(v[b]);
         }
@@ -266,15 +266,15 @@ __global__ void __launch_bounds__(kRowWarps * 32)
   }
   if (dwr == nullptr) return;
   if (un.part < 0) {
-    store8<VEC>(dwr + un.e * ld_dw, c, H, acc);
+    store8<U>(dwr + un.e * ld_dw, c, H, acc);
   } else {
     float* out = part_rows + static_cast<size_t>(un.part) * H;  // packed: whole vectors only where H allows it
-    if (VEC && H % 8 == 0) {
-      store8<VEC>(out, c, H, acc);
+    if (U == 8 && H % 8 == 0) {
+      store8<U>(out, c, H, acc);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c.first + i * c.step < H) out[c.first + i * c.step] = el(acc, i);
+        if (c.at(i) < H) out[c.at(i)] = el(acc, i);
     }
   }
 }
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kSlabThreads)
   copies_wait(0);
   __syncthreads();
   const int sub = lane / kLanes, l = lane % kLanes;
-  const Cols<true> c(col, l, kLanes);
+  const Cols<8> c(col, l, kLanes);
   const unsigned char* mine = slab + l * 16;
   const int64_t step = static_cast<int64_t>(gridDim.y) * (kSlabThreads / 32) * kTokens;
   // lane l of the token's lanes reads routes l, l + kLanes, ...
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kSlabThreads)
   auto ahead = [&](int64_t at) {
     route(at, l, id_next, g_next);
     raw_zero(a_next);
-    if (at < T && add != nullptr) load8<true>(add + at * ld_add, c, H, a_next);
+    if (at < T && add != nullptr) load8<8>(add + at * ld_add, c, H, a_next);
   };
   ahead(t);
   for (; t - sub < T; t += step) {
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kSlabThreads)
       route(t, j0 + l, id, g);
     }
     if (t >= T) continue;
-    store8<true>(dx + t * ld_dx, c, H, acc + unpack(ar));
+    store8<8>(dx + t * ld_dx, c, H, acc + unpack(ar));
   }
 }
 
@@ -434,7 +434,7 @@ cudaError_t launch_route_grad(const RouteGradArgs& a, cudaStream_t st) {
   if (a.dx.p != nullptr && a.T > 0) {
     const Rows none = {nullptr, 0, MOE_ROW_BF16};
     if (static_cast<int64_t>(R) * a.H >= kSlabElements && (a.E + 1) * kSlabColumns * 2 <= kNormSmem &&
-        vec_ok(a.w_router) && vec_ok(a.dx) && vec_ok(a.add))
+        row_unit({a.w_router, a.dx, a.add}) == 8)
       e = a.dx.type == MOE_ROW_F32 ? launch_route_dx<float>(a, st) : launch_route_dx<bf16_t>(a, st);
     else
       e = launch_join(a.w_router, none, a.ids, a.dlogits, a.T, a.k, a.H, a.E, a.dx, a.add, nullptr, a.status, st);
@@ -442,14 +442,20 @@ cudaError_t launch_route_grad(const RouteGradArgs& a, cudaStream_t st) {
   }
   if (!rows) return cudaSuccess;
   const int pieces = a.dw_router.p != nullptr ? (a.H + 255) / 256 : 1;
-  const bool vec = vec_ok(a.x) && vec_ok(a.dw_router);
+  const int unit = row_unit({a.x, a.dw_router});
   auto go = [&](auto kern) {
     return launch_pdl(kern, dim3((units + kRowWarps - 1) / kRowWarps, pieces), dim3(kRowWarps * 32), 0, st, a.dlogits,
                       a.offsets, a.perm, static_cast<const bf16_t*>(a.x.p), a.x.ld, R, a.k, a.E, a.H, ws.units, units,
                       static_cast<float*>(a.dw_router.p), a.dw_router.ld, a.dbias, ws.rows, ws.bias, a.status);
   };
-  e = direct ? (vec ? go(route_rows_kernel<true, true>) : go(route_rows_kernel<false, true>))
-             : (vec ? go(route_rows_kernel<true, false>) : go(route_rows_kernel<false, false>));
+  if (direct)
+    e = unit == 8   ? go(route_rows_kernel<8, true>)
+        : unit == 2 ? go(route_rows_kernel<2, true>)
+                    : go(route_rows_kernel<1, true>);
+  else
+    e = unit == 8   ? go(route_rows_kernel<8, false>)
+        : unit == 2 ? go(route_rows_kernel<2, false>)
+                    : go(route_rows_kernel<1, false>);
   if (e != cudaSuccess || multi == 0) return e;
   return launch_pdl(route_join_kernel, dim3(multi, (a.H + 1023) / 1024), dim3(256), 0, st, ws.multi, ws.rows, ws.bias,
                     a.H, static_cast<float*>(a.dw_router.p), a.dw_router.ld, a.dbias);

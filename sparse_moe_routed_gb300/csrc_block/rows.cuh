@@ -1,11 +1,12 @@
 // Rows of fp32 or bf16 elements, moved eight elements per lane.
 //
-// A row is cut into pieces of 8 elements per thread.  Where rows start on
-// 8-element boundaries (VEC) a thread's eight elements are adjacent: one 16
-// byte access for bf16, one 32 byte access for fp32, so that bf16 and fp32
-// rows of one call are indexed alike and every access fills whole 32 byte
-// sectors.  Else they are n threads apart and every access is one element
-// wide.  The last piece of a row may be partial in both forms.
+// A row is cut into pieces of 8 elements per thread, in units of U adjacent
+// elements.  U = 8, where all rows start on 8-element boundaries: one 16 byte
+// access for bf16, one 32 byte access for fp32, so that bf16 and fp32 rows of
+// one call are indexed alike and every access fills whole 32 byte sectors.
+// U = 2, where they start on even elements, and U = 1: the units are n threads
+// apart, so that a warp's accesses are adjacent.  A row's last piece and its
+// last unit may be partial.
 #pragma once
 
 #include <stdint.h>
@@ -153,37 +154,62 @@ __device__ __forceinline__ void raw_zero(Raw8<T>& r) {
   for (unsigned i = 0; i < sizeof(r.v) / sizeof(r.v[0]); ++i) r.v[i] = 0;
 }
 
-// Which columns thread `tid` of `n` holds of the piece that starts at
-// column `base` and spans 8 n columns: element i is column first + i * step.
-template <bool VEC>
+// Which columns thread `tid` of `n` holds of the piece that starts at column
+// `base` and spans 8 n columns.
+template <int U>
 struct Cols {
-  int first;
-  int step;
-  __device__ __forceinline__ Cols(int base, int tid, int n) : first(base + (VEC ? tid * 8 : tid)), step(VEC ? 1 : n) {}
+  int first;  // of the thread's first unit
+  int step;   // from unit to unit
+  __device__ __forceinline__ Cols(int base, int tid, int n) : first(base + tid * U), step(n * U) {}
+  __device__ __forceinline__ int at(int i) const { return first + i / U * step + i % U; }
 };
 
+// Two adjacent elements of a row that starts on an even one.
+__device__ __forceinline__ void load_pair(const float* p, int i, Raw8<float>& r) {
+  asm volatile("ld.global.v2.f32 {%0,%1}, [%2];" : "=f"(r.v[i]), "=f"(r.v[i + 1]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void load_pair(const bf16_t* p, int i, Raw8<bf16_t>& r) {
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(r.v[i / 2]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void store_pair(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+__device__ __forceinline__ void store_pair(bf16_t* p, float2 v) { *reinterpret_cast<uint32_t*>(p) = pack2(v.x, v.y); }
+
 // Elements past column H read as zero.
-template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T* row, const Cols<VEC>& c, int H, Raw8<T>& r) {
-  if (VEC && c.first + 8 <= H) {
+template <int U, typename T>
+__device__ __forceinline__ void load8(const T* row, const Cols<U>& c, int H, Raw8<T>& r) {
+  if (U == 8 && c.first + 8 <= H) {
     load_vec(row + c.first, r);
-  } else {
-    raw_zero(r);
+    return;
+  }
+  raw_zero(r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c.first + i * c.step < H) raw_set(r, i, row[c.first + i * c.step]);
+  for (int i = 0; i < 8; i += 2) {
+    const int a = c.at(i);
+    if (U == 2 && a + 1 < H) {
+      load_pair(row + a, i, r);
+    } else {
+      if (a < H) raw_set(r, i, row[a]);
+      if (c.at(i + 1) < H) raw_set(r, i + 1, row[c.at(i + 1)]);
+    }
   }
 }
-template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* row, const Cols<VEC>& c, int H, const V8& f) {
-  if (VEC && c.first + 8 <= H) {
+template <int U, typename T>
+__device__ __forceinline__ void store8(T* row, const Cols<U>& c, int H, const V8& f) {
+  if (U == 8 && c.first + 8 <= H) {
     Raw8<T> r;
     pack(f, r);
     store_vec(row + c.first, r);
-  } else {
+    return;
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c.first + i * c.step < H) put(row + c.first + i * c.step, el(f, i));
+  for (int i = 0; i < 8; i += 2) {
+    const int a = c.at(i);
+    if (U == 2 && a + 1 < H) {
+      store_pair(row + a, f.v[i / 2]);
+    } else {
+      if (a < H) put(row + a, el(f, i));
+      if (c.at(i + 1) < H) put(row + c.at(i + 1), el(f, i + 1));
+    }
   }
 }
 

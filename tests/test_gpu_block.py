@@ -65,7 +65,7 @@ SIZES = [  # T, H, k
 
 @pytest.mark.parametrize("types", TYPES, ids=str)
 @pytest.mark.parametrize("T,H,k", SIZES)
-@pytest.mark.parametrize("pad,shift,drop", [(0, 0, 0.0), (8, 0, 0.3), (3, 1, 0.3)])
+@pytest.mark.parametrize("pad,shift,drop", [(0, 0, 0.0), (8, 0, 0.3), (3, 1, 0.3), (2, 2, 0.0)])
 def test_rows_to_experts_and_back(T, H, k, types, pad, shift, drop):
     rows, tok = types
     g = gen(T * 7919 + H * 31 + k)
@@ -282,12 +282,12 @@ def norm_case(T, H, types, gate_kind, post, pad, shift, seed, scale=0.75, eps=1e
 
 NORM_SIZES = [(1, 1), (1, 2560), (3, 8), (2, 31), (5, 257), (7, 520), (16, 2560), (33, 1001), (3, 4096), (3, 4104),
               (2, 8192), (2, 8200), (3, 16384), (1, 16383), (1300, 256), (2500, 64), (701, 640), (450, 2560),
-              (317, 4200), (309, 9000)]
+              (317, 4200), (309, 9000), (160, 8191)]
 
 
 @pytest.mark.parametrize("T,H", NORM_SIZES)
 @pytest.mark.parametrize("types", TYPES, ids=str)
-@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 0), (3, 1)])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 0), (3, 1), (2, 2)])
 def test_block_norm_sizes(T, H, types, pad, shift):
     norm_case(T, H, (types[1], types[0]), "channel", True, pad, shift, seed=T * 131 + H)
 
@@ -316,6 +316,23 @@ def test_block_norm_small_rows_with_eps_zero():
     want = ref.norm_grad(dxo, dn, xo, y, gate, None, None, 1.0, r1, r2, True, F32, F32)
     for name, got in (("dx", dx), ("dy", dy), ("dgate", dg)):
         near(got, want[name], name)
+
+
+@pytest.mark.parametrize("T,H", [(40, 257), (37, 2560), (7, 5001)])
+@pytest.mark.parametrize("gate", ["token", "full"])
+def test_block_norm_rows_on_odd_elements(T, H, gate):
+    """bf16 rows whose starts alternate between the halves of a word, beside NaN in the gaps."""
+    norm_case(T, H, (BF16, BF16), gate, True, 1 + H % 2, 1, seed=T)
+    g = gen(T)
+    x, y = rand(g, T, H, BF16), rand(g, T, H, BF16)
+    xg = torch.full((T, H + 1 + H % 2), NAN, dtype=BF16, device=DEV)
+    yg = xg.clone()
+    xg[:, :H], yg[:, :H] = x, y
+    outs = [torch.empty((T, H), dtype=BF16, device=DEV) for _ in range(4)]
+    M.moe_block_norm(x, y, outs[0], outs[1])
+    M.moe_block_norm(xg[:, :H], yg[:, :H], outs[2], outs[3])
+    near(outs[2], ref.norm(x, y, None, None, None, 1.0, 1e-6, True, BF16, BF16)["x_out"])
+    near(outs[3], ref.norm(x, y, None, None, None, 1.0, 1e-6, True, BF16, BF16)["n_out"])
 
 
 def test_block_norm_zero_row_and_special_rows():
@@ -427,7 +444,7 @@ def route_case(T, H, k, E, dtype, pad, shift, seed, hot=None, same=False):
     (37, 1001, 3, 5, None), (300, 128, 8, 8, None), (1000, 2560, 10, 512, None), (1025, 136, 32, 1024, 40),
     (2100, 72, 2, 9, 2), (777, 4100, 5, 33, 5), (256, 64, 1, 3, 1), (257, 64, 1, 3, 1), (2, 65536, 2, 4, None),
 ])
-@pytest.mark.parametrize("dtype,pad,shift", [(F32, 0, 0), (BF16, 8, 0), (F32, 3, 1)], ids=str)
+@pytest.mark.parametrize("dtype,pad,shift", [(F32, 0, 0), (BF16, 8, 0), (F32, 3, 1), (BF16, 2, 2)], ids=str)
 def test_route_gradient(T, H, k, E, hot, dtype, pad, shift):
     route_case(T, H, k, E, dtype, pad, shift, seed=T + H + k + E, hot=hot)
 
