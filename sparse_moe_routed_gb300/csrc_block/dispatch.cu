@@ -99,8 +99,8 @@ __device__ __forceinline__ void write_dw(const float (&part)[NB][8], float (*red
 
 constexpr int kSoloWarps = 4;  // tokens per CTA where a warp owns a token
 
-// NK: routes per CTA at most (with DOT each has a register).  SOLO: grid (tokens / kSoloWarps); else grid
-// (token, group of jb routes).
+// NK: routes per CTA at most (with DOT each has a register).  SOLO: grid
+// (tokens / kSoloWarps); else grid (token, group of jb routes).
 template <typename TT, typename TR, int U, bool DOT, int NK, bool SOLO>
 __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO ? 7 : 2)
     spread_kernel(const TT* tok, int64_t ld_tok, const TR* dot, int64_t ld_dot, const int32_t* __restrict__ slot_of,
@@ -240,13 +240,19 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
 // tokens: 47 us with 24 warps per SM, 36 with 120).
 inline int warps_wanted() { return 24 * sm_count(); }
 
+// Routes of a DOT kernel with half the registers for its sums.  Kernels without
+// them have one form.
+template <bool DOT>
+constexpr int kFew = DOT ? 16 : kMaxK;
+
 template <typename TT, typename TR, int U, bool DOT>
 cudaError_t spread(const Rows& tok, const Rows& dot, const int32_t* slot_of, const float* w, int T, int k, int H,
                    int R, const Rows& out, float* dw, int32_t* status, cudaStream_t st) {
   const int pieces = (H + 255) / 256, want = DOT ? warps_wanted() : 5 * warps_wanted();
   // few tokens: more warps per token, then a token's routes over several CTAs
   const int warps = std::min({kMaxWarps, pieces, (want + T - 1) / T});
-  const int split = static_cast<int>(std::min<int64_t>(k, std::max<int64_t>(1, want / (static_cast<int64_t>(T) * pieces))));
+  const int64_t all = static_cast<int64_t>(T) * pieces;
+  const int split = static_cast<int>(std::min<int64_t>(k, std::max<int64_t>(1, want / all)));
   const int jb = (k + split - 1) / split;
   auto go = [&](auto kern, dim3 grid, int threads) {
     return launch_pdl(kern, grid, dim3(threads), 0, st, static_cast<const TT*>(tok.p), tok.ld,
@@ -255,12 +261,12 @@ cudaError_t spread(const Rows& tok, const Rows& dot, const int32_t* slot_of, con
   };
   if (warps == 1 && split == 1) {
     const dim3 grid((T + kSoloWarps - 1) / kSoloWarps);
-    return DOT && k <= 16 ? go(spread_kernel<TT, TR, U, DOT, DOT ? 16 : 32, true>, grid, kSoloWarps * 32)
-                   : go(spread_kernel<TT, TR, U, DOT, 32, true>, grid, kSoloWarps * 32);
+    return DOT && k <= 16 ? go(spread_kernel<TT, TR, U, DOT, kFew<DOT>, true>, grid, kSoloWarps * 32)
+                          : go(spread_kernel<TT, TR, U, DOT, kMaxK, true>, grid, kSoloWarps * 32);
   }
   const dim3 grid(T, (k + jb - 1) / jb);
-  return DOT && jb <= 16 ? go(spread_kernel<TT, TR, U, DOT, DOT ? 16 : 32, false>, grid, warps * 32)
-                  : go(spread_kernel<TT, TR, U, DOT, 32, false>, grid, warps * 32);
+  return DOT && jb <= 16 ? go(spread_kernel<TT, TR, U, DOT, kFew<DOT>, false>, grid, warps * 32)
+                         : go(spread_kernel<TT, TR, U, DOT, kMaxK, false>, grid, warps * 32);
 }
 
 template <typename TR, typename TO, int U, bool DOT>
@@ -281,12 +287,12 @@ cudaError_t join(const Rows& rows, const Rows& dot, const int32_t* slot_of, cons
   };
   if (warps == 1 && parts == 1) {
     const dim3 grid((T + kSoloWarps - 1) / kSoloWarps);
-    return DOT && k <= 16 ? go(join_kernel<TR, TO, U, DOT, DOT ? 16 : 32, true>, grid, kSoloWarps * 32)
-                   : go(join_kernel<TR, TO, U, DOT, 32, true>, grid, kSoloWarps * 32);
+    return DOT && k <= 16 ? go(join_kernel<TR, TO, U, DOT, kFew<DOT>, true>, grid, kSoloWarps * 32)
+                          : go(join_kernel<TR, TO, U, DOT, kMaxK, true>, grid, kSoloWarps * 32);
   }
   const dim3 grid(T, parts);
-  return DOT && k <= 16 ? go(join_kernel<TR, TO, U, DOT, DOT ? 16 : 32, false>, grid, warps * 32)
-                 : go(join_kernel<TR, TO, U, DOT, 32, false>, grid, warps * 32);
+  return DOT && k <= 16 ? go(join_kernel<TR, TO, U, DOT, kFew<DOT>, false>, grid, warps * 32)
+                        : go(join_kernel<TR, TO, U, DOT, kMaxK, false>, grid, warps * 32);
 }
 
 // f(type tag of a, type tag of b, the unit as an integral constant)

@@ -54,7 +54,8 @@ inline NormPlan norm_plan(int T, int H, int slot, int words, int max_threads) {
 
 inline void plan_steps(NormPlan& p, std::initializer_list<Rows> all) {
   int i = 0;
-  for (const Rows& r : all) p.by[i++] = static_cast<int64_t>(p.grid) * p.groups * r.ld * (r.type == MOE_ROW_F32 ? 4 : 2);
+  const int64_t step = static_cast<int64_t>(p.grid) * p.groups;
+  for (const Rows& r : all) p.by[i++] = step * r.ld * (r.type == MOE_ROW_F32 ? 4 : 2);
 }
 
 // The widest unit of adjacent columns that the width and every row allow.

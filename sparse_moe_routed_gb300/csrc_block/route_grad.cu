@@ -118,8 +118,9 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_tot, u
 // the units of every expert.
 __global__ void __launch_bounds__(kPlanThreads)
     route_plan_kernel(const float* __restrict__ dw, const float* __restrict__ w, const int32_t* __restrict__ ids,
-                      const int32_t* __restrict__ offsets, int T, int k, int E, float* __restrict__ dl, Unit* units_out, Multi* multi_out, int units_max,
-                      int multi_max, int plan, int unit, int32_t* status) {
+                      const int32_t* __restrict__ offsets, int T, int k, int E, float* __restrict__ dl,
+                      Unit* units_out, Multi* multi_out, int units_max, int multi_max, int plan, int unit,
+                      int32_t* status) {
   __shared__ uint64_t warp_tot[32];
   __shared__ int first[kPlanThreads], start[kPlanThreads], count[kPlanThreads], part0[kPlanThreads];
   pdl_wait();
@@ -188,8 +189,8 @@ template <int U, bool DIRECT>
 __global__ void __launch_bounds__(kRowWarps * 32)
     route_rows_kernel(const float* __restrict__ dl, const int32_t* __restrict__ offsets,
                       const int32_t* __restrict__ perm, const bf16_t* __restrict__ x, int64_t ldx, int R, int k, int E,
-                      int H, const Unit* units, int units_max, float* dwr, int64_t ld_dw, float* dbias, float* part_rows,
-                      float* part_bias, int32_t* status) {
+                      int H, const Unit* units, int units_max, float* dwr, int64_t ld_dw, float* dbias,
+                      float* part_rows, float* part_bias, int32_t* status) {
   __shared__ int2 routes[kRowWarps][32];  // token (-1: none) and the bits of dl
   pdl_wait();
   pdl_trigger();
@@ -427,8 +428,8 @@ cudaError_t launch_route_grad(const RouteGradArgs& a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (a.T > 0) {
     const int warps = kPlanThreads / 32, ctas = std::min((a.T + warps - 1) / warps, 4 * sm_count());
-    e = launch_pdl(route_plan_kernel, dim3(ctas + plan), dim3(kPlanThreads), 0, st, a.dw, a.w, a.ids, a.offsets, a.T, a.k,
-                   a.E, a.dlogits, ws.units, ws.multi, units, multi, plan, unit_for(R), a.status);
+    e = launch_pdl(route_plan_kernel, dim3(ctas + plan), dim3(kPlanThreads), 0, st, a.dw, a.w, a.ids, a.offsets, a.T,
+                   a.k, a.E, a.dlogits, ws.units, ws.multi, units, multi, plan, unit_for(R), a.status);
     if (e != cudaSuccess) return e;
   }
   if (a.dx.p != nullptr && a.T > 0) {
