@@ -25,14 +25,15 @@ constexpr int kThreads = 1024;
 template <typename TX, typename TY, int G, int NCH>
 __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     block_norm_kernel(const NormArgs a, const NormPlan p) {
-  constexpr bool STAGED = NCH <= kMaxStagedChunks, BY_WORDS = kByWords<TX, G> || kByWords<TY, G>;
+  constexpr bool STAGED = NCH <= kMaxStagedChunks, BY_CHUNKS = kByChunks<G>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) float red[15][2][16];
   const int nt = p.nt, H = a.H;
   const int group = threadIdx.x / nt, tid = threadIdx.x - group * nt;
   const bool has_y = a.y.p != nullptr, has_n = a.n_out.p != nullptr;
-  // without a block before it y is a row of zeros: its places are never written
-  stage_init(red, smem, !has_y ? p.smem : 0);
+  // zeros where nothing is copied: without a block before it y is a row of
+  // zeros, and chunks end with the row
+  stage_init(red, smem, BY_CHUNKS || !has_y ? p.smem : 0);
   pdl_wait();
   pdl_trigger();
   const bool full = a.gate_kind == MOE_GATE_FULL, token = a.gate_kind == MOE_GATE_TOKEN;
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
   unsigned char* m2 = m1 + NCH * nt * 32;
   auto read_c = [&](const unsigned char* m, int h, V8& f) {
     if (STAGED) {
-      read_staged<float, G>(m, nullptr, h, tid, nt, H, f);
+      read_staged<float, G>(m, nullptr, h, nt, f);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -112,13 +113,13 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     const unsigned char *ax = mx + at, *ay = my + at;
     if (STAGED) {
       if (p.stages == 1) {
-        if (BY_WORDS) group_sync(nt, group);  // the row before has been read
+        if (BY_CHUNKS) group_sync(nt, group);  // the row before has been read
         stage(0);
         copies_wait(0);
-        if (BY_WORDS) group_sync(nt, group);
+        if (BY_CHUNKS) group_sync(nt, group);
       } else {
         copies_wait(p.stages - 2);
-        if (BY_WORDS) group_sync(nt, group);  // this row is there, the one before has been read
+        if (BY_CHUNKS) group_sync(nt, group);  // this row is there, the one before has been read
         stage(at == 0 ? (p.stages - 1) * p.stage : at - p.stage);
       }
       at = at + p.stage == p.stages * p.stage ? 0 : at + p.stage;
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     if (token && t + step < a.T) gt_next = gate_v[t + step];
     auto read_y = [&](int h, V8& f) {
       if (STAGED)
-        read_staged<TY, G>(ay + off_y, y + t * a.y.ld, h, tid, nt, H, f);
+        read_staged<TY, G>(ay + off_y, y + t * a.y.ld, h, nt, f);
       else
         read_global<TY, G>(has_y ? y + t * a.y.ld : y, h, tid, nt, has_y ? H : 0, f);
     };
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
 #pragma unroll
     for (int h = 0; h < NCH; ++h) {
       if (STAGED)
-        read_staged<TX, G>(ax, x + t * a.x.ld, h, tid, nt, H, xo[h]);
+        read_staged<TX, G>(ax, x + t * a.x.ld, h, nt, xo[h]);
       else
         read_global<TX, G>(x + t * a.x.ld, h, tid, nt, H, xo[h]);
       if (NCH > 1) read_y(h, f);
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
       if (full) {
         V8 g;
         if (STAGED)
-          read_staged<TY, G>(ay + off_g, gate + t * a.gate.ld, h, tid, nt, H, g);
+          read_staged<TY, G>(ay + off_g, gate + t * a.gate.ld, h, nt, g);
         else
           read_global<TY, G>(gate + t * a.gate.ld, h, tid, nt, H, g);
         f = f * g;
@@ -189,7 +190,7 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t st) {
   const Rows gate = full ? a.gate : Rows{nullptr, 0, MOE_ROW_F32};
   const int unit = norm_unit(a.H, {a.x, a.y, gate, a.x_out, a.n_out});
   NormPlan p = norm_plan(a.T, a.H, row_bytes8(a.x) + (a.y.type == MOE_ROW_F32 ? 32 : 16) + row_bytes8(gate),
-                         unit == 1 && (a.x.type == MOE_ROW_BF16 || a.y.type == MOE_ROW_BF16) ? 3 : 0, kThreads);
+                         unit == 1 ? 3 : 0, kThreads);
   plan_steps(p, {a.x, a.y, gate, a.x_out, a.n_out});
   return norm_dispatch(a.x.type, a.y.type, unit, p.nch, [&](auto tx, auto ty, auto g, auto n) {
     auto kern = block_norm_kernel<decltype(tx), decltype(ty), decltype(g)::value, decltype(n)::value>;

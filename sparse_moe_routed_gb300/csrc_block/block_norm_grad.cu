@@ -32,14 +32,15 @@ constexpr int kThreads = 640;
 template <typename TX, typename TY, int G, int NCH>
 __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     block_norm_grad_kernel(const NormGradArgs a, const NormPlan p, int want_cols) {
-  constexpr bool STAGED = NCH <= kMaxStagedChunks, BY_WORDS = kByWords<TX, G> || kByWords<TY, G>;
+  constexpr bool STAGED = NCH <= kMaxStagedChunks, BY_CHUNKS = kByChunks<G>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) float red[15][2][16];
   const int nt = p.nt, H = a.H;
   const int group = threadIdx.x / nt, tid = threadIdx.x - group * nt;
   const bool has_d = a.dx_out.p != nullptr, has_n = a.dn.p != nullptr, has_y = a.y.p != nullptr;
-  // an absent gradient is a row of zeros: its places are never written
-  stage_init(red, smem, !has_d || !has_n ? p.smem : 0);
+  // zeros where nothing is copied: an absent gradient is a row of zeros, and
+  // chunks end with the row
+  stage_init(red, smem, BY_CHUNKS || !has_d || !has_n ? p.smem : 0);
   pdl_wait();
   pdl_trigger();
   const bool full = a.gate_kind == MOE_GATE_FULL, token = a.gate_kind == MOE_GATE_TOKEN;
@@ -59,7 +60,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
   unsigned char* m2 = m1 + NCH * nt * 32;
   auto read_c = [&](const unsigned char* m, int h, V8& f) {
     if (STAGED) {
-      read_staged<float, G>(m, nullptr, h, tid, nt, H, f);
+      read_staged<float, G>(m, nullptr, h, nt, f);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -156,13 +157,13 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     const unsigned char *ax = mx + at, *ay = my + at;
     if (STAGED) {
       if (p.stages == 1) {
-        if (BY_WORDS) group_sync(nt, group);  // the row before has been read
+        if (BY_CHUNKS) group_sync(nt, group);  // the row before has been read
         stage(0);
         copies_wait(0);
-        if (BY_WORDS) group_sync(nt, group);
+        if (BY_CHUNKS) group_sync(nt, group);
       } else {
         copies_wait(p.stages - 2);
-        if (BY_WORDS) group_sync(nt, group);  // this row is there, the one before has been read
+        if (BY_CHUNKS) group_sync(nt, group);  // this row is there, the one before has been read
         stage(at == 0 ? (p.stages - 1) * p.stage : at - p.stage);
       }
       at = at + p.stage == p.stages * p.stage ? 0 : at + p.stage;
@@ -171,13 +172,13 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     factors(t + step);
     auto read_x = [&](int off, const TX* q, int64_t ld, int h, V8& f) {
       if (STAGED)
-        read_staged<TX, G>(ax + off, q + t * ld, h, tid, nt, H, f);
+        read_staged<TX, G>(ax + off, q + t * ld, h, nt, f);
       else
         read_global<TX, G>(q == nullptr ? q : q + t * ld, h, tid, nt, q == nullptr ? 0 : H, f);
     };
     auto read_y = [&](int off, const TY* q, int64_t ld, int h, V8& f) {
       if (STAGED)
-        read_staged<TY, G>(ay + off, q + t * ld, h, tid, nt, H, f);
+        read_staged<TY, G>(ay + off, q + t * ld, h, nt, f);
       else
         read_global<TY, G>(q == nullptr ? q : q + t * ld, h, tid, nt, q == nullptr ? 0 : H, f);
     };
@@ -336,8 +337,7 @@ cudaError_t launch_block_norm_grad(const NormGradArgs& a, cudaStream_t st) {
     const int sx = a.dx.type == MOE_ROW_F32 ? 32 : 16, sy = a.y.type == MOE_ROW_F32 ? 32 : 16;
     const int slot = 2 * sx + sy + row_bytes8(a.y) + row_bytes8(gate);
     const int unit = norm_unit(a.H, {a.dx_out, a.x_out, a.dn, a.y, gate, dgate, a.dx, a.dy});
-    const bool bf16 = a.dx.type == MOE_ROW_BF16 || a.y.type == MOE_ROW_BF16;
-    NormPlan p = norm_plan(a.T, a.H, slot, unit == 1 && bf16 ? 5 : 0, kThreads);
+    NormPlan p = norm_plan(a.T, a.H, slot, unit == 1 ? 5 : 0, kThreads);
     p.grid = std::min(p.grid, sm_count());
     const int cols = p.nch <= kMaxStagedChunks ? (p.groups - 1) * 2 * p.nch * 8 * p.nt * 4 : 2 * p.nch * 8 * p.nt * 4;
     p.smem = std::max(p.smem, cols);  // the sums' join takes the stages' place

@@ -27,12 +27,19 @@ namespace blk {
 
 namespace {
 
-// Routes whose loads a thread has in flight: a lone warp per token wants eight
+// Routes whose loads a thread has in flight.  A lone warp per token wants eight
 // (collect's gradient at 16,384 tokens: 269 us against 273 with four), CTAs of
 // several warps are better off with four and twice the CTAs per SM (dispatch's
-// gradient at 2,048 tokens: 24.7 against 33.2 us, 1,024: 14.9 against 20.0).
-template <bool SOLO>
-constexpr int kBatch = SOLO ? 8 : 4;
+// gradient at 2,048 tokens: 24.7 against 33.2 us).  fp32 rows, and single
+// elements, need twice the registers for a route: half of each, or what the
+// launch bounds leave spills (dispatch's gradient of fp32 rows, 4,096 tokens:
+// 83.7 us with four, 128 with eight; 1,024 tokens: 25.4 with two, 29.8 with
+// four, but collect without dw 20.2 with four, 21.4 with two; of odd bf16 rows,
+// 4,096 tokens: 86.3 us with two, 110 with four).
+template <bool SOLO, bool DOT, typename TR, int U>
+constexpr int kBatch = sizeof(TR) == 2 && U > 1 ? (SOLO ? 8 : 4)
+                       : sizeof(TR) == 4 && SOLO ? 4
+                                                 : (DOT ? 2 : 4);
 constexpr int kMaxWarps = 16;  // warps per CTA
 
 // Sums of eight values over the warp, each lane giving its eight: lane l
@@ -110,6 +117,7 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
   __shared__ float red[DOT ? (SOLO ? kSoloWarps : kMaxWarps) : 1][kMaxK];
   pdl_wait();
   pdl_trigger();
+  constexpr int B = kBatch<SOLO, DOT, TR, U>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = SOLO ? 1 : blockDim.x >> 5;
   const int tid = SOLO ? lane : threadIdx.x;
   const int64_t t = SOLO ? static_cast<int64_t>(blockIdx.x) * kSoloWarps + warp : blockIdx.x;
@@ -133,13 +141,13 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
     load8<U>(row, c, H, xr);
     const V8 x = unpack(xr);
 #pragma unroll
-    for (int b = 0; b < NK / kBatch<SOLO>; ++b) {
-      if (b * kBatch<SOLO> >= n) break;
-      Raw8<TR> v[DOT ? kBatch<SOLO> : 1];
+    for (int b = 0; b < NK / B; ++b) {
+      if (b * B >= n) break;
+      Raw8<TR> v[DOT ? B : 1];
       if (DOT) {
 #pragma unroll
-        for (int u = 0; u < kBatch<SOLO>; ++u) {
-          const int j = b * kBatch<SOLO> + u;
+        for (int u = 0; u < B; ++u) {
+          const int j = b * B + u;
           const int64_t s = j < n ? sh.at[j] : -1;
           if (s >= 0)
             load8<U>(dot + s * ld_dot, c, H, v[DOT ? u : 0]);
@@ -148,8 +156,8 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
         }
       }
 #pragma unroll
-      for (int u = 0; u < kBatch<SOLO>; ++u) {
-        const int j = b * kBatch<SOLO> + u;
+      for (int u = 0; u < B; ++u) {
+        const int j = b * B + u;
         const int64_t s = j < n ? sh.at[j] : -1;
         if (s < 0) continue;
         if (DOT) {
@@ -175,6 +183,7 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
   __shared__ float red[DOT ? (SOLO ? kSoloWarps : kMaxWarps) : 1][kMaxK];
   pdl_wait();
   pdl_trigger();
+  constexpr int B = kBatch<SOLO, DOT, TR, U>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = SOLO ? 1 : blockDim.x >> 5;
   const int tid = SOLO ? lane : threadIdx.x;
   const int64_t t = SOLO ? static_cast<int64_t>(blockIdx.x) * kSoloWarps + warp : blockIdx.x;
@@ -198,12 +207,12 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
       x = unpack(xr);
     }
 #pragma unroll
-    for (int b = 0; b < NK / kBatch<SOLO>; ++b) {
-      if (b * kBatch<SOLO> >= k) break;
-      Raw8<TR> v[kBatch<SOLO>];
+    for (int b = 0; b < NK / B; ++b) {
+      if (b * B >= k) break;
+      Raw8<TR> v[B];
 #pragma unroll
-      for (int u = 0; u < kBatch<SOLO>; ++u) {
-        const int j = b * kBatch<SOLO> + u;
+      for (int u = 0; u < B; ++u) {
+        const int j = b * B + u;
         const int64_t s = j < k ? sh.at[j] : -1;
         if (s >= 0)
           load8<U>(rows + s, c, H, v[u]);
@@ -211,8 +220,8 @@ __global__ void __launch_bounds__(SOLO ? kSoloWarps * 32 : kMaxWarps * 32, SOLO 
           raw_zero(v[u]);
       }
 #pragma unroll
-      for (int u = 0; u < kBatch<SOLO>; ++u) {
-        const int j = b * kBatch<SOLO> + u;
+      for (int u = 0; u < B; ++u) {
+        const int j = b * B + u;
         if (j >= k || sh.at[j] < 0) continue;
         const V8 y = unpack(v[u]);
         acc = fma8(y, sh.w[j], acc);

@@ -11,7 +11,7 @@ namespace moe {
 namespace blk {
 
 constexpr int kMaxGroupThreads = 512;      // threads of a row's group, 8 * nch columns each
-constexpr int kNormSmem = 224 * 1024;      // dynamic shared memory per CTA (227 KB with the kernels' own)
+constexpr int kNormSmem = 224 * 1024 + 256;      // dynamic shared memory per CTA (227 KB with the kernels' own)
 constexpr int kMaxStages = 2;              // rows staged per group (3: gradient 46.5 us, not 43.4, at 4,096 x 2,560)
 constexpr int kMaxStagedChunks = 2;        // wider rows (H > 8192) are read without staging
 
@@ -23,13 +23,13 @@ struct NormPlan {
   int64_t by[8];  // bytes from a group's row to its next, per operand
 };
 
-// slot: bytes per thread of all operands' eight columns; words: how many
-// operands are staged by words at most (kByWords); max_threads: threads per CTA
-// where a thread has eight columns.  One CTA per SM walks the rows (more where
+// slot: bytes per thread of all operands' eight columns; chunked: how
+// many operands are staged by chunks at most (kByChunks); max_threads: threads
+// per CTA where a thread has eight columns.  One CTA per SM walks the rows (more where
 // CTAs are small): a row's two sums put two barriers between its reads and its
 // writes, so the copies of the rows ahead, not more threads, keep the memory
 // busy.
-inline NormPlan norm_plan(int T, int H, int slot, int words, int max_threads) {
+inline NormPlan norm_plan(int T, int H, int slot, int chunked, int max_threads) {
   NormPlan p;
   const int chunks = (H + 7) / 8;
   p.nch = chunks <= kMaxGroupThreads ? 1 : chunks <= 2 * kMaxGroupThreads ? 2 : 4;
@@ -38,7 +38,7 @@ inline NormPlan norm_plan(int T, int H, int slot, int words, int max_threads) {
   const int sms = sm_count();
   p.groups = std::max(1, std::min(p.nt == 32 ? 32 : 15, max_threads / p.nt));
   p.groups = std::max(1, std::min(p.groups, (T + sms - 1) / sms));
-  p.stage = p.nch <= kMaxStagedChunks ? slot * p.nch * p.nt + 16 * words : 0;
+  p.stage = p.nch <= kMaxStagedChunks ? slot * p.nch * p.nt + 16 * chunked : 0;
   p.gains = p.nch <= kMaxStagedChunks ? 2 * 32 * p.nch * p.nt : 0;
   const int room = kNormSmem - p.gains;
   while (p.groups > 1 && p.stage * p.groups * 2 > room) --p.groups;

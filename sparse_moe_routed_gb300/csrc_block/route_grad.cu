@@ -36,7 +36,10 @@ namespace {
 // 256; 16,384 tokens 101 with 256, 120 with 128.
 inline int unit_for(int R) { return R <= 10000 ? 64 : R <= 100000 ? 128 : 256; }
 constexpr int kPlanThreads = 1024;  // >= kMaxE
-constexpr int kBatch = 8;           // rows whose loads a thread has in flight
+// Rows whose loads a thread has in flight (single elements need eight registers
+// a row: 134 us with four, 166 with eight at 4,096 tokens).
+template <int U>
+constexpr int kBatch = U == 1 ? 4 : 8;
 constexpr int kRowWarps = 4;        // warps per CTA of the row sums
 
 // A unit: n routes of expert e (-1: no unit) from slot s0 on; part is where
@@ -235,19 +238,19 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     next = fetch(i0 + 32 + lane);
     if (dwr == nullptr) continue;
 #pragma unroll 1
-    for (int j0 = 0; j0 < 32 && valid >> j0 != 0; j0 += kBatch) {
-      Raw8<bf16_t> v[kBatch];
-      float w[kBatch];
-      if (whole && (~(valid >> j0) & ((1u << kBatch) - 1)) == 0) {  // the usual batch: nothing to test per row
+    for (int j0 = 0; j0 < 32 && valid >> j0 != 0; j0 += kBatch<U>) {
+      Raw8<bf16_t> v[kBatch<U>];
+      float w[kBatch<U>];
+      if (whole && (~(valid >> j0) & ((1u << kBatch<U>) - 1)) == 0) {  // the usual batch: nothing to test per row
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
+        for (int b = 0; b < kBatch<U>; ++b) {
           const int2 rt = routes[warp][j0 + b];
           w[b] = __int_as_float(rt.y);
           load_vec(x + rt.x * ldx + c.first, v[b]);
         }
       } else {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
+        for (int b = 0; b < kBatch<U>; ++b) {
           const int2 rt = routes[warp][j0 + b];
           w[b] = __int_as_float(rt.y);
           if (rt.x >= 0)
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
         }
       }
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) acc = fma8(unpack(v[b]), w[b], acc);
+      for (int b = 0; b < kBatch<U>; ++b) acc = fma8(unpack(v[b]), w[b], acc);
     }
   }
   if (dbias != nullptr && blockIdx.y == 0) {

@@ -45,38 +45,42 @@ __device__ __forceinline__ int col0(int h, int i, int tid, int nt) {
   return (h * (8 / G) + i / G) * nt * G + tid * G + i % G;
 }
 
-// bf16 rows that start on any element (G = 1) cannot be copied column by
-// column: a copy has four bytes.  Their group copies the aligned words that
-// hold the row instead, into the row's region of shared memory from its start
-// on, and after a barrier a thread reads its columns from there, one element
-// on where the row starts in the middle of a word.  The first and the last
-// word may hold an element that is not the row's, which nothing uses; a word
-// that holds one byte of an allocation lies inside it.
-template <typename T, int G>
-constexpr bool kByWords = G * sizeof(T) < 4;
+// Rows that start on any element (G = 1) would take many narrow copies that
+// way, and bf16 ones none at all (a copy has four bytes at least).  Their group
+// copies the aligned 16-byte chunks that hold the
+// row instead, into the operand's region of shared memory from its start on,
+// and after a barrier a thread reads its columns from there, as many bytes on
+// as the row starts behind its first chunk.  What the first chunk holds in
+// front of the row is read, but not used; a chunk that holds one byte of an
+// allocation lies inside it.
+template <int G>
+constexpr bool kByChunks = G == 1;
 
 // Bytes of one operand's row in a stage.
 template <typename T, int G, int NCH>
 __device__ __forceinline__ int region(int nt) {
-  return NCH * nt * kSlot<T> + (kByWords<T, G> ? 16 : 0);
+  return NCH * nt * kSlot<T> + (kByChunks<G> ? 16 : 0);
 }
 
 // A thread's share of a row into the operand's region, columns past H as
-// zeros (by words: as anything).  src: the thread's first column of the row;
-// at: its first place.
+// zeros.  src: the thread's first column of the row; at: its first place.
 template <typename T, int G, int NCH>
 __device__ __forceinline__ void stage_row(unsigned char* at, const T* src, int tid, int nt, int H) {
   constexpr int UB = G * static_cast<int>(sizeof(T));  // bytes of one unit of G columns
-  if constexpr (kByWords<T, G>) {
-    const uintptr_t row = reinterpret_cast<uintptr_t>(src - tid), from = row & ~static_cast<uintptr_t>(3);
-    const int words = (static_cast<int>(row - from) + 2 * H + 3) / 4;
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(at)) - 2 * tid;
-    for (int w = tid; w < words; w += nt) copy_async<4>(to + 4 * w, reinterpret_cast<const void*>(from + 4 * w), 4);
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(at));
+  if constexpr (kByChunks<G>) {
+    const uintptr_t row = reinterpret_cast<uintptr_t>(src - tid * G), from = row & ~static_cast<uintptr_t>(15);
+    const int end = static_cast<int>(row - from) + H * static_cast<int>(sizeof(T));  // of the row in its region
+    // two chunks of zeros more: the row before may have ended that far on
+    const int chunks = min(NCH * nt * kSlot<T> / 16 + 1, (end + 15) / 16 + 2);
+    for (int w = tid; w < chunks; w += nt) {
+      const int have = max(0, min(16, end - 16 * w));
+      copy_async<16>(to - tid * UB + 16 * w, reinterpret_cast<const void*>(have > 0 ? from + 16 * w : from), have);
+    }
   } else {
 #pragma unroll
     for (int p = 0; p < NCH * 8 / G; ++p)
-      copy_async<UB>(static_cast<uint32_t>(__cvta_generic_to_shared(at)) + p * nt * UB, src + p * nt * G,
-                     (p * nt + tid) * G < H ? UB : 0);
+      copy_async<UB>(to + p * nt * UB, src + p * nt * G, (p * nt + tid) * G < H ? UB : 0);
   }
 }
 
@@ -107,21 +111,16 @@ __device__ __forceinline__ void read_unit(const unsigned char* at, int p, V8& f)
 }
 
 // Chunk h of the thread's columns; at: its first place, row: where the row
-// starts in global memory (by words only).
+// starts in global memory (by chunks only; null: in the region's first byte).
 template <typename T, int G>
-__device__ __forceinline__ void read_staged(const unsigned char* at, const T* row, int h, int tid, int nt, int H,
-                                            V8& f) {
+__device__ __forceinline__ void read_staged(const unsigned char* at, const T* row, int h, int nt, V8& f) {
   constexpr int UB = G * static_cast<int>(sizeof(T));
-  if (kByWords<T, G>) at += reinterpret_cast<uintptr_t>(row) & 2;
+  if (kByChunks<G>) at += reinterpret_cast<uintptr_t>(row) & 15;
 #pragma unroll
-  for (int p = 0; p < 8 / G; ++p) {
-    const int u = (h * (8 / G) + p) * nt;
-    read_unit<T, G>(at + u * UB, p, f);
-    if (kByWords<T, G> && u + tid >= H) el(f, p) = 0.f;
-  }
+  for (int p = 0; p < 8 / G; ++p) read_unit<T, G>(at + (h * (8 / G) + p) * nt * UB, p, f);
 }
 
-// The group's threads meet (staging by words).
+// The group's threads meet (staging by chunks).
 __device__ __forceinline__ void group_sync(int nt, int group) {
   if (nt == 32)
     __syncwarp();
