@@ -210,7 +210,7 @@ def _gate(fn, dev, gate, name, T, H, dtype, kind=None):
     if kind is None:
         if gate.dim() == 1:
             kind = MOE_GATE_CHANNEL
-        elif gate.dim() == 2 and gate.shape[1] == 1 and gate.dtype is torch.float32:
+        elif gate.shape[1:] == (1,) and gate.dtype is torch.float32 and (H > 1 or dtype is not torch.float32):
             kind = MOE_GATE_TOKEN
         else:
             kind = MOE_GATE_FULL

@@ -143,7 +143,7 @@ def norm_grad(dx_out, dn, x_out, y, gate, gamma_post, gamma_pre, scale, r1, r2, 
     pb = (Db + 6 * U * D.abs()) * z.abs()
     if gate.dim() == 1:
         got["dgate"] = out(p.sum(0), pb.sum(0) + (T + 6) * U * p.abs().sum(0), torch.float32)
-    elif gate.shape[1] == 1:
+    elif gate.shape[1] == 1 and gate.dtype != torch.bfloat16:  # bf16: a full gate of width 1
         s = p.sum(1, keepdim=True)
         got["dgate"] = out(s, pb.sum(1, keepdim=True) + (H + 6) * U * p.abs().sum(1, keepdim=True), torch.float32)
     else:

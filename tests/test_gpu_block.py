@@ -300,6 +300,13 @@ def test_block_norm_gates(gate, post, types, T, H):
     norm_case(T, H, (types[1], types[0]), gate, post, 0, 0, seed=T + H, scale=1.0, gammas=H % 2 == 0)
 
 
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("types", TYPES, ids=str)
+def test_block_norm_width_one(gate, types):
+    """A [T, 1] gate is the full one where its type is y's."""
+    norm_case(20, 1, types, gate, True, 3, 1, seed=4)
+
+
 def test_block_norm_small_rows_with_eps_zero():
     """Rows of 1e-15 with eps = 0: factors of 1e15, whose cube fp32 cannot hold."""
     g = gen(2)
