@@ -80,11 +80,15 @@ def _matrix(fn, t, name):
     """(rows, width, type, GPU) of the matrix that the others are measured by."""
     if t.dim() != 2:
         _no(fn, MOE_ESHAPE, f"{name} must be two-dimensional")
+    n, H = t.shape
+    return n, H, _type(fn, t, name), t.get_device()
+
+
+def _type(fn, t, name):
     ty = _TYPES.get(t.dtype)
     if ty is None:
         _no(fn, MOE_EINVAL, f"{name} has type {t.dtype}, expected float32 or bfloat16")
-    n, H = t.shape
-    return n, H, ty, t.get_device()
+    return ty
 
 
 def _tensor_no(fn, dev, t, name, shape, dtype):
@@ -136,11 +140,16 @@ def _routes(fn, dev, inv_perm, T, name="inv_perm"):
     return k, _flat(fn, dev, inv_perm, name, (T, k), torch.int32)
 
 
+_functions = {}
+
+
 def _issue(fn, dev, stream, args):
     """The C call with the GPU of its tensors current, on `stream` or that GPU's current stream."""
-    f = getattr(load(), fn)
+    f = _functions.get(fn)
+    if f is None:
+        f = _functions[fn] = getattr(load(), fn)
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         st = f(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -154,7 +163,7 @@ def moe_dispatch(x, inv_perm, x_perm, w=None, dev_status=None, stream=None):
     fn = "moe_dispatch"
     T, H, ty, dev = _matrix(fn, x, "x")
     k, inv = _routes(fn, dev, inv_perm, T)
-    R = _matrix(fn, x_perm, "x_perm")[0]
+    R = len(x_perm)
     px, ldx = _rows(fn, dev, x, "x", T, H, x.dtype)
     pp, ldp = _rows(fn, dev, x_perm, "x_perm", R, H, x.dtype)
     _issue(fn, dev, stream, (px, ldx, ty, inv, _flat(fn, dev, w, "w", (T, k)), T, k, H, R, pp, ldp,
@@ -166,7 +175,7 @@ def moe_dispatch_backward(dx_perm, inv_perm, dx, w=None, x=None, dw=None, add=No
     fn = "moe_dispatch_backward"
     T, H, dty, dev = _matrix(fn, dx, "dx")
     k, inv = _routes(fn, dev, inv_perm, T)
-    R, _, ty, _ = _matrix(fn, dx_perm, "dx_perm")
+    R, ty = len(dx_perm), _type(fn, dx_perm, "dx_perm")
     pp, ldp = _rows(fn, dev, dx_perm, "dx_perm", R, H, dx_perm.dtype)
     px, ldx = _rows(fn, dev, x, "x", T, H, dx_perm.dtype)
     pd, ldd = _rows(fn, dev, dx, "dx", T, H, dx.dtype)
@@ -181,7 +190,7 @@ def moe_collect(y_perm, inv_perm, w, out, add=None, dev_status=None, stream=None
     fn = "moe_collect"
     T, H, oty, dev = _matrix(fn, out, "out")
     k, inv = _routes(fn, dev, inv_perm, T)
-    R, _, ty, _ = _matrix(fn, y_perm, "y_perm")
+    R, ty = len(y_perm), _type(fn, y_perm, "y_perm")
     pp, ldp = _rows(fn, dev, y_perm, "y_perm", R, H, y_perm.dtype)
     po, ldo = _rows(fn, dev, out, "out", T, H, out.dtype)
     pa, lda = _rows(fn, dev, add, "add", T, H, out.dtype)
@@ -194,7 +203,7 @@ def moe_collect_backward(dout, y_perm, inv_perm, w, dy_perm, dw=None, dev_status
     fn = "moe_collect_backward"
     T, H, oty, dev = _matrix(fn, dout, "dout")
     k, inv = _routes(fn, dev, inv_perm, T)
-    R, _, ty, _ = _matrix(fn, dy_perm, "dy_perm")
+    R, ty = len(dy_perm), _type(fn, dy_perm, "dy_perm")
     po, ldo = _rows(fn, dev, dout, "dout", T, H, dout.dtype)
     py, ldy = _rows(fn, dev, y_perm, "y_perm", R, H, dy_perm.dtype)
     pd, ldd = _rows(fn, dev, dy_perm, "dy_perm", R, H, dy_perm.dtype)
@@ -234,7 +243,7 @@ def moe_block_norm(x, y, x_out, n_out, gamma_post=None, gamma_pre=None, gate=Non
     act = y if y is not None else n_out
     if act is None:
         _no(fn, MOE_EINVAL, "y and n_out are both None")
-    yty, yt = _matrix(fn, act, "y" if y is not None else "n_out")[2], act.dtype
+    yty, yt = _type(fn, act, "y" if y is not None else "n_out"), act.dtype
     px, ldx = _rows(fn, dev, x, "x", T, H, x.dtype)
     py, ldy = _rows(fn, dev, y, "y", T, H, yt)
     kind, pg, ldg = _gate(fn, dev, gate, "gate", T, H, yt)
@@ -263,7 +272,7 @@ def moe_block_norm_backward(dx_out, dn, x_out, y, dx, dy, workspace, gamma_post=
     act = y if y is not None else dn
     if act is None:
         _no(fn, MOE_EINVAL, "y and dn are both None")
-    xt, yty, yt = dx.dtype, _matrix(fn, act, "y" if y is not None else "dn")[2], act.dtype
+    xt, yty, yt = dx.dtype, _type(fn, act, "y" if y is not None else "dn"), act.dtype
     pdo, lddo = _rows(fn, dev, dx_out, "dx_out", T, H, xt)
     pdn, lddn = _rows(fn, dev, dn, "dn", T, H, yt)
     px, ldx = _rows(fn, dev, x_out, "x_out", T, H, xt)
@@ -295,13 +304,13 @@ def moe_route_backward(dw, topk_w, topk_ids, x, w_router, offsets, perm, dlogits
     fn = "moe_route_backward"
     i32 = torch.int32
     T, H, _, dev = _matrix(fn, x, "x")
-    E = _matrix(fn, w_router, "w_router")[0]
+    E = len(w_router)
     k, ids = _routes(fn, dev, topk_ids, T, "topk_ids")
     px, ldx = _rows(fn, dev, x, "x", T, H, torch.bfloat16)
     pr, ldr = _rows(fn, dev, w_router, "w_router", E, H, torch.bfloat16)
     dty, pd, ldd, pa, lda = MOE_ROW_F32, None, 0, None, 0
     if dx is not None:
-        dty = _matrix(fn, dx, "dx")[2]
+        dty = _type(fn, dx, "dx")
         pd, ldd = _rows(fn, dev, dx, "dx", T, H, dx.dtype)
         pa, lda = _rows(fn, dev, add, "add", T, H, dx.dtype)
     elif add is not None:
