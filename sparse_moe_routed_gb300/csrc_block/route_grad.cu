@@ -34,7 +34,7 @@ namespace {
 // 512 experts, width 2,560, zipf 1 popularity: 512 tokens 13.7 us with units
 // of 64, 16.1 with 128; 4,096 tokens 37.1 with 128, 40.7 with 64 and with
 // 256; 16,384 tokens 101 with 256, 120 with 128.
-inline int unit_for(int R) { return R <= 10000 ? 64 : R <= 100000 ? 128 : 256; }
+inline int unit_for(int R) { return R <= 16000 ? 64 : R <= 100000 ? 128 : 256; }
 constexpr int kPlanThreads = 1024;  // >= kMaxE
 // Rows whose loads a thread has in flight (single elements need eight registers
 // a row: 134 us with four, 166 with eight at 4,096 tokens).
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                       Unit* units_out, Multi* multi_out, int units_max, int multi_max, int plan, int unit,
                       int32_t* status) {
   __shared__ uint64_t warp_tot[32];
-  __shared__ int first[kPlanThreads], start[kPlanThreads], count[kPlanThreads], part0[kPlanThreads];
+  __shared__ int start[kPlanThreads], count[kPlanThreads], part0[kPlanThreads];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31;
@@ -141,29 +141,30 @@ __global__ void __launch_bounds__(kPlanThreads)
                                        (several ? static_cast<uint64_t>(units) << 26 | 1ull << 53 : 0ull),
                                    warp_tot, total);
     const int p0 = static_cast<int>(at >> 26 & 0x7ffffff), m0 = static_cast<int>(at >> 53);
-    first[tid] = static_cast<int>(at & 0x3ffffff);
+    const int all = static_cast<int>(total & 0x3ffffff), shared = static_cast<int>(total >> 26 & 0x7ffffff);
+    // the units of experts with several come first: they are the long ones,
+    // and what starts last should be short
+    part0[tid] = p0;
     start[tid] = a;
     count[tid] = n;
-    part0[tid] = several ? p0 : -1;
-    if (several) multi_out[m0] = {tid, p0, units, 0};
+    if (several)
+      multi_out[m0] = {tid, p0, units, 0};
+    else if (units == 1)
+      units_out[shared + static_cast<int>(at & 0x3ffffff) - p0] = {tid, a, n, -1};
     for (int i = static_cast<int>(total >> 53) + tid; i < multi_max; i += kPlanThreads) multi_out[i] = {0, 0, 0, 0};
+    for (int u = all + tid; u < units_max; u += kPlanThreads) units_out[u] = {-1, 0, 0, -1};
     __syncthreads();
-    const int units_all = static_cast<int>(total & 0x3ffffff);
-    for (int u = tid; u < units_max; u += kPlanThreads) {
-      Unit d = {-1, 0, 0, -1};
-      if (u < units_all) {
-        int lo = 0, hi = E;  // the expert whose first unit is the last at or before u
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) / 2;
-          if (first[mid] <= u)
-            lo = mid;
-          else
-            hi = mid;
-        }
-        const int i = u - first[lo];
-        d = {lo, start[lo] + i * unit, min(unit, count[lo] - i * unit), part0[lo] < 0 ? -1 : part0[lo] + i};
+    for (int u = tid; u < shared; u += kPlanThreads) {
+      int lo = 0, hi = E;  // the last expert whose first partial row is at or before u
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (part0[mid] <= u)
+          lo = mid;
+        else
+          hi = mid;
       }
-      units_out[u] = d;
+      const int i = u - part0[lo];
+      units_out[u] = {lo, start[lo] + i * unit, min(unit, count[lo] - i * unit), u};
     }
     if (tid == 0 && bad) set_status(status, MOE_DEV_BAD_EXPERT);
     return;
