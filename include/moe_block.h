@@ -9,13 +9,13 @@
  * *dev_status, which may be NULL here), with these additions:
  *  - Rows may be fp32 or bf16 (moe_row_type) and may be strided: row i of a
  *    matrix starts ld * i ELEMENTS after its pointer, its elements are
- *    adjacent, and ld >= the row's width.  Columns between rows are neither
- *    read nor written.
+ *    adjacent, and ld >= the row's width.  Columns between rows are not
+ *    written, and no result depends on them (a norm's rows on odd elements are
+ *    read in aligned 16-byte pieces, which may begin before the row).
  *  - Any width 1 <= H <= 65536 (the norms: 16384) and any alignment that the
- *    element type has by itself.  Rows that start on 8-element boundaries
- *    (bf16: pointer % 16 == 0, fp32: pointer % 32 == 0, ld % 8 == 0) move in
- *    16 and 32 byte pieces, others element by element; the norms also take
- *    units of 4 and 2 elements, where these divide H and all rows allow it.
+ *    element type has by itself.  Fastest are rows that start on 8-element
+ *    boundaries (bf16: pointer % 16 == 0, fp32: pointer % 32 == 0, ld % 8 == 0),
+ *    then rows that start on even elements.
  *  - Every sum, norm factor, product and gradient is computed in fp32 in a
  *    fixed order: the same bits on every call.  A bf16 output is rounded once.
  *  - Outputs must not overlap inputs or one another, except where a call

@@ -19,7 +19,7 @@ import torch
 
 from . import _lib
 from . import build as _build
-from ._lib import MOE_EINVAL, MOE_ESHAPE, MOE_OK, MoEError
+from ._lib import MOE_EINVAL, MOE_ENOTSUP, MOE_ESHAPE, MOE_OK, MoEError
 
 MOE_ROW_F32, MOE_ROW_BF16 = 0, 1
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = range(4)
@@ -105,6 +105,8 @@ def _rows(fn, dev, t, name, n, H, dtype):
         return None, 0
     if t.get_device() != dev or t.dtype is not dtype or t.shape != (n, H) or dev < 0:
         _tensor_no(fn, dev, t, name, (n, H), dtype)
+    if n > 0x7fffffff or H > 0x7fffffff:
+        _no(fn, MOE_ENOTSUP, f"{name} has shape {(n, H)}: sizes are 32-bit")
     ld, step = t.stride()
     if step != 1 and H > 1:
         _no(fn, MOE_EINVAL, f"{name}: the elements of a row must be adjacent")

@@ -10,11 +10,14 @@
 // per-channel dgate = (1 + gamma_post) A, and B = sum_t dn xh is dgamma_pre:
 // two accumulators per column, whatever the gate.
 //
-// Bound by HBM: four rows in, two out.  A group of threads owns a row, the
-// rows ahead are staged in shared memory (stage.cuh) and read from there again
-// in each of the row's three steps, which leaves the registers to D and the
-// column sums.  One CTA per SM keeps A and B over all its rows and writes one
-// partial row of each; a second launch adds these in order.
+// Bound by HBM: four rows in, two out.  A group of threads owns a row, the row
+// ahead is staged in shared memory (stage.cuh); where a thread has eight
+// columns it holds the normalised rows between the row's three steps, else it
+// reads the stage again.  One CTA per SM keeps A and B over all its rows and
+// writes one partial row of each; a second launch adds these in order.  fp32
+// stream, bf16 block, width 2,560: 39 us at 4,096 rows (72 % of the measured
+// copy rate), 118 us at 16,384 (94 %): 6.5 ns a row and 10 us of start, column
+// sums and second launch.
 #include <math.h>
 
 #include "norm.h"

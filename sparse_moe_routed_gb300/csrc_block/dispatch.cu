@@ -16,6 +16,9 @@
 // slots to its dw.  With few, the warps of a CTA share a token's pieces (and
 // CTAs its routes or columns), and dw adds the warps' sums in order.  dw needs
 // no atomics in either form, and the token's row is read once whatever k is.
+// Top 10, width 2,560, bf16: dispatch 36 us (90 % of the measured copy rate) and
+// its gradient with dw 50 us (78 %) at 4,096 tokens, collect's gradient 270 us
+// (96 %) at 16,384; of fp32 rows dispatch's gradient 84 us (96 %) at 4,096.
 #include <algorithm>
 #include <type_traits>
 

@@ -31,9 +31,10 @@ namespace {
 
 // Routes per unit: short units keep few routes from waiting on one warp's
 // long chain, long ones save partial rows.  Per call with dx NULL, top 10 of
-// 512 experts, width 2,560, zipf 1 popularity: 512 tokens 13.7 us with units
-// of 64, 16.1 with 128; 4,096 tokens 37.1 with 128, 40.7 with 64 and with
-// 256; 16,384 tokens 101 with 256, 120 with 128.
+// 512 experts, width 2,560, popularity 1 / rank: 512 tokens 13.7 us with units
+// of 64, 13.8 with 32, 16.0 with 128; 1,024 tokens 16.9 with 64, 19.2 with 128;
+// 4,096 tokens 36.2 with 128, 39.3 with 64, 39.9 with 256; 16,384 tokens 95
+// with 256, 120 with 128.
 inline int unit_for(int R) { return R <= 16000 ? 64 : R <= 100000 ? 128 : 256; }
 constexpr int kPlanThreads = 1024;  // >= kMaxE
 // Rows whose loads a thread has in flight (single elements need eight registers

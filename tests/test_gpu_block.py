@@ -553,6 +553,8 @@ def test_refusals_of_the_binding():
     refused(_lib.MOE_ESHAPE, M.moe_dispatch, x, inv[:3], xp)
     refused(_lib.MOE_ESHAPE, M.moe_dispatch, x, inv, xp[:, :60])
     refused(_lib.MOE_ESHAPE, M.moe_dispatch, x, inv, xp[:1].expand(8, 64))
+    # more rows than the C ABI's int holds (one row in memory, seen 2^32 + 8 times)
+    refused(_lib.MOE_ENOTSUP, M.moe_dispatch, x, inv, xp[:1].expand((1 << 32) + 8, 64))
     refused(_lib.MOE_ESHAPE, M.moe_dispatch, x, inv, xp, w=torch.zeros((4, 3), device=DEV))
     refused(_lib.MOE_EINVAL, M.moe_dispatch, x, inv, xp, w=torch.zeros((2, 4), device=DEV).t())
     refused(_lib.MOE_EINVAL, M.moe_dispatch_backward, xp, inv, x, dw=torch.zeros((4, 2), device=DEV))
