@@ -125,8 +125,7 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
     if (full) advance(s_g, p.by[4]);
     copies_commit();
   };
-  if (STAGED)
-    for (int s = 0; s < p.stages - 1; ++s) stage(s * p.stage);
+  if (STAGED && p.stages == 2) stage(0);
   float r1n = 1.f, r2n = 0.f, gtn = 1.f;  // the next row's factors
   auto factors = [&](int64_t row) {
     if (row >= a.T) return;
@@ -162,14 +161,11 @@ __global__ void __launch_bounds__(NCH == 1 ? kThreads : kMaxGroupThreads)
       if (p.stages == 1) {
         if (BY_CHUNKS) group_sync(nt, group);  // the row before has been read
         stage(0);
-        copies_wait(0);
-        if (BY_CHUNKS) group_sync(nt, group);
-      } else {
-        copies_wait(p.stages - 2);
-        if (BY_CHUNKS) group_sync(nt, group);  // this row is there, the one before has been read
-        stage(at == 0 ? (p.stages - 1) * p.stage : at - p.stage);
       }
-      at = at + p.stage == p.stages * p.stage ? 0 : at + p.stage;
+      copies_wait();
+      if (BY_CHUNKS) group_sync(nt, group);  // this row is there, and with two stages the one before has been read
+      if (p.stages == 2) stage(p.stage - at);
+      at = p.stages == 2 ? p.stage - at : 0;
     }
     const float r1 = r1n, r2 = r2n, gt = gtn;
     factors(t + step);

@@ -11,8 +11,11 @@ namespace moe {
 namespace blk {
 
 constexpr int kMaxGroupThreads = 512;      // threads of a row's group, 8 * nch columns each
-constexpr int kNormSmem = 224 * 1024 + 256;      // dynamic shared memory per CTA (227 KB with the kernels' own)
-constexpr int kMaxStages = 2;              // rows staged per group (3: gradient 46.5 us, not 43.4, at 4,096 x 2,560)
+// Dynamic shared memory per CTA (227 KB with the kernels' own).
+constexpr int kNormSmem = 224 * 1024 + 256;
+// Rows staged per group, one or two (with three the gradient took 46.5 us, not
+// 43.4, at 4,096 x 2,560).
+constexpr int kMaxStages = 2;
 constexpr int kMaxStagedChunks = 2;        // wider rows (H > 8192) are read without staging
 
 // How a launch cuts its rows: CTAs of `groups` groups of `nt` threads, each

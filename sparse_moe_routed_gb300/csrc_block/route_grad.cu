@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kSlabThreads)
                  : "memory");
   }
   copies_commit();
-  copies_wait(0);
+  copies_wait();
   __syncthreads();
   const int sub = lane / kLanes, l = lane % kLanes;
   const Cols<8> c(col, l, kLanes);

@@ -134,13 +134,9 @@ __device__ __forceinline__ void store_vec(bf16_t* p, const Raw8<bf16_t>& r) {
                : "memory");
 }
 
-__device__ __forceinline__ float as_f32(float v) { return v; }
-__device__ __forceinline__ float as_f32(bf16_t v) { return bf16_to_f32(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(bf16_t* p, float v) { *p = f32_to_bf16(v); }
 
-__device__ __forceinline__ uint32_t raw_bits(float v) { return __float_as_uint(v); }
-__device__ __forceinline__ uint32_t raw_bits(bf16_t v) { return v; }
 __device__ __forceinline__ void raw_set(Raw8<float>& r, int i, float v) { r.v[i] = v; }
 __device__ __forceinline__ void raw_set(Raw8<bf16_t>& r, int i, bf16_t v) {
   if (i & 1)

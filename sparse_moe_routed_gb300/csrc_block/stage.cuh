@@ -4,10 +4,11 @@
 //   col(h, i) = h * 8 nt + ((i / G) * nt + tid) * G + i % G,   i = 0..7
 // for h = 0..NCH-1: G adjacent columns at a time (G divides H), so that every
 // access of a warp covers whole sectors (G = 4: 16 bytes of fp32, 8 of bf16 a
-// lane; G = 2: even widths; G = 1: any) and no unit of G is partial.  Each thread copies its own
-// columns into its own places in shared memory and reads them back itself:
-// copies of the rows ahead stay in flight while a row is worked on, cost no
-// registers, and need no barrier, only the thread's own wait.
+// lane; G = 2: even widths; G = 1: any) and no unit of G is partial.  Each
+// thread copies its own columns into its own places in shared memory and reads
+// them back itself: the copy of the row ahead stays in flight while a row is
+// worked on, costs no registers, and needs no barrier, only the thread's own
+// wait.
 #pragma once
 
 #include "launch.h"
@@ -30,15 +31,8 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int ha
                  : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most `left` of the thread's committed groups are in flight.
-__device__ __forceinline__ void copies_wait(int left) {
-  if (left >= 2)
-    asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else if (left == 1)
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
+// Waits for all of the thread's copies.
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 template <int G>
 __device__ __forceinline__ int col0(int h, int i, int tid, int nt) {
@@ -47,12 +41,12 @@ __device__ __forceinline__ int col0(int h, int i, int tid, int nt) {
 
 // Rows that start on any element (G = 1) would take many narrow copies that
 // way, and bf16 ones none at all (a copy has four bytes at least).  Their group
-// copies the aligned 16-byte chunks that hold the
-// row instead, into the operand's region of shared memory from its start on,
-// and after a barrier a thread reads its columns from there, as many bytes on
-// as the row starts behind its first chunk.  What the first chunk holds in
-// front of the row is read, but not used; a chunk that holds one byte of an
-// allocation lies inside it.
+// copies the aligned 16-byte chunks that hold the row instead, into the
+// operand's region of shared memory from its start on, and after a barrier a
+// thread reads its columns from there, as many bytes on as the row starts
+// behind its first chunk.  What the first chunk holds in front of the row is
+// read, but not used; a chunk that holds one byte of an allocation lies inside
+// it.
 template <int G>
 constexpr bool kByChunks = G == 1;
 
