@@ -485,6 +485,7 @@ class MoEStack:
         self.gammas = gammas
         self.post_gammas, self.gates, self.scale = post_gammas, gates, float(scale)
         H = self.layers[0].H
+        assert all(L.H == H for L in self.layers)
         dev = self.layers[0].w_router.device
         self.T_max = T_max
         self.n = torch.empty((T_max, H), dtype=torch.bfloat16, device=dev)
@@ -542,6 +543,9 @@ class MoEStack:
         s = torch.cuda.current_stream() if stream is None else stream
         T = x.shape[0]
         L = self.layers[l]
+        # the calls take pointers: n, the layer's buffers and a gate per token hold no more rows than these
+        assert x.dtype == torch.float32 and x.is_contiguous() and x.shape[1:] == self.n.shape[1:]
+        assert T <= self.T_max and T <= L.T_max
         if not self.post_norm:
             return [self._norm_call(x, l, s, raw)] + L.bound_calls(self.n[:T], T, stream=s, residual=x, out_f32=x,
                                                                   route=route)
@@ -549,9 +553,10 @@ class MoEStack:
             L.bound_calls(self.n[:T], T, stream=s, route=route) + [self._block_norm_call(x, l, nxt, s)]
 
     def forward(self, x, stream=None, layers=None):
-        """x [T,H] fp32 on the GPU, updated in place through the layers."""
-        assert x.dtype == torch.float32 and x.is_contiguous()
+        """x [T,H] fp32 on the GPU, updated in place through the layers; T is at
+        most T_max, the stack's and that of every layer."""
         order = list(range(len(self.layers)) if layers is None else layers)
+        assert all(x.shape[0] <= self.layers[l].T_max for l in order)  # nothing is issued for the layers before it
         for i, l in enumerate(order):
             nxt = order[i + 1] if self.post_norm and i + 1 < len(order) else None
             for call in self.layer_calls(x, l, stream, first=i == 0, nxt=nxt):
