@@ -490,11 +490,18 @@ class MoEStack:
         self.T_max = T_max
         self.n = torch.empty((T_max, H), dtype=torch.bfloat16, device=dev)
         self.post_norm = post_gammas is not None or gates is not None or self.scale != 1.0
-        for vectors in (post_gammas, gates):
-            for v in vectors or ():
-                assert v is None or (v.is_cuda and v.is_contiguous() and v.dtype == torch.float32)
-                assert v is None or v.shape == (H,) or (vectors is gates and v.shape == (T_max, 1))
+        for vectors, per_token in ((post_gammas, False), (gates, True)):
+            assert vectors is None or len(vectors) == len(self.layers)
+            for v in () if vectors is None else vectors:
+                self._check_vector(v, per_token)
         self._norm_bound = {}
+
+    def _check_vector(self, v, per_token=False):
+        """A layer's vector: None, [H] or (per_token) [T_max,1], where the layers are."""
+        if v is not None:
+            T_max, H = self.n.shape
+            assert v.device == self.n.device and v.dtype == torch.float32 and v.is_contiguous()
+            assert v.shape == (H,) or (per_token and v.shape == (T_max, 1))
 
     def _norm_call(self, x, l, s, raw=None):
         key = (x.data_ptr(), x.shape[0], l, s.cuda_stream, None if raw is None else raw.data_ptr())

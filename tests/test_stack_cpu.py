@@ -53,3 +53,26 @@ def test_a_layer_smaller_than_the_stack_is_refused_before_the_first_call(kw):
 def test_layers_of_different_widths_are_refused():
     with pytest.raises(AssertionError):
         MoEStack([Layer(8), Layer(8, 2 * H)], 8)
+
+
+@pytest.mark.parametrize("name", ["post_gammas", "gates"])
+def test_one_vector_per_layer(name):
+    stack(**{name: [None, None]})
+    stack(**{name: [torch.zeros(H), None]})
+    for n in (0, 1, 3):
+        with pytest.raises(AssertionError):
+            stack(**{name: [None] * n})
+
+
+def test_vectors_of_another_shape_type_or_device_are_refused():
+    stack(gates=[None, torch.zeros((8, 1))])
+    bad = [torch.zeros(H - 1), torch.zeros(H, dtype=torch.bfloat16), torch.zeros(2 * H)[::2],
+           torch.zeros(H, device="meta")]
+    for name, more in (("post_gammas", [torch.zeros((8, 1))]), ("gates", [torch.zeros((7, 1)), torch.zeros((8, 2))])):
+        for v in bad + more:
+            with pytest.raises(AssertionError):
+                stack(**{name: [None, v]})
+    # one list for both: a gate per token is no gain
+    both = [torch.zeros((8, 1))] * 2
+    with pytest.raises(AssertionError):
+        stack(post_gammas=both, gates=both)
