@@ -475,7 +475,10 @@ class MoEStack:
     the stream, x <- scale * x + gate_l * RMSNorm(MoE_l(RMSNorm(x))): the
     combine writes the output (bf16) alone, and moe_block_norm does everything
     between it and the next layer's router in one launch, so that a layer
-    issues as many launches as without.
+    issues as many launches as without.  The vectors, ``scale`` and ``eps`` are
+    read at every call: entries may be replaced between two (a gate per token
+    is new with every batch).  A captured graph keeps the addresses that it was
+    captured with.
     """
 
     def __init__(self, layers, T_max: int, eps: float = 1e-6, gammas=None, post_gammas=None, gates=None,
@@ -489,12 +492,15 @@ class MoEStack:
         dev = self.layers[0].w_router.device
         self.T_max = T_max
         self.n = torch.empty((T_max, H), dtype=torch.bfloat16, device=dev)
-        self.post_norm = post_gammas is not None or gates is not None or self.scale != 1.0
         for vectors, per_token in ((post_gammas, False), (gates, True)):
             assert vectors is None or len(vectors) == len(self.layers)
             for v in () if vectors is None else vectors:
                 self._check_vector(v, per_token)
         self._norm_bound = {}
+
+    @property
+    def post_norm(self):
+        return self.post_gammas is not None or self.gates is not None or self.scale != 1.0
 
     def _check_vector(self, v, per_token=False):
         """A layer's vector: None, [H] or (per_token) [T_max,1], where the layers are."""
@@ -503,13 +509,21 @@ class MoEStack:
             assert v.device == self.n.device and v.dtype == torch.float32 and v.is_contiguous()
             assert v.shape == (H,) or (per_token and v.shape == (T_max, 1))
 
+    def _vector(self, vectors, l, per_token=False):
+        """(entry l or None, its address), as the caller's list holds it now."""
+        v = None if vectors is None else vectors[l]
+        self._check_vector(v, per_token)
+        return v, 0 if v is None else v.data_ptr()
+
+    # A bound call holds addresses and values: its key names everything that
+    # the caller may replace between two calls on one stream buffer.
     def _norm_call(self, x, l, s, raw=None):
-        key = (x.data_ptr(), x.shape[0], l, s.cuda_stream, None if raw is None else raw.data_ptr())
+        g, g_at = self._vector(self.gammas, l)
+        key = (x.data_ptr(), x.shape[0], l, s.cuda_stream, None if raw is None else raw.data_ptr(), g_at, self.eps)
         c = self._norm_bound.get(key)
         if c is None:
             lib = _lib.load()
             P = _lib._ptr
-            g = None if self.gammas is None else self.gammas[l]
             T, H = x.shape
             c = ("moe_rmsnorm", lib.moe_rmsnorm,
                  (P(x), P(g), C.c_float(self.eps), T, H, P(self.n), P(raw), C.c_void_p(s.cuda_stream)))
@@ -521,16 +535,17 @@ class MoEStack:
     def _block_norm_call(self, x, l, nxt, s):
         """moe_block_norm after layer l: its output into x, and the norm before
         layer nxt (None: none) into n."""
-        key = ("block", x.data_ptr(), x.shape[0], l, nxt, s.cuda_stream)
+        post, post_at = self._vector(self.post_gammas, l)
+        gate, gate_at = self._vector(self.gates, l, per_token=True)
+        pre, pre_at = (None, 0) if nxt is None else self._vector(self.gammas, nxt)
+        kind = _block.MOE_GATE_NONE if gate is None else \
+            _block.MOE_GATE_CHANNEL if gate.dim() == 1 else _block.MOE_GATE_TOKEN
+        key = ("block", x.data_ptr(), x.shape[0], nxt is None, s.cuda_stream, self.layers[l].out.data_ptr(), post_at,
+               gate_at, kind, pre_at, self.scale, self.eps)
         c = self._norm_bound.get(key)
         if c is None:
             P = _lib._ptr
             T, H = x.shape
-            post = None if self.post_gammas is None else self.post_gammas[l]
-            gate = None if self.gates is None else self.gates[l]
-            kind = _block.MOE_GATE_NONE if gate is None else \
-                _block.MOE_GATE_CHANNEL if gate.dim() == 1 else _block.MOE_GATE_TOKEN
-            pre = None if nxt is None or self.gammas is None else self.gammas[nxt]
             f32, bf16 = _block.MOE_ROW_F32, _block.MOE_ROW_BF16
             c = ("moe_block_norm", _block.load().moe_block_norm,
                  (P(x), H, f32, P(self.layers[l].out), H, bf16, P(gate), kind, 0, P(post), P(pre), 1,

@@ -76,3 +76,50 @@ def test_vectors_of_another_shape_type_or_device_are_refused():
     both = [torch.zeros((8, 1))] * 2
     with pytest.raises(AssertionError):
         stack(post_gammas=both, gates=both)
+
+
+def bound(s, x, l=0, nxt=1):
+    """The arguments of the norm before layer l and of the norms after it."""
+    calls = {c[0]: c[2] for c in s.layer_calls(x, l, STREAM, nxt=nxt)}
+    plain = [v.value if hasattr(v, "value") else v for v in calls["moe_rmsnorm"]]
+    return plain, [v.value if hasattr(v, "value") else v for v in calls["moe_block_norm"]]
+
+
+def test_replaced_vectors_scale_and_eps_reach_the_next_call():
+    """A per-token gate is new with every batch: the calls of one stream buffer follow the stack's attributes."""
+    vec = lambda: [torch.zeros(H) for _ in range(2)]
+    s, x = stack(gammas=vec(), post_gammas=vec(), gates=vec()), torch.zeros((8, H))
+    bound(s, x)
+    s.gates[0] = torch.zeros((8, 1))
+    s.post_gammas[0], s.gammas[0], s.gammas[1] = torch.zeros(H), torch.zeros(H), torch.zeros(H)
+    s.scale, s.eps = 0.5, 1e-3
+    s.layers[0].out = torch.empty((8, H), dtype=torch.bfloat16)
+    before, after = bound(s, x)
+    assert before[1] == s.gammas[0].data_ptr() and abs(before[2] - 1e-3) < 1e-9
+    assert after[3] == s.layers[0].out.data_ptr()
+    assert (after[6], after[7]) == (s.gates[0].data_ptr(), 2)  # per token
+    assert (after[9], after[10]) == (s.post_gammas[0].data_ptr(), s.gammas[1].data_ptr())
+    assert after[12] == 0.5 and abs(after[13] - 1e-3) < 1e-9
+    s.gates[0] = None
+    assert bound(s, x)[1][6:8] == [None, 0]
+    s.gates = None
+    assert bound(s, x)[1][6:8] == [None, 0]
+
+
+def test_norms_after_the_layers_may_be_asked_for_later():
+    s, x = stack(), torch.zeros((8, H))
+    assert [c[0] for c in s.layer_calls(x, 0, STREAM)] == ["moe_rmsnorm", "layer"]
+    s.scale = 0.5
+    assert bound(s, x)[1][12] == 0.5
+
+
+def test_a_replaced_vector_is_checked():
+    s, x = stack(gammas=[None, None], gates=[None, None], post_gammas=[None, None]), torch.zeros((8, H))
+    bound(s, x)
+    for name in ("gammas", "gates", "post_gammas"):
+        for v in (torch.zeros(H - 1), torch.zeros(H, dtype=torch.bfloat16), torch.zeros(2 * H)[::2]):
+            getattr(s, name)[0] = v
+            with pytest.raises(AssertionError):
+                s.layer_calls(x, 0, STREAM)
+        getattr(s, name)[0] = None
+    assert bound(s, x)
