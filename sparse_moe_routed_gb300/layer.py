@@ -560,8 +560,9 @@ class MoEStack:
         """Calls of layer l on the residual stream x; raw (optional, [T,H]
         bf16) receives x rounded to bf16 before normalisation.  With norms
         after the layers, first=False leaves out the norm before the layer
-        (the call of the layer before it made it) and nxt names the layer
-        whose norm this layer's last call makes."""
+        (the call of the layer before it made it; it writes no raw, so raw is
+        refused) and nxt names the layer whose norm this layer's last call
+        makes."""
         s = torch.cuda.current_stream() if stream is None else stream
         T = x.shape[0]
         L = self.layers[l]
@@ -571,6 +572,7 @@ class MoEStack:
         if not self.post_norm:
             return [self._norm_call(x, l, s, raw)] + L.bound_calls(self.n[:T], T, stream=s, residual=x, out_f32=x,
                                                                   route=route)
+        assert first or raw is None
         return ([self._norm_call(x, l, s, raw)] if first else []) + \
             L.bound_calls(self.n[:T], T, stream=s, route=route) + [self._block_norm_call(x, l, nxt, s)]
 

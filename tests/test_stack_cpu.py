@@ -123,3 +123,12 @@ def test_a_replaced_vector_is_checked():
                 s.layer_calls(x, 0, STREAM)
         getattr(s, name)[0] = None
     assert bound(s, x)
+
+
+def test_raw_without_the_norm_that_writes_it_is_refused():
+    s, x, raw = stack(scale=0.5), torch.zeros((8, H)), torch.zeros((8, H), dtype=torch.bfloat16)
+    assert s.layer_calls(x, 0, STREAM, raw=raw)[0][2][6].value == raw.data_ptr()
+    with pytest.raises(AssertionError):
+        s.layer_calls(x, 1, STREAM, raw=raw, first=False)
+    # without norms after the layers every layer has its own norm before it
+    assert stack().layer_calls(x, 1, STREAM, raw=raw, first=False)[0][2][6].value == raw.data_ptr()
