@@ -55,9 +55,11 @@ struct Multi {
   int32_t e, part0, n, pad;
 };
 
+// With unit u an expert of n routes has ceil(n / u) <= n / u + 1 units, and one
+// of several has n > u routes: at most R / u experts, and no more than E.
 inline int max_units(int R, int E) { return E + R / unit_for(R); }
-inline int max_multi(int R) { return R / unit_for(R); }
-inline int max_partials(int R) { return 2 * (R / unit_for(R)) + 1; }
+inline int max_multi(int R, int E) { return std::min(E, R / unit_for(R)); }
+inline int max_partials(int R, int E) { return R / unit_for(R) + max_multi(R, E) + 1; }
 
 // The workspace's parts, 256-byte aligned: the units, the experts of several
 // units, partial rows [..][H], their bias sums.
@@ -77,9 +79,9 @@ Ws ws_layout(void* p, int R, int E, int H) {
   };
   Ws w;
   w.units = reinterpret_cast<Unit*>(take(sizeof(Unit) * max_units(R, E)));
-  w.multi = reinterpret_cast<Multi*>(take(sizeof(Multi) * max_multi(R)));
-  w.rows = reinterpret_cast<float*>(take(sizeof(float) * static_cast<size_t>(max_partials(R)) * H));
-  w.bias = reinterpret_cast<float*>(take(sizeof(float) * max_partials(R)));
+  w.multi = reinterpret_cast<Multi*>(take(sizeof(Multi) * max_multi(R, E)));
+  w.rows = reinterpret_cast<float*>(take(sizeof(float) * static_cast<size_t>(max_partials(R, E)) * H));
+  w.bias = reinterpret_cast<float*>(take(sizeof(float) * max_partials(R, E)));
   w.bytes = at;
   return w;
 }
@@ -429,7 +431,7 @@ cudaError_t launch_route_grad(const RouteGradArgs& a, cudaStream_t st) {
   const bool rows = a.dw_router.p != nullptr || a.dbias != nullptr, direct = a.T <= kDirectTokens;
   const int plan = rows && !direct;
   const Ws ws = ws_layout(a.ws, R, a.E, a.H);
-  const int units = direct ? a.E : max_units(R, a.E), multi = direct ? 0 : max_multi(R);
+  const int units = direct ? a.E : max_units(R, a.E), multi = direct ? 0 : max_multi(R, a.E);
   cudaError_t e = cudaSuccess;
   if (a.T > 0) {
     const int warps = kPlanThreads / 32, ctas = std::min((a.T + warps - 1) / warps, 4 * sm_count());

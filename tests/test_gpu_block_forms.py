@@ -3,8 +3,10 @@ only larger calls reach, against the definitions in 64 bits."""
 import pytest
 import torch
 
+import block_reference as ref
 import sparse_moe_routed_gb300 as M
 import workloads as wl
+from test_gpu_block import group, near, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +43,30 @@ def test_stack_follows_its_replaced_gates_and_scale():
         assert torch.equal(got, fresh.forward(x0.clone())) and not torch.equal(got, first)
     with pytest.raises(AssertionError):
         s.forward(torch.zeros((T_max + 1, wl.TINY.H), device=DEV))
+
+
+@pytest.mark.parametrize("T,k,E,H,n", [
+    (520, 1, 8, 264, 65),       # eight experts of one unit and one route: the most partial rows there can be
+    (2064, 1, 8, 72, 129),      # the last unit of an expert holds one route
+    (20000, 1, 2, 136, None),   # far more units than experts
+    (16640, 8, 8, 64, None),    # units of 256 routes, every token in every expert
+])
+def test_router_gradient_fills_its_workspace(T, k, E, H, n):
+    g = gen(T + E)
+    if n is None:
+        ids = torch.rand((T, E), generator=g, device=DEV).topk(k, 1)[1].to(torch.int32).contiguous()
+    else:
+        ids = (torch.arange(T, device=DEV) % E).to(torch.int32).view(T, 1)
+        assert T == n * E
+    w, dw = torch.rand((T, k), generator=g, device=DEV), torch.randn((T, k), generator=g, device=DEV)
+    x, wr = rand(g, T, H, BF16), rand(g, E, H, BF16)
+    offsets, perm = group(ids, E)
+    size = M.moe_route_backward_workspace_size(T, k, E, H)
+    ws = torch.full((size + 4096,), 255, dtype=torch.uint8, device=DEV)
+    dl, dx = torch.empty((T, k), device=DEV), torch.empty((T, H), device=DEV)
+    dwr, db = torch.empty((E, H), device=DEV), torch.empty(E, device=DEV)
+    M.moe_route_backward(dw, w, ids, x, wr, offsets, perm, dl, dx, dwr, db, ws[:size])
+    want = ref.route_grad(dw, w, ids, x, wr, None, F32)
+    for name, got in (("dlogits", dl), ("dx", dx), ("dw_router", dwr), ("dbias", db)):
+        near(got, want[name], name)
+    assert bool((ws[size:] == 255).all())
