@@ -312,8 +312,9 @@ __global__ void __launch_bounds__(1024) norm_cols_kernel(const float* __restrict
     if (dgamma_pre != nullptr) dgamma_pre[c] = v;
     return;
   }
-  if (dgamma_post != nullptr) dgamma_post[c] = gate_c != nullptr ? gate_c[c] * v : v;
-  if (dgate_c != nullptr) dgate_c[c] = post_norm ? gain(gamma_post, c) * v : v;
+  // no rows: zero, whatever the gate and the gain hold
+  if (dgamma_post != nullptr) dgamma_post[c] = gate_c != nullptr && parts > 0 ? gate_c[c] * v : v;
+  if (dgate_c != nullptr) dgate_c[c] = post_norm && parts > 0 ? gain(gamma_post, c) * v : v;
 }
 
 }  // namespace

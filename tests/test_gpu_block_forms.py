@@ -70,3 +70,16 @@ def test_router_gradient_fills_its_workspace(T, k, E, H, n):
     for name, got in (("dlogits", dl), ("dx", dx), ("dw_router", dwr), ("dbias", db)):
         near(got, want[name], name)
     assert bool((ws[size:] == 255).all())
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")], ids=str)
+def test_norm_gradient_of_no_rows_is_zero_whatever_the_gate_holds(value):
+    H = 40
+    e = lambda *s: torch.empty(s, device=DEV)
+    cols = [torch.full((H,), 7.0, device=DEV) for _ in range(3)]
+    ws = torch.empty(M.moe_block_norm_workspace_size(0, H), dtype=torch.uint8, device=DEV)
+    full = lambda: torch.full((H,), value, device=DEV)
+    M.moe_block_norm_backward(e(0, H), e(0, H), e(0, H), e(0, H), e(0, H), e(0, H), ws, gate=full(), gamma_post=full(),
+                              gamma_pre=full(), rstd_post=e(0), rstd_pre=e(0), dgate=cols[0], dgamma_post=cols[1],
+                              dgamma_pre=cols[2])
+    assert all(bool((c == 0).all()) for c in cols)
