@@ -46,8 +46,7 @@ def load():
     with _lock:
         if _blk is not None:
             return _blk
-        _build.build()
-        lib = C.CDLL(_build.LIB_BLOCK)
+        lib = C.CDLL(_build.build(lib=_build.LIB_BLOCK))
         p, i, l, f, sz = C.c_void_p, C.c_int, C.c_int64, C.c_float, C.c_size_t
         sig = {
             "moe_block_abi_version": ([], i),

@@ -46,7 +46,7 @@ def load(path: str | None = None):
         if _lib is not None:
             return _lib
         if path is None:
-            path = _build.build()
+            path = _build.build(lib=_build.LIB)
         lib = C.CDLL(path)
         p, i, sz = C.c_void_p, C.c_int, C.c_size_t
         f = C.c_float

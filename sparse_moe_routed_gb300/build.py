@@ -4,7 +4,7 @@ sm_103a.
 Each translation unit compiles in parallel with nvcc, then the shared libraries
 are linked next to this file.  No cmake, no torch extension machinery: the
 libraries have plain C ABIs (include/moe.h, include/moe_block.h) and are loaded
-with ctypes.
+with ctypes.  Loading one library builds that one alone.
 """
 from __future__ import annotations
 
@@ -45,22 +45,29 @@ def block_sources():
     return sorted(glob.glob(os.path.join(CSRC_BLOCK, "*.cu")))
 
 
-def _deps():
-    return [f for d in (CSRC, CSRC_BLOCK, INCLUDE) for ext in ("*.cu", "*.cuh", "*.h")
-            for f in glob.glob(os.path.join(d, ext))]
+def _sources(lib):
+    return sources() if lib == LIB else block_sources()
 
 
-def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(LIB_BLOCK)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(LIB_BLOCK))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+def _deps(lib):
+    """Files that `lib` is made of.  libmoe_block includes headers of csrc/, libmoe none of csrc_block/."""
+    own = [CSRC] if lib == LIB else [CSRC_BLOCK, CSRC]
+    headers = [f for d in own for ext in ("*.cuh", "*.h") for f in glob.glob(os.path.join(d, ext))]
+    public = [os.path.join(INCLUDE, "moe.h")] + ([] if lib == LIB else [os.path.join(INCLUDE, "moe_block.h")])
+    return _sources(lib) + headers + public
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    """Build both libraries; returns the path of libmoe.so."""
-    if not force and up_to_date():
-        return LIB
+def up_to_date(lib: str | None = None) -> bool:
+    """Is `lib` (None: both libraries) newer than everything that it is made of?"""
+    return all(os.path.exists(f) and all(os.path.getmtime(d) <= os.path.getmtime(f) for d in _deps(f))
+               for f in ((LIB, LIB_BLOCK) if lib is None else (lib,)))
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=None, lib: str | None = None) -> str:
+    """Build `lib`, LIB or LIB_BLOCK (None: both), where it is out of date; returns its path (None: libmoe.so's)."""
+    stale = [f for f in ((LIB, LIB_BLOCK) if lib is None else (lib,)) if force or not up_to_date(f)]
+    if not stale:
+        return lib or LIB
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     flags = NVCC_FLAGS + list(extra_flags or [])
@@ -78,16 +85,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         run([nvcc, *ARCH, *flags, "-c", src, "-o", obj], f"nvcc failed on {name}")
         return obj
 
-    libs = ((LIB, sources()), (LIB_BLOCK, block_sources()))
+    todo = [src for f in stale for src in _sources(f)]
     with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 4)) as ex:
-        objs = dict(zip((src for _, srcs in libs for src in srcs),
-                        ex.map(compile_one, (src for _, srcs in libs for src in srcs))))
-    for lib, srcs in libs:
-        tmp = lib + ".tmp"
-        run([nvcc, *ARCH, "-shared", "-o", tmp, *(objs[s] for s in srcs), "-lcudart_static", "-ldl", "-lrt",
+        objs = dict(zip(todo, ex.map(compile_one, todo)))
+    for f in stale:
+        tmp = f + ".tmp"
+        run([nvcc, *ARCH, "-shared", "-o", tmp, *(objs[s] for s in _sources(f)), "-lcudart_static", "-ldl", "-lrt",
              "-lpthread"], "link failed")
-        os.replace(tmp, lib)
-    return LIB
+        os.replace(tmp, f)
+    return lib or LIB
 
 
 if __name__ == "__main__":
