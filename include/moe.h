@@ -246,7 +246,8 @@ MOE_API moe_status moe_route_permute(const uint16_t *x, const uint16_t *w_router
  * has finished; they wait for it only where they read its output (x_perm
  * or h).  The library decides this from its own launch order on the
  * stream, so any other order is safe and simply waits: it needs no action
- * from the caller.  Calls that share a stream are issued from one host
+ * from the caller.  (A call of moe_block.h between the two does not count as
+ * another order: it writes neither offsets nor weights.)  Calls that share a stream are issued from one host
  * thread at a time, as their order on the stream requires anyway.
  * ------------------------------------------------------------------------- */
 MOE_API moe_status moe_expert_gateup(const uint16_t *x_perm, const int32_t *offsets, int R, int E, int H,

@@ -21,8 +21,13 @@ cudaError_t ensure_smem(void (*kern)(KArgs...), int bytes) {
 // A launch may leave a token on its stream: the address of a buffer it read
 // only after its grid-dependency wait and did not write.  Every launch of
 // this library clears its stream's token first, so a token seen before a
-// launch names the launch right before it.  (Launches outside the library
-// do not clear it, but they do not let a later launch start early either.)
+// launch names the last launch of this library before it.  Launches outside
+// the library do not clear it.  Most of them do not let a later launch start
+// early; libmoe_block's do, but only once everything before them has completed
+// (each waits first), and they write neither offsets nor packed records, so
+// that what a launch with the token reads before its wait is complete and
+// unchanged.  A kernel there that wrote either would have to leave out its
+// trigger.
 void stream_token_set(cudaStream_t st, const void* token);
 const void* stream_token_get(cudaStream_t st);
 void stream_token_clear(cudaStream_t st);

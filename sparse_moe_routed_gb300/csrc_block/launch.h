@@ -18,7 +18,10 @@ namespace blk {
 int sm_count();
 
 // Launch with programmatic stream serialization (see pdl_wait in
-// ../csrc/common.cuh): every kernel waits before its first global access.
+// ../csrc/common.cuh): every kernel waits before its first global access and
+// before its trigger.  libmoe's int4 contractions may read offsets and packed
+// records while a launch of this library right before them still runs (see the
+// stream token in ../csrc/launch.h): no kernel that triggers writes those.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                        Args&&... args) {

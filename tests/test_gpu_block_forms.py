@@ -6,6 +6,7 @@ import torch
 import block_reference as ref
 import sparse_moe_routed_gb300 as M
 import workloads as wl
+from sparse_moe_routed_gb300 import _lib, pack_layer_experts
 from test_gpu_block import group, near, rand
 
 pytestmark = pytest.mark.gpu
@@ -83,3 +84,44 @@ def test_norm_gradient_of_no_rows_is_zero_whatever_the_gate_holds(value):
                               gamma_pre=full(), rstd_post=e(0), rstd_pre=e(0), dgate=cols[0], dgamma_post=cols[1],
                               dgamma_pre=cols[2])
     assert all(bool((c == 0).all()) for c in cols)
+
+
+def test_int4_launches_right_after_a_block_call_read_what_it_wrote():
+    """moe_dispatch rewrites x_perm between the row gather and the gate/up launch, moe_collect_backward rewrites h
+    between that and the down launch: both int4 launches start early and read the rows only after these calls."""
+    cfg = wl.LayerConfig("int4_between", T=16, H=1024, E=64, k=4, I=256, bias=None, seed=53)
+    T, k, E, H, I, R, fmt = 16, cfg.k, cfg.E, cfg.H, cfg.I, 64, _lib.MOE_W_INT4_G64_TILED
+    d = wl.layer_inputs(cfg, DEV)
+    q_gu, s_gu = wl.quantize_int4_g64(d["w_gateup"])
+    q_d, s_d = wl.quantize_int4_g64(d["w_down"])
+    gu, dn = pack_layer_experts(q_gu, q_d, _lib.MOE_W_INT4_G64, E, H, I, s_gateup=s_gu, s_down=s_d)
+    g = gen(53)
+    ids = torch.rand((T, E), generator=g, device=DEV).topk(k, 1)[1].to(torch.int32).contiguous()
+    x, x2, th = rand(g, T, H, BF16), rand(g, T, H, BF16), rand(g, T, I, BF16)
+    w = torch.rand((T, k), generator=g, device=DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    counts, offsets, perm, inv = (torch.empty(n, **i32) for n in (E, E + 1, R, R))
+    st = torch.zeros(1, **i32)
+
+    def steps(wait):
+        xp, h = torch.zeros((R, H), dtype=BF16, device=DEV), torch.zeros((R, I), dtype=BF16, device=DEV)
+        y, slots = torch.zeros((R, H), device=DEV), inv.view(T, k)
+        torch.cuda.synchronize()
+        for call in (lambda: _lib.moe_permute(ids, E, x, counts, offsets, perm, inv, xp, st),
+                     lambda: M.moe_dispatch(x2, slots, xp, w=w, dev_status=st),
+                     lambda: _lib.moe_expert_gateup(xp, offsets, E, H, I, gu, h, st, fmt=fmt)):
+            call()
+            wait()
+        h_gate = h.clone()
+        for call in (lambda: _lib.moe_expert_gateup(xp, offsets, E, H, I, gu, h, st, fmt=fmt),
+                     lambda: M.moe_collect_backward(th, None, slots, w, h, dev_status=st),
+                     lambda: _lib.moe_expert_down(h, offsets, E, H, I, dn, y, st, fmt=fmt)):
+            call()
+            wait()
+        return xp, h_gate, h, y
+
+    want = steps(torch.cuda.synchronize)
+    assert int(st) == 0 and bool((want[3] != 0).any())
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(want, steps(lambda: None)))
+    assert int(st) == 0
