@@ -48,7 +48,7 @@ def test_stack_follows_its_replaced_gates_and_scale():
 
 @pytest.mark.parametrize("T,k,E,H,n", [
     (520, 1, 8, 264, 65),       # eight experts of one unit and one route: the most partial rows there can be
-    (2064, 1, 8, 72, 129),      # the last unit of an expert holds one route
+    (1032, 1, 8, 72, 129),      # the last unit of an expert holds one route
     (20000, 1, 2, 136, None),   # far more units than experts
     (16640, 8, 8, 64, None),    # units of 256 routes, every token in every expert
 ])
