@@ -26,7 +26,8 @@
  *    MOE_ENOTSUP.
  *  - Values are not checked: infinities and NaN go where the formulas take
  *    them.  Rows that no route names are never read.  Sums of squares are
- *    fp32: a norm's rows stay below about 1e18 in size.
+ *    fp32: a norm's rows have one below 3e38 (elements below 1e17 at the widest)
+ *    and, with eps 0, above 1e-37; outside that the factor is 0 or infinite.
  *  - A call may be captured into a CUDA graph; make one call of its kind on
  *    the device before, which loads the library's device code.  Captured calls
  *    that share a workspace must not be replayed at the same time.

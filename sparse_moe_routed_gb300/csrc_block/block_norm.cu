@@ -12,7 +12,8 @@
 // row; the row ahead is staged in shared memory (stage.cuh), with c1 and c2
 // beside the stages.  fp32 stream, bf16 block, width 2,560: 24 us at 4,096 rows
 // (77 % of the measured copy rate), 81 us at 16,384 (91 %): 4.6 ns a row (98 %)
-// and 5 us of start and end.
+// and 5 us of start and end.  Rows of 1,024 x 9,000 (unstaged) take 77 us, of
+// 1,024 x 8,192 23.
 #include <math.h>
 
 #include "norm.h"

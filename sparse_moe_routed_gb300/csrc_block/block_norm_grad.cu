@@ -16,8 +16,10 @@
 // reads the stage again.  One CTA per SM keeps A and B over all its rows and
 // writes one partial row of each; a second launch adds these in order.  fp32
 // stream, bf16 block, width 2,560: 39 us at 4,096 rows (72 % of the measured
-// copy rate), 118 us at 16,384 (94 %): 6.5 ns a row and 10 us of start, column
-// sums and second launch.
+// copy rate), 118 us at 16,384 (94 %): 6.5 ns a row and 10 us that do not grow
+// with the rows, 6 of them the column sums with their launch (at 1,024, 4,096
+// and 16,384 rows alike), the rest start and first rows.  Rows of 1,024 x 9,000
+// (unstaged) take 214 us, of 1,024 x 8,192 50.
 #include <math.h>
 
 #include "norm.h"
@@ -29,7 +31,8 @@ namespace blk {
 namespace {
 
 // 96 registers a thread: spills would miss the small L1 that the stages leave
-// (a form that spilled six registers per row took 56 us, not 46).
+// (a form that spilled six registers per row took 56 us, not 46).  The forms of
+// eight columns per thread spill up to 36 bytes, those of wider rows 224 to 752.
 constexpr int kThreads = 640;
 
 template <typename TX, typename TY, int G, int NCH>

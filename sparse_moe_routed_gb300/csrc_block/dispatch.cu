@@ -35,10 +35,14 @@ namespace {
 // several warps are better off with four and twice the CTAs per SM (dispatch's
 // gradient at 2,048 tokens: 24.7 against 33.2 us).  fp32 rows, and single
 // elements, need twice the registers for a route: half of each, or what the
-// launch bounds leave spills (dispatch's gradient of fp32 rows, 4,096 tokens:
+// launch bounds leave spills more (dispatch's gradient of fp32 rows, 4,096 tokens:
 // 83.7 us with four, 128 with eight; 1,024 tokens: 25.4 with two, 29.8 with
 // four, but collect without dw 20.2 with four, 21.4 with two; of odd bf16 rows,
-// 4,096 tokens: 86.3 us with two, 110 with four).
+// 4,096 tokens: 86.3 us with two, 110 with four).  Most kernels with dw still
+// spill: where a warp owns a token up to 120 bytes a thread for up to 16 routes
+// (48 for bf16 rows in whole pieces) and 300 above; join with several warps per
+// token on odd elements 264 to 356 bytes, above 16 routes 636 to 820 (without dw
+// 56 to 80).
 template <bool SOLO, bool DOT, typename TR, int U>
 constexpr int kBatch = sizeof(TR) == 2 && U > 1 ? (SOLO ? 8 : 4)
                        : sizeof(TR) == 4 && SOLO ? 4

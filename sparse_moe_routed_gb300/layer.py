@@ -596,8 +596,8 @@ class PrefillRing:
     ring: layer l + 1 lands in one ring slot while layer l computes from the
     other, and the copy into a slot waits until the layer that last used it
     is done (AFN-019, section "Hypothesis H5: prefill and decode need
-    different streaming modes").  The residual stack is MoEStack's:
-    x <- x + MoE_l(RMSNorm(x)); the output is bit-identical to MoEStack over
+    different streaming modes").  The residual stack is MoEStack's without
+    norms after the layers, x <- x + MoE_l(RMSNorm(x)); the output is bit-identical to MoEStack over
     the same records resident in HBM.
 
     routers: [(w_router [E,H] bf16, bias or None)] per layer (device);
