@@ -2,7 +2,8 @@
  * moe_block.h -- C ABI of libmoe_block: what stands around the expert
  * contractions in a block (token rows to expert order and back, the norms
  * with gate and residual scale), with the gradients of these and of the
- * router.
+ * router; and the experts' feed-forward block for training, with its backward
+ * pass and activations kept in 8 bits between the two.
  *
  * Conventions are those of moe.h (device pointers owned by the caller, no
  * allocation, host checks before anything is enqueued, MOE_DEV_* bits in
@@ -223,6 +224,118 @@ MOE_API moe_status moe_route_backward(const float *dw, const float *topk_w, cons
                                       int64_t ldx_grad, int dx_type, const void *add, int64_t ld_add,
                                       float *dw_router, int64_t ld_dw, float *dbias, void *workspace,
                                       size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_checkpoint_save -- rows of activations into 8 bits.
+ *
+ * 32 adjacent columns of a row (its last group may have fewer) share a scale
+ * 2^e, the smallest power of two, -126 <= e <= 121, with max|x| <= 127 * 2^e:
+ *   q[t,c]        = x[t,c] / 2^e, rounded to the nearest whole number (ties to
+ *                   even), at most 127 either way
+ *   exp[t,c / 32] = e + 127
+ * The quotient is exact, so q and exp are the same bits wherever they are
+ * computed, and q * 2^e is a bf16 number: reading back rounds nothing.  It is
+ * off by at most half of 2^e, less than 1/127 of the group's largest value
+ * (from 127.5 * 2^121 on by at most 2^121).  A NaN or an infinity in a group makes
+ * its exp 255, and the whole group reads back as NaN.
+ *
+ *   x   [T,H] row_type
+ *   q   [T,H] int8 (out), exp [T, ceil(H/32)] uint8 (out): rows ldq and ld_exp
+ *       elements apart, any alignment
+ * Source: AFN-021 "Replay decode as prefill", section "Do not store every large
+ * activation".
+ * ------------------------------------------------------------------------- */
+MOE_API moe_status moe_checkpoint_save(const void *x, int64_t ldx, int row_type, int T, int H, int8_t *q, int64_t ldq,
+                                       uint8_t *exp, int64_t ld_exp, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_checkpoint_load -- rows that moe_checkpoint_save kept, as values.
+ *
+ *   out[t,c]             = q[t,c] * 2^(exp[t,c / 32] - 127)        inv_perm NULL
+ *   out[inv_perm[t,j],c] = w[t,j] * q[t,c] * 2^(exp[t,c / 32] - 127)
+ *                                                    (w NULL: factor 1)
+ * The second form is moe_dispatch of the rows without writing them in token
+ * order first: one byte per value is read for its k copies.
+ *
+ *   inv_perm [T,k] int32 or NULL: as in moe_dispatch (-1: no slot)
+ *   w        [T,k] f32 or NULL; NULL where inv_perm is
+ *   out      (out) row_type: [R,H] with inv_perm, else [T,H] (k and R ignored)
+ * exp 0 (which moe_checkpoint_save never writes) stands for 2^-127, 249 to 254
+ * for 2^122 to 2^127.
+ * ------------------------------------------------------------------------- */
+MOE_API moe_status moe_checkpoint_load(const int8_t *q, int64_t ldq, const uint8_t *exp, int64_t ld_exp, int T, int H,
+                                       const int32_t *inv_perm, const float *w, int k, int R, void *out,
+                                       int64_t ld_out, int row_type, int32_t *dev_status, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_ffn -- the experts' gated feed-forward block, keeping what its backward
+ * pass needs.
+ *
+ *   for every slot s of expert e (offsets[e] <= s < offsets[e+1]):
+ *   g = W_gate x[s], u = W_up x[s]              (fp32 accumulate)
+ *   h[s] = silu(g) * u                          (rounded once to bf16)
+ *   act[s] = (g, u)                             (rounded once to its type)
+ *   y[s] = W_down h[s]                          (fp32 accumulate)
+ * moe_grouped_swiglu with plain bf16 weights for any H and I that are
+ * multiples of 8, strided rows, y of either type and kept activations.  E == 1
+ * with offsets {0, R} is one dense block.
+ *
+ *   x_perm   [R,H] bf16;  w_gateup [E,2I,H] bf16: gate rows, then up rows;
+ *            w_down [E,H,I] bf16;  offsets [E+1] int32 (moe_permute)
+ *   h        [R,I] bf16 (out), contiguous: scratch between the two contractions
+ *   act      (out) by act_kind: MOE_ACT_NONE (NULL), MOE_ACT_BF16 [R,2I] bf16,
+ *            MOE_ACT_Q8 [R,2I] int8 with act_exp [R, 2 ceil(I/32)] uint8: gate
+ *            and up columns each as moe_checkpoint_save keeps a matrix of width I
+ *   y_perm   [R,H] y_type (out), or NULL when only h and act are wanted
+ * Rows from offsets[E] on are not read for any result and not written.
+ * H % 8 == 0, I % 8 == 0, H, I <= 65536; bf16 and f32 matrices start on 16 byte
+ * boundaries with ld % 8 == 0.  offsets outside [0,R] or falling are clamped.
+ * dev_status gets MOE_DEV_TIMEOUT if a bounded pipeline wait ran out (the
+ * launch then stops early; outputs are incomplete).
+ * Source: AFN-019 "Hide SSD misses before the router knows they exist", section
+ * "Why overlap alone cannot defeat the byte roofline" (gate, up and down of an
+ * expert).
+ * ------------------------------------------------------------------------- */
+typedef enum moe_act_kind { MOE_ACT_NONE = 0, MOE_ACT_BF16 = 1, MOE_ACT_Q8 = 2 } moe_act_kind;
+
+MOE_API moe_status moe_ffn(const uint16_t *x_perm, int64_t ldx, const uint16_t *w_gateup, const uint16_t *w_down,
+                           const int32_t *offsets, int R, int E, int H, int I, uint16_t *h, void *act, int act_kind,
+                           int64_t ld_act, uint8_t *act_exp, int64_t ld_exp, void *y_perm, int64_t ldy, int y_type,
+                           int32_t *dev_status, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_ffn_backward -- gradient of moe_ffn.
+ *
+ * With (g, u) = act[s], r = 1 / (1 + exp(-g)), per slot s of expert e:
+ *   dh = W_down^T dy[s]                                     (fp32)
+ *   dg = dh * u * r * (1 + g * (1 - r)),  du = dh * g * r   (rounded to bf16)
+ *   h  = g * r * u                                          (rounded to bf16)
+ *   dx[s] = W_gate^T dg + W_up^T du
+ *   dw_gateup[e] = sum over the expert's slots of (dg, du) x[s]^T
+ *   dw_down[e]   = sum over the expert's slots of dy[s] h^T
+ * dg, du and h are operands of the contractions after them and are rounded to
+ * bf16 for that, once; sums are fp32, in a fixed order.
+ *
+ *   dy_perm  [R,H] bf16;  x_perm [R,H] bf16 (what moe_ffn read, or what
+ *            moe_checkpoint_load gives back; NULL allowed without dw_gateup)
+ *   act, act_kind (not MOE_ACT_NONE), act_exp: as moe_ffn wrote them
+ *   dx_perm  [R,H] dx_type (out) or NULL
+ *   dw_gateup [E,2I,H], dw_down [E,H,I] dw_type (out), each NULL when not
+ *            wanted (not all three NULL); 32 byte aligned, contiguous.  An
+ *            expert without slots gets zeros.
+ *   accumulate  != 0: the weight gradients are added to what is there
+ *   workspace >= moe_ffn_backward_workspace_size(R, I) bytes, 16-byte aligned,
+ *            contents do not matter; not to be shared by calls that overlap on
+ *            the GPU
+ * Sizes, alignment, offsets, rows from offsets[E] on and dev_status: as moe_ffn.
+ * ------------------------------------------------------------------------- */
+MOE_API size_t moe_ffn_backward_workspace_size(int R, int I);
+MOE_API moe_status moe_ffn_backward(const uint16_t *dy_perm, int64_t lddy, const uint16_t *x_perm, int64_t ldx,
+                                    const void *act, int act_kind, int64_t ld_act, const uint8_t *act_exp,
+                                    int64_t ld_exp, const uint16_t *w_gateup, const uint16_t *w_down,
+                                    const int32_t *offsets, int R, int E, int H, int I, void *dx_perm, int64_t lddx,
+                                    int dx_type, void *dw_gateup, void *dw_down, int dw_type, int accumulate,
+                                    void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }

@@ -23,6 +23,8 @@ from ._lib import MOE_EINVAL, MOE_ENOTSUP, MOE_ESHAPE, MOE_OK, MoEError
 
 MOE_ROW_F32, MOE_ROW_BF16 = 0, 1
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = range(4)
+MOE_ACT_NONE, MOE_ACT_BF16, MOE_ACT_Q8 = range(3)
+GROUP = 32  # columns that share an exponent in 8 bits
 
 HEADER = os.path.join(_build.INCLUDE, "moe_block.h")
 
@@ -60,6 +62,11 @@ def load():
                                          p, p, p, sz, p], i),
             "moe_route_backward_workspace_size": ([i, i, i, i], sz),
             "moe_route_backward": ([p, p, p, p, l, p, l, p, p, i, i, i, i, p, p, l, i, p, l, p, l, p, p, sz, p, p], i),
+            "moe_checkpoint_save": ([p, l, i, i, i, p, l, p, l, p], i),
+            "moe_checkpoint_load": ([p, l, p, l, i, i, p, p, i, i, p, l, i, p, p], i),
+            "moe_ffn": ([p, l, p, p, p, i, i, i, i, p, p, i, l, p, l, p, l, i, p, p], i),
+            "moe_ffn_backward_workspace_size": ([i, i], sz),
+            "moe_ffn_backward": ([p, l, p, l, p, i, l, p, l, p, p, p, i, i, i, i, p, l, i, p, p, i, i, p, sz, p, p], i),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -323,3 +330,123 @@ def moe_route_backward(dw, topk_w, topk_ids, x, w_router, offsets, perm, dlogits
             _flat(fn, dev, offsets, "offsets", (E + 1,), i32), _flat(fn, dev, perm, "perm", (T * k,), i32), T, k, E, H,
             _flat(fn, dev, dlogits, "dlogits", (T, k)), pd, ldd, dty, pa, lda, pw, ldw,
             _flat(fn, dev, dbias, "dbias", (E,)), ws, nbytes, _flat(fn, dev, dev_status, "dev_status", (1,), i32)))
+
+
+def _groups(H):
+    return -(-H // GROUP)
+
+
+def moe_checkpoint_save(x, q, exp, stream=None):
+    """x's rows into 8 bits: q [T,H] int8 whole numbers, exp [T, ceil(H/32)] uint8, the power of two (+127) that 32
+    adjacent columns share."""
+    fn = "moe_checkpoint_save"
+    T, H, ty, dev = _matrix(fn, x, "x")
+    px, ldx = _rows(fn, dev, x, "x", T, H, x.dtype)
+    pq, ldq = _rows(fn, dev, q, "q", T, H, torch.int8)
+    pe, lde = _rows(fn, dev, exp, "exp", T, _groups(H), torch.uint8)
+    _issue(fn, dev, stream, (px, ldx, ty, T, H, pq, ldq, pe, lde))
+
+
+def moe_checkpoint_load(q, exp, out, inv_perm=None, w=None, dev_status=None, stream=None):
+    """The rows that moe_checkpoint_save kept: out [T,H], or with inv_perm [T,k] moe_dispatch of them (out [R,H])."""
+    fn = "moe_checkpoint_load"
+    if q.dim() != 2 or out.dim() != 2:
+        _no(fn, MOE_ESHAPE, "q and out must be two-dimensional")
+    T, H = q.shape
+    dev, ty = q.get_device(), _type(fn, out, "out")
+    pq, ldq = _rows(fn, dev, q, "q", T, H, torch.int8)
+    pe, lde = _rows(fn, dev, exp, "exp", T, _groups(H), torch.uint8)
+    k, R, inv = 1, T, None
+    if inv_perm is not None:
+        k, inv = _routes(fn, dev, inv_perm, T)
+        R = len(out)
+    elif w is not None:
+        _no(fn, MOE_EINVAL, "w without inv_perm")
+    po, ldo = _rows(fn, dev, out, "out", R, H, out.dtype)
+    _issue(fn, dev, stream, (pq, ldq, pe, lde, T, H, inv, _flat(fn, dev, w, "w", (T, k)), k, R, po, ldo, ty,
+                             _flat(fn, dev, dev_status, "dev_status", (1,), torch.int32)))
+
+
+def _act(fn, dev, act, act_exp, R, I):
+    """(pointer, kind, row stride, pointer and row stride of the exponents)."""
+    if act is None:
+        if act_exp is not None:
+            _no(fn, MOE_EINVAL, "act_exp without act")
+        return None, MOE_ACT_NONE, 0, None, 0
+    if act.dtype is torch.bfloat16:
+        if act_exp is not None:
+            _no(fn, MOE_EINVAL, "act_exp with bfloat16 act")
+        pa, lda = _rows(fn, dev, act, "act", R, 2 * I, torch.bfloat16)
+        return pa, MOE_ACT_BF16, lda, None, 0
+    pa, lda = _rows(fn, dev, act, "act", R, 2 * I, torch.int8)
+    if act_exp is None:
+        _no(fn, MOE_EINVAL, "int8 act needs act_exp")
+    return (pa, MOE_ACT_Q8, lda) + _rows(fn, dev, act_exp, "act_exp", R, 2 * _groups(I), torch.uint8)
+
+
+def _experts(fn, dev, w_gateup, w_down, offsets):
+    """(E, H, I, pointers of both weights and of the offsets)."""
+    some = w_gateup if w_gateup is not None else w_down
+    if some is None or some.dim() != 3:
+        _no(fn, MOE_ESHAPE, "w_gateup must be [E, 2I, H], w_down [E, H, I]")
+    E = some.shape[0]
+    H, I = (some.shape[2], some.shape[1] // 2) if w_gateup is not None else some.shape[1:]
+    return (E, H, I, _flat(fn, dev, w_gateup, "w_gateup", (E, 2 * I, H), torch.bfloat16),
+            _flat(fn, dev, w_down, "w_down", (E, H, I), torch.bfloat16),
+            _flat(fn, dev, offsets, "offsets", (E + 1,), torch.int32))
+
+
+def moe_ffn(x_perm, w_gateup, w_down, offsets, h, y_perm, act=None, act_exp=None, dev_status=None, stream=None):
+    """y = W_down (silu(W_gate x) * (W_up x)) for every expert's rows (offsets), keeping gate and up values.
+
+    x_perm, y_perm [R,H] (y of either type, or None: only h and act), h [R,I]
+    bf16 scratch.  act: None, [R,2I] bf16, or [R,2I] int8 with act_exp
+    [R, 2 ceil(I/32)] uint8 (each half as moe_checkpoint_save keeps it).
+    """
+    fn = "moe_ffn"
+    R, _, _, dev = _matrix(fn, x_perm, "x_perm")
+    if w_gateup is None:
+        _no(fn, MOE_EINVAL, "w_gateup is None")
+    E, H, I, pgu, pdn, off = _experts(fn, dev, w_gateup, w_down, offsets)
+    px, ldx = _rows(fn, dev, x_perm, "x_perm", R, H, torch.bfloat16)
+    py, ldy = _rows(fn, dev, y_perm, "y_perm", R, H, y_perm.dtype if y_perm is not None else None)
+    yty = _type(fn, y_perm, "y_perm") if y_perm is not None else MOE_ROW_BF16
+    _issue(fn, dev, stream, (px, ldx, pgu, pdn, off, R, E, H, I, _flat(fn, dev, h, "h", (R, I), torch.bfloat16))
+           + _act(fn, dev, act, act_exp, R, I)
+           + (py, ldy, yty, _flat(fn, dev, dev_status, "dev_status", (1,), torch.int32)))
+
+
+def moe_ffn_backward_workspace_size(R, I):
+    return load().moe_ffn_backward_workspace_size(R, I)
+
+
+def moe_ffn_backward(dy_perm, x_perm, act, w_gateup, w_down, offsets, dx_perm, dw_gateup, dw_down, workspace,
+                     act_exp=None, accumulate=False, dev_status=None, stream=None):
+    """Gradients of moe_ffn from dy_perm and the act (and act_exp) that it kept.
+
+    dx_perm [R,H], dw_gateup [E,2I,H] and dw_down [E,H,I] may be None; the
+    weight gradients are of one type, fp32 or bf16, and are added to what they
+    hold with accumulate.  x_perm may be None without dw_gateup.
+    """
+    fn = "moe_ffn_backward"
+    R, _, _, dev = _matrix(fn, dy_perm, "dy_perm")
+    if act is None or w_down is None:
+        _no(fn, MOE_EINVAL, "act or w_down is None")
+    E, H, I, pgu, pdn, off = _experts(fn, dev, w_gateup, w_down, offsets)
+    bf = torch.bfloat16
+    pdy, lddy = _rows(fn, dev, dy_perm, "dy_perm", R, H, bf)
+    px, ldx = _rows(fn, dev, x_perm, "x_perm", R, H, bf)
+    dxty, pdx, lddx = MOE_ROW_BF16, None, 0
+    if dx_perm is not None:
+        dxty = _type(fn, dx_perm, "dx_perm")
+        pdx, lddx = _rows(fn, dev, dx_perm, "dx_perm", R, H, dx_perm.dtype)
+    some = dw_gateup if dw_gateup is not None else dw_down
+    wty, wt = (_type(fn, some, "dw_gateup" if dw_gateup is not None else "dw_down"), some.dtype) if some is not None \
+        else (MOE_ROW_BF16, None)
+    pa, kind, lda, pe, lde = _act(fn, dev, act, act_exp, R, I)
+    ws, nbytes = _bytes(fn, dev, workspace, "workspace")
+    _issue(fn, dev, stream,
+           (pdy, lddy, px, ldx, pa, kind, lda, pe, lde, pgu, pdn, off, R, E, H, I, pdx, lddx, dxty,
+            _flat(fn, dev, dw_gateup, "dw_gateup", (E, 2 * I, H), wt),
+            _flat(fn, dev, dw_down, "dw_down", (E, H, I), wt), wty, bool(accumulate), ws, nbytes,
+            _flat(fn, dev, dev_status, "dev_status", (1,), torch.int32)))

@@ -32,6 +32,7 @@ int sm_count() {
 
 namespace {
 
+using moe::blk::Bytes;
 using moe::blk::Rows;
 
 constexpr int kMaxH = 65536;      // the row movements
@@ -54,6 +55,17 @@ inline moe_status check_rows(const Rows& r, int64_t n, int H) {
   return MOE_OK;
 }
 
+inline Bytes bytes(const void* p, int64_t ld) {
+  return Bytes{const_cast<uint8_t*>(static_cast<const uint8_t*>(p)), ld};
+}
+inline moe_status check_bytes(const Bytes& b, int64_t n, int width) {
+  if (b.p == nullptr) return MOE_OK;
+  if (b.ld < width) return MOE_ESHAPE;
+  if (n > 0 && b.ld > (INT64_MAX / 8) / n) return MOE_ENOTSUP;
+  return MOE_OK;
+}
+inline int groups(int H) { return (H + 31) / 32; }
+
 inline moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ECUDA; }
 
 #define MOE_TRY(expr)                 \
@@ -68,6 +80,27 @@ moe_status check_routes(int T, int k, int H, int R, const int32_t* slots, const 
   if (T > 0 && !slots) return MOE_EINVAL;
   if (!a4(slots) || !a4(w) || !a4(status)) return MOE_EINVAL;
   return MOE_OK;
+}
+
+// The contractions read and write whole 16-byte pieces.
+moe_status check_operand(const Rows& r, int64_t n, int H) {
+  MOE_TRY(check_rows(r, n, H));
+  return r.p == nullptr || (aligned(r.p, 16) && r.ld % 8 == 0) ? MOE_OK : MOE_EINVAL;
+}
+
+moe_status check_ffn(int R, int E, int H, int I, const int32_t* offsets, const int32_t* status) {
+  if (R < 0 || E <= 0 || H <= 0 || I <= 0) return MOE_ESHAPE;
+  if (E > moe::kMaxE || H > kMaxH || I > kMaxH || H % 8 != 0 || I % 8 != 0 || R > kMaxT) return MOE_ENOTSUP;
+  return a4(offsets) && a4(status) ? MOE_OK : MOE_EINVAL;
+}
+
+moe_status check_act(void* act, int kind, int64_t ld, uint8_t* exp, int64_t ld_exp, int R, int I, moe::blk::Act* out) {
+  if (kind != MOE_ACT_NONE && kind != MOE_ACT_BF16 && kind != MOE_ACT_Q8) return MOE_EINVAL;
+  *out = moe::blk::Act{act, kind, ld, bytes(exp, ld_exp)};
+  if (kind == MOE_ACT_NONE) return act ? MOE_EINVAL : MOE_OK;
+  if (kind == MOE_ACT_BF16) return check_operand(rows(act, ld, MOE_ROW_BF16), R, 2 * I);
+  MOE_TRY(check_bytes(bytes(act, ld), R, 2 * I));
+  return check_bytes(out->exp, R, 2 * groups(I));
 }
 
 }  // namespace
@@ -321,6 +354,126 @@ moe_status moe_route_backward(const float* dw, const float* topk_w, const int32_
   a.ws = workspace;
   a.status = dev_status;
   return cuda_status(moe::blk::launch_route_grad(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_checkpoint_save(const void* x, int64_t ldx, int row_type, int T, int H, int8_t* q, int64_t ldq,
+                               uint8_t* exp, int64_t ld_exp, void* stream) {
+  if (T < 0 || H <= 0) return MOE_ESHAPE;
+  if (H > kMaxH || T > kMaxT) return MOE_ENOTSUP;
+  if (!type_ok(row_type)) return MOE_EINVAL;
+  const Rows rx = rows(x, ldx, row_type);
+  const Bytes bq = bytes(q, ldq), be = bytes(exp, ld_exp);
+  MOE_TRY(check_rows(rx, T, H));
+  MOE_TRY(check_bytes(bq, T, H));
+  MOE_TRY(check_bytes(be, T, groups(H)));
+  if (T == 0) return MOE_OK;
+  if (!x || !q || !exp || x == q || x == exp || bq.p == be.p) return MOE_EINVAL;
+  return cuda_status(moe::blk::launch_checkpoint_save(rx, T, H, bq, be, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_checkpoint_load(const int8_t* q, int64_t ldq, const uint8_t* exp, int64_t ld_exp, int T, int H,
+                               const int32_t* inv_perm, const float* w, int k, int R, void* out, int64_t ld_out,
+                               int row_type, int32_t* dev_status, void* stream) {
+  if (!inv_perm) k = 1, R = T;
+  if (!type_ok(row_type)) return MOE_EINVAL;
+  if (T < 0 || k <= 0 || H <= 0 || R < 0) return MOE_ESHAPE;
+  if (k > moe::kMaxK || H > kMaxH || T > kMaxT || static_cast<long long>(T) * k >= (1LL << 31)) return MOE_ENOTSUP;
+  if (!a4(inv_perm) || !a4(w) || !a4(dev_status) || (w && !inv_perm)) return MOE_EINVAL;
+  const Rows ro = rows(out, ld_out, row_type);
+  const Bytes bq = bytes(q, ldq), be = bytes(exp, ld_exp);
+  MOE_TRY(check_rows(ro, R, H));
+  MOE_TRY(check_bytes(bq, T, H));
+  MOE_TRY(check_bytes(be, T, groups(H)));
+  if (T == 0) return MOE_OK;
+  if (!q || !exp || (R > 0 && !out) || out == q || out == exp) return MOE_EINVAL;
+  return cuda_status(moe::blk::launch_checkpoint_load(bq, be, T, H, inv_perm, w, k, R, ro, dev_status,
+                                                      static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_ffn(const uint16_t* x_perm, int64_t ldx, const uint16_t* w_gateup, const uint16_t* w_down,
+                   const int32_t* offsets, int R, int E, int H, int I, uint16_t* h, void* act, int act_kind,
+                   int64_t ld_act, uint8_t* act_exp, int64_t ld_exp, void* y_perm, int64_t ldy, int y_type,
+                   int32_t* dev_status, void* stream) {
+  MOE_TRY(check_ffn(R, E, H, I, offsets, dev_status));
+  if (!type_ok(y_type)) return MOE_EINVAL;
+  moe::blk::FfnArgs a{};
+  a.x = rows(x_perm, ldx, MOE_ROW_BF16);
+  a.y = rows(y_perm, ldy, y_type);
+  MOE_TRY(check_operand(a.x, R, H));
+  MOE_TRY(check_operand(a.y, R, H));
+  MOE_TRY(check_act(act, act_kind, ld_act, act_exp, ld_exp, R, I, &a.act));
+  if (R == 0) return MOE_OK;
+  if (!x_perm || !w_gateup || !h || !offsets || (y_perm && !w_down) || (act_kind != MOE_ACT_NONE && !act))
+    return MOE_EINVAL;
+  if (act_kind == MOE_ACT_Q8 && !act_exp) return MOE_EINVAL;
+  if (!aligned(w_gateup, 16) || !aligned(w_down, 16) || !aligned(h, 16)) return MOE_EINVAL;
+  for (const void* out : {static_cast<const void*>(h), static_cast<const void*>(act), static_cast<const void*>(y_perm)})
+    if (out && (out == x_perm || out == w_gateup || out == w_down)) return MOE_EINVAL;
+  if (h == y_perm || h == act || (act && act == y_perm)) return MOE_EINVAL;
+  a.w_gateup = w_gateup;
+  a.w_down = w_down;
+  a.offsets = offsets;
+  a.R = R;
+  a.E = E;
+  a.H = H;
+  a.I = I;
+  a.h = h;
+  a.status = dev_status;
+  return cuda_status(moe::blk::launch_ffn(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_ffn_backward_workspace_size(int R, int I) {
+  if (R < 0 || I <= 0 || I > kMaxH) return 0;
+  return (static_cast<size_t>(R) * 3 * I * 2 + 15) / 16 * 16;
+}
+
+moe_status moe_ffn_backward(const uint16_t* dy_perm, int64_t lddy, const uint16_t* x_perm, int64_t ldx,
+                            const void* act, int act_kind, int64_t ld_act, const uint8_t* act_exp, int64_t ld_exp,
+                            const uint16_t* w_gateup, const uint16_t* w_down, const int32_t* offsets, int R, int E,
+                            int H, int I, void* dx_perm, int64_t lddx, int dx_type, void* dw_gateup, void* dw_down,
+                            int dw_type, int accumulate, void* workspace, size_t workspace_bytes,
+                            int32_t* dev_status, void* stream) {
+  MOE_TRY(check_ffn(R, E, H, I, offsets, dev_status));
+  if (!type_ok(dx_type) || !type_ok(dw_type) || act_kind == MOE_ACT_NONE) return MOE_EINVAL;
+  moe::blk::FfnGradArgs a{};
+  a.dy = rows(dy_perm, lddy, MOE_ROW_BF16);
+  a.x = rows(dw_gateup ? x_perm : nullptr, ldx, MOE_ROW_BF16);
+  a.dx = rows(dx_perm, lddx, dx_type);
+  MOE_TRY(check_operand(a.dy, R, H));
+  MOE_TRY(check_operand(a.x, R, H));
+  MOE_TRY(check_operand(a.dx, R, H));
+  MOE_TRY(check_act(const_cast<void*>(act), act_kind, ld_act, const_cast<uint8_t*>(act_exp), ld_exp, R, I, &a.act));
+  if (!dx_perm && !dw_gateup && !dw_down) return MOE_EINVAL;
+  if (!aligned(dw_gateup, 32) || !aligned(dw_down, 32) || (dw_gateup && dw_gateup == dw_down)) return MOE_EINVAL;
+  if (R > 0) {
+    if (!dy_perm || !act || !w_down || !offsets || (dx_perm && !w_gateup) || (dw_gateup && !x_perm)) return MOE_EINVAL;
+    if (act_kind == MOE_ACT_Q8 && !act_exp) return MOE_EINVAL;
+    if (!aligned(w_gateup, 16) || !aligned(w_down, 16)) return MOE_EINVAL;
+    for (const void* out : {static_cast<const void*>(dx_perm), static_cast<const void*>(dw_gateup),
+                            static_cast<const void*>(dw_down), static_cast<const void*>(workspace)})
+      if (out && (out == dy_perm || out == x_perm || out == act || out == w_gateup || out == w_down))
+        return MOE_EINVAL;
+    if (!workspace) return MOE_EWORKSPACE;
+    if (!aligned(workspace, 16)) return MOE_EINVAL;
+    if (workspace_bytes < moe_ffn_backward_workspace_size(R, I)) return MOE_EWORKSPACE;
+    if (dx_perm && (dx_perm == dw_gateup || dx_perm == dw_down)) return MOE_EINVAL;
+    if (workspace == dx_perm || workspace == dw_gateup || workspace == dw_down) return MOE_EINVAL;
+  }
+  a.w_gateup = w_gateup;
+  a.w_down = w_down;
+  a.offsets = offsets;
+  a.R = R;
+  a.E = E;
+  a.H = H;
+  a.I = I;
+  a.dw_gateup = dw_gateup;
+  a.dw_down = dw_down;
+  a.dw_type = dw_type;
+  a.accumulate = accumulate != 0;
+  a.da = static_cast<uint16_t*>(workspace);
+  a.h = a.da + static_cast<size_t>(R) * 2 * I;
+  a.status = dev_status;
+  return cuda_status(moe::blk::launch_ffn_grad(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

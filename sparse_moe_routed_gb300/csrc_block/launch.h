@@ -108,5 +108,48 @@ struct RouteGradArgs {
 size_t route_grad_ws_bytes(int T, int k, int E, int H);
 cudaError_t launch_route_grad(const RouteGradArgs& a, cudaStream_t st);
 
+// checkpoint.cu.  q [T,H] int8, exp [T, ceil(H/32)]: rows of bytes.
+struct Bytes {
+  uint8_t* p;
+  int64_t ld;
+};
+cudaError_t launch_checkpoint_save(const Rows& x, int T, int H, const Bytes& q, const Bytes& exp, cudaStream_t st);
+// slot_of NULL: out [T,H]
+cudaError_t launch_checkpoint_load(const Bytes& q, const Bytes& exp, int T, int H, const int32_t* slot_of,
+                                   const float* w, int k, int R, const Rows& out, int32_t* status, cudaStream_t st);
+
+// ffn.cu
+struct Act {
+  void* p;
+  int kind;
+  int64_t ld;
+  Bytes exp;
+};
+struct FfnArgs {
+  Rows x;
+  const uint16_t *w_gateup, *w_down;
+  const int32_t* offsets;
+  int R, E, H, I;
+  uint16_t* h;  // [R,I]
+  Act act;
+  Rows y;
+  int32_t* status;
+};
+cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st);
+
+struct FfnGradArgs {
+  Rows dy, x;
+  const uint16_t *w_gateup, *w_down;
+  const int32_t* offsets;
+  int R, E, H, I;
+  Act act;
+  Rows dx;
+  void *dw_gateup, *dw_down;
+  int dw_type, accumulate;
+  uint16_t *da, *h;  // workspace: [R,2I], [R,I]
+  int32_t* status;
+};
+cudaError_t launch_ffn_grad(const FfnGradArgs& a, cudaStream_t st);
+
 }  // namespace blk
 }  // namespace moe
