@@ -1,8 +1,33 @@
-// The experts' feed-forward block for training, and its gradient: six
-// contractions per expert, from operands in shared memory on the CUDA cores.
+// The experts' feed-forward block for training, and its gradient, on the
+// tensor cores.
+//
+// Six contractions per expert over its rows (slots s of one segment):
+//   gate/up   [g;u] = W_gu x            features x rows, sum over H
+//   down      y  = W_d h                features x rows, sum over I
+//   dh        dh = W_d^T dy             features x rows, sum over H
+//   dx        dx = W_gu^T [dg;du]       features x rows, sum over 2I
+//   dW_gu     [dg;du] x^T               features x features, sum over rows
+//   dW_d      dy h^T                    features x features, sum over rows
+// One persistent kernel template computes all of them.  Two CTAs on neighbouring
+// SMs work on one 256 x N tile (tcgen05 cta_group::2): each loads 128 rows of the
+// first operand and N/2 of the second per step of 64, so that a step of a
+// 256 x 256 tile moves 32 KB into each SM for 512 cycles of MMA; a CTA alone on
+// 128 x 256 would need 48 KB, more than L2 delivers at that rate.  The features
+// are the MMA's M (they come in whole tiles), an expert's rows its N, which can
+// be any multiple of 32 up to 256: experts of a few hundred rows waste little.
+//
+// Warp 0 of each CTA loads operands by TMA into six stages; warp 1 of the even
+// CTA issues the MMAs for both, warp 1 of the odd one passes on that its half of
+// a stage has arrived; warps 2 to 9 turn accumulators into results while the
+// next tile's MMAs run (two accumulators of 256 columns fill tensor memory).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <mutex>
 
 #include "launch.h"
+#include "pair.cuh"
 #include "q8.cuh"
 #include "rows.cuh"
 
@@ -11,158 +36,593 @@ namespace blk {
 
 namespace {
 
-constexpr int kTile = 64, kStep = 16;
+enum Mode { kGateUp, kDown, kDh, kDx, kGrad };
 
-struct P {
-  const uint16_t *a, *b;  // operands: a weights (weight gradients: the output's rows)
-  int64_t lda, ldb;
-  const int32_t* offsets;
-  int R, E, H, I;
-  void* out;
-  int64_t ld_out;
-  int out_type, accumulate;
-  Act act;
-  uint16_t *da, *h;
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kStages = 6;
+constexpr int kK = 64;  // contraction per stage: one 128-byte swizzled row
+constexpr int kABytes = 128 * kK * 2, kBBytes = 128 * kK * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kRowBox = 32;                     // rows of the second operand per copy
+constexpr int kSwap = 2 * 2 * 2 * 2 * 8 * 32;   // floats: (group, pair of warps, parity, direction, row, lane)
+constexpr int kBars = 3 * kStages + 4 + 1;
+constexpr int kSmem = 1024 + kStages * kStageBytes + kSwap * 4 + kBars * 8 + 16 + 2 * (kMaxE + 1) * 4;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+struct Out {
+  void* p;
+  int64_t ld;
+  int type;
 };
 
-enum { kGateUp, kDown, kDh, kDx, kDwGateUp, kDwDown };
+struct P {
+  const int32_t* offsets;
+  int R, E, H, I;
+  Out out;            // down, dx
+  Act act;            // gate/up, dh
+  uint16_t *da, *h;   // gate/up: h; dh: both
+  void *dwgu, *dwd;   // weight gradients (either may be null)
+  int dw_type, accumulate;
+  int32_t* status;
+};
 
-__device__ __forceinline__ int seg(const P& p, int e) { return min(max(p.offsets[e], 0), p.R); }
+inline __host__ __device__ int up(int a, int b) { return (a + b - 1) / b; }
 
-__device__ __forceinline__ void put_any(void* out, int type, int64_t i, float v, int accumulate) {
-  if (type == MOE_ROW_F32) {
-    float* o = static_cast<float*>(out) + i;
-    *o = accumulate ? *o + v : v;
+// Columns of a gradient tile: as even as multiples of 32 allow.
+inline __host__ __device__ int tile_cols(int n) { return up(up(n, up(n, 256)), 32) * 32; }
+
+struct Tile {
+  int e;
+  int m0;       // first feature (of the pair)
+  int n0;       // first row, or first column of a gradient
+  int n;        // rows or columns of the tile
+  int N;        // n up to a multiple of 32
+  int s0;       // gradient: first row of the sum
+  int k;        // contraction length
+  bool down;    // gradient: dW_d
+};
+
+// The tiles of a launch: for rows, expert by expert, at most kBand row chunks at
+// a time for all features (their rows stay in L2 while the weights stream); for
+// gradients, expert by expert.
+constexpr int kBand = 8;
+
+template <int MODE>
+struct Sched {
+  const int* first;  // tiles before each expert
+  const int* off;
+  int mt;            // 256-feature tiles (gate/up: 128 gate and 128 up)
+  int tgu, tall;     // gradient: tiles of dW_gu per expert, of both
+  int total;
+  const P& p;
+
+  __device__ __forceinline__ Sched(const P& p_, const int* first_, const int* off_) : first(first_), off(off_), p(p_) {
+    const int H = p.H, I = p.I;
+    mt = MODE == kGateUp ? up(I, 128) : MODE == kDh ? up(I, 256) : up(H, 256);
+    tgu = MODE == kGrad && p.dwgu != nullptr ? up(2 * I, 256) * up(H, tile_cols(H)) : 0;
+    tall = tgu + (MODE == kGrad && p.dwd != nullptr ? up(H, 256) * up(I, tile_cols(I)) : 0);
+    total = 0;
+  }
+
+  __device__ __forceinline__ Tile tile(int t) const {
+    Tile r;
+    if (MODE == kGrad) {
+      r.e = t / tall;
+      int l = t - r.e * tall;
+      r.down = l >= tgu;
+      if (r.down) l -= tgu;
+      const int cols = r.down ? p.I : p.H, tc = tile_cols(cols), nt = up(cols, tc);
+      r.m0 = l / nt * 256;
+      r.n0 = l % nt * tc;
+      r.n = min(tc, cols - r.n0);
+      r.s0 = off[r.e];
+      r.k = max(off[r.e + 1] - r.s0, 0);
+    } else {
+      int lo = 0, hi = p.E;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= t) lo = mid; else hi = mid;
+      }
+      r.e = lo;
+      const int s0 = off[lo], len = off[lo + 1] - s0, chunks = up(len, 256);
+      const int each = up(up(len, chunks), 32) * 32;
+      int l = t - first[lo];
+      const int band = l / (kBand * mt), in_band = min(kBand, chunks - band * kBand);
+      l -= band * kBand * mt;
+      const int c = band * kBand + l % in_band;
+      r.m0 = l / in_band * (MODE == kGateUp ? 128 : 256);
+      r.n0 = s0 + c * each;
+      r.n = min(each, len - c * each);
+      r.s0 = 0;
+      r.down = false;
+      r.k = MODE == kGateUp || MODE == kDh ? p.H : MODE == kDown ? p.I : 2 * p.I;
+    }
+    r.N = up(r.n, 32) * 32;
+    return r;
+  }
+};
+
+template <int MODE>
+constexpr bool kAMn = MODE == kDh || MODE == kDx || MODE == kGrad;  // features contiguous
+constexpr bool b_mn(int mode) { return mode == kGrad; }
+
+struct Pipe {
+  uint32_t s = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == kStages) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// --------------------------------------------------------------- epilogues
+// Each thread holds one feature (lane of tensor memory) of `C` rows.
+
+// Results of down and dx: rows of features; a warp writes 32 adjacent features.
+__device__ __forceinline__ void store_rows(const Out& o, const float (&v)[32], int64_t row, int n, int col, int width) {
+  if (col >= width) return;
+  if (o.type == MOE_ROW_F32) {
+    float* q = static_cast<float*>(o.p) + row * o.ld + col;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) q[j * o.ld] = v[j];
   } else {
-    uint16_t* o = static_cast<uint16_t*>(out) + i;
-    *o = f32_to_bf16(accumulate ? bf16_to_f32(*o) + v : v);
+    uint16_t* q = static_cast<uint16_t*>(o.p) + row * o.ld + col;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) put(q + j * o.ld, v[j]);
   }
 }
 
-// grid (tiles of m, [tiles of n,] experts).  m: features; n: the expert's slots, or for a weight gradient the
-// output's columns, with the slots as k.
+// 32 adjacent columns of a row of a weight gradient, n of them (a multiple of 8)
+// inside.
+__device__ __forceinline__ void store_grad(const P& p, void* base, float (&v)[32], int64_t at, int n) {
+  if (p.dw_type == MOE_ROW_F32) {
+    float* q = static_cast<float*>(base) + at;
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+      if (j >= n) break;
+      Raw8<float> r;
+      if (p.accumulate) {
+        load_vec(q + j, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j + i] += r.v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.v[i] = v[j + i];
+      store_vec(q + j, r);
+    }
+  } else {
+    bf16_t* q = static_cast<bf16_t*>(base) + at;
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+      if (j >= n) break;
+      Raw8<bf16_t> r;
+      if (p.accumulate) {
+        load_vec(q + j, r);
+        const V8 old = unpack(r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j + i] += el(old, i);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.v[i] = pack2(v[j + 2 * i], v[j + 2 * i + 1]);
+      store_vec(q + j, r);
+    }
+  }
+}
+
+__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + expf(-g)); }
+
+// Gate and up values of 8 rows, one feature per lane: h, and what is kept.
+__device__ __forceinline__ void gate_up(const P& p, const float (&g)[8], const float (&u)[8], int64_t row, int n, int i) {
+  const int I = p.I, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j >= n) break;
+    const int64_t s = row + j;
+    if (p.act.kind == MOE_ACT_Q8) {
+      const uint32_t eg = exp_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(g[j]) & 0x7fffffffu));
+      const uint32_t eu = exp_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(u[j]) & 0x7fffffffu));
+      uint8_t* q = static_cast<uint8_t*>(p.act.p) + s * p.act.ld;
+      if (i < I) {
+        q[i] = static_cast<uint8_t>(to_q8(g[j], inv_scale(eg)));
+        q[I + i] = static_cast<uint8_t>(to_q8(u[j], inv_scale(eu)));
+        uint8_t* x = p.act.exp.p + s * p.act.exp.ld + i / kGroup;
+        if (lane < 2) x[lane == 0 ? 0 : up(I, kGroup)] = static_cast<uint8_t>(lane == 0 ? eg : eu);
+      }
+    } else if (p.act.kind == MOE_ACT_BF16 && i < I) {
+      uint16_t* a = static_cast<uint16_t*>(p.act.p) + s * p.act.ld + i;
+      put(a, g[j]);
+      put(a + I, u[j]);
+    }
+    if (i < I) put(p.h + s * I + i, g[j] * sigmoid(g[j]) * u[j]);
+  }
+}
+
+// dh of 16 rows, one feature per lane: dg, du and h from the kept values.
+__device__ __forceinline__ void d_gate_up(const P& p, const float (&dh)[16], int64_t row, int n, int i) {
+  const int I = p.I;
+  if (i >= I) return;
+  float g[16], u[16];
+  if (p.act.kind == MOE_ACT_Q8) {
+    const int G = up(I, kGroup);
+    const int8_t* q = static_cast<const int8_t*>(p.act.p) + row * p.act.ld + i;
+    const uint8_t* x = p.act.exp.p + row * p.act.exp.ld + i / kGroup;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (j < n) {
+        g[j] = static_cast<float>(q[j * p.act.ld]) * scale_of(x[j * p.act.exp.ld]);
+        u[j] = static_cast<float>(q[j * p.act.ld + I]) * scale_of(x[j * p.act.exp.ld + G]);
+      }
+    }
+  } else {
+    const uint16_t* a = static_cast<const uint16_t*>(p.act.p) + row * p.act.ld + i;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (j < n) {
+        g[j] = bf16_to_f32(a[j * p.act.ld]);
+        u[j] = bf16_to_f32(a[j * p.act.ld + I]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (j >= n) break;
+    const float r = sigmoid(g[j]), gr = g[j] * r;
+    uint16_t* d = p.da + (row + j) * 2 * I + i;
+    put(d, dh[j] * u[j] * (r + gr * (1.f - r)));
+    put(d + I, dh[j] * gr);
+    put(p.h + (row + j) * I + i, gr * u[j]);
+  }
+}
+
+// ------------------------------------------------------------------ kernel
 template <int MODE>
-__global__ void __launch_bounds__(256) ffn_simple_kernel(P p) {
-  __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1], sc[kTile][kTile + 1];
+__global__ void __launch_bounds__(kThreads, 1)
+    ffn_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+               const __grid_constant__ CUtensorMap ma2, const __grid_constant__ CUtensorMap mb2,
+               const __grid_constant__ P p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - ptx::smem_u32(smem_raw));
+  float* swap = reinterpret_cast<float*>(sm + kStages * kStageBytes);
+  const uint32_t bars = base + kStages * kStageBytes + kSwap * 4;
+  const uint32_t full = bars, empty = bars + 8 * kStages, pfull = bars + 16 * kStages, accfull = bars + 24 * kStages,
+                 accempty = accfull + 16, done = accempty + 16;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(sm + kStages * kStageBytes + kSwap * 4 + kBars * 8);
+  volatile uint32_t* abort = misc + 1;
+  int* soff = reinterpret_cast<int*>(misc + 4);
+  int* first = soff + kMaxE + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = pair::cta_rank();
+  if (threadIdx.x == 0) {
+    misc[1] = 0;
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(full + 8 * i, 1);
+      ptx::mbar_init(empty + 8 * i, 1);
+      ptx::mbar_init(pfull + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(accfull + 8 * i, 1);
+      ptx::mbar_init(accempty + 8 * i, 2 * kEpiWarps);
+    }
+    ptx::mbar_init(done, 1);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) pair::tmem_alloc(ptx::smem_u32(misc));
+  ptx::tc_fence_before();
+  pair::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = misc[0];
+
   pdl_wait();
-  constexpr bool kW = MODE == kDwGateUp || MODE == kDwDown;
-  const int e = kW ? blockIdx.z : blockIdx.y, tid = threadIdx.x;
-  const int s0 = seg(p, e), n_e = max(seg(p, e + 1) - s0, 0);
-  const int I = p.I, H = p.H;
-  const int M = MODE == kGateUp || MODE == kDwGateUp ? 2 * I : MODE == kDh ? I : H;
-  const int K = kW ? n_e : MODE == kGateUp || MODE == kDh ? H : MODE == kDown ? I : 2 * I;
-  const int N = kW ? (MODE == kDwGateUp ? H : I) : n_e;
-  const int nstep = kW ? (N + kTile - 1) / kTile * kTile : kTile;
-  for (int n0 = kW ? blockIdx.y * kTile : 0; n0 < N; n0 += nstep) {
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += kStep) {
-      for (int i = tid; i < kTile * kStep; i += 256) {
-        const int r = MODE == kGateUp || MODE == kDown ? i / kStep : i % kTile;
-        const int c = MODE == kGateUp || MODE == kDown ? i % kStep : i / kTile;
-        const int k = k0 + c;
-        int m = blockIdx.x * kTile + r;
-        if (MODE == kGateUp) m = r < 32 ? blockIdx.x * 32 + r : I + blockIdx.x * 32 + r - 32;  // a gate half and its up half
-        const bool in = k < K && (MODE == kGateUp ? blockIdx.x * 32 + (r & 31) < I : m < M);
-        int64_t at;
-        if (MODE == kGateUp || MODE == kDown)
-          at = (static_cast<int64_t>(e) * M + m) * K + k;
-        else if (!kW)
-          at = (static_cast<int64_t>(e) * K + k) * M + m;
-        else
-          at = (s0 + k) * p.lda + m;
-        sa[c][r] = in ? bf16_to_f32(p.a[at]) : 0.f;
-        const int rb = kW ? i % kTile : i / kStep, cb = kW ? i / kTile : i % kStep;
-        const int n = n0 + rb, kb = k0 + cb;
-        sb[cb][rb] = n < N && kb < K ? bf16_to_f32(p.b[kW ? (s0 + kb) * p.ldb + n : (s0 + n) * p.ldb + kb]) : 0.f;
-      }
-      __syncthreads();
+  pdl_trigger();
+  // Offsets, kept inside the buffers and rising, whatever they hold.
+  for (int i = threadIdx.x; i <= p.E; i += kThreads) soff[i] = min(max(__ldcg(p.offsets + i), 0), p.R);
+  __syncthreads();
+  Sched<MODE> sc(p, first, soff);
+  if (MODE == kGrad) {
+    sc.total = sc.tall * p.E;
+  } else {
+    if (warp == 0) {
+      int running = 0;
+      for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const int e = e0 + lane;
+        const int n = e < p.E ? up(max(soff[e + 1] - soff[e], 0), 256) * sc.mt : 0;
+        int incl = n;
 #pragma unroll
-      for (int k = 0; k < kStep; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] += sa[k][tid % 16 + 16 * i] * sb[k][tid / 16 + 16 * j];
-      __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sc[tid / 16 + 16 * j][tid % 16 + 16 * i] = acc[i][j];
-    __syncthreads();
-    // a warp per n, its lanes along m
-    for (int n = tid / 32; n < kTile && n0 + n < N; n += 8) {
-      const int lane = tid & 31;
-      const int64_t s = s0 + n0 + n;
-      if (MODE == kGateUp) {
-        const int i = blockIdx.x * 32 + lane;
-        const float g = sc[n][lane], u = sc[n][lane + 32];
-        if (p.act.kind == MOE_ACT_Q8) {
-          const uint32_t eg = exp_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(g) & 0x7fffffffu));
-          const uint32_t eu = exp_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(u) & 0x7fffffffu));
-          const int G = (I + kGroup - 1) / kGroup;
-          uint8_t* q = static_cast<uint8_t*>(p.act.p) + s * p.act.ld;
-          uint8_t* ex = p.act.exp.p + s * p.act.exp.ld + blockIdx.x;
-          if (i < I) q[i] = static_cast<uint8_t>(to_q8(g, inv_scale(eg))), q[I + i] = static_cast<uint8_t>(to_q8(u, inv_scale(eu)));
-          if (lane == 0) ex[0] = static_cast<uint8_t>(eg), ex[G] = static_cast<uint8_t>(eu);
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += y;
         }
-        if (i >= I) continue;
-        if (p.act.kind == MOE_ACT_BF16) {
-          uint16_t* a = static_cast<uint16_t*>(p.act.p) + s * p.act.ld;
-          a[i] = f32_to_bf16(g);
-          a[I + i] = f32_to_bf16(u);
-        }
-        p.h[s * I + i] = f32_to_bf16(g / (1.f + expf(-g)) * u);
-        continue;
+        if (e < p.E) first[e] = running + incl - n;
+        running += __shfl_sync(0xffffffffu, incl, 31);
       }
-      for (int c = lane; c < kTile; c += 32) {
-        const int m = blockIdx.x * kTile + c;
-        if (m >= M) continue;
-        const float v = sc[n][c];
-        if (MODE == kDh) {
-          float g, u;
-          if (p.act.kind == MOE_ACT_Q8) {
-            const int G = (I + kGroup - 1) / kGroup;
-            const int8_t* q = static_cast<const int8_t*>(p.act.p) + s * p.act.ld;
-            const uint8_t* ex = p.act.exp.p + s * p.act.exp.ld + m / kGroup;
-            g = q[m] * scale_of(ex[0]);
-            u = q[I + m] * scale_of(ex[G]);
-          } else {
-            const uint16_t* a = static_cast<const uint16_t*>(p.act.p) + s * p.act.ld;
-            g = bf16_to_f32(a[m]);
-            u = bf16_to_f32(a[I + m]);
-          }
-          const float r = 1.f / (1.f + expf(-g));
-          p.da[s * 2 * I + m] = f32_to_bf16(v * u * r * (1.f + g * (1.f - r)));
-          p.da[s * 2 * I + I + m] = f32_to_bf16(v * g * r);
-          p.h[s * I + m] = f32_to_bf16(g * r * u);
-        } else if (kW) {
-          put_any(p.out, p.out_type, (static_cast<int64_t>(e) * M + m) * N + n0 + n, v, p.accumulate);
-        } else {
-          put_any(p.out, p.out_type, s * p.ld_out + m, v, 0);
-        }
-      }
+      if (lane == 0) misc[2] = running;
     }
     __syncthreads();
+    sc.total = misc[2];
   }
+  const int t0 = blockIdx.x >> 1, tstep = gridDim.x >> 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- operands
+    if (lane == 0) {
+      const uint64_t pol = ptx::policy_evict_normal();
+      Pipe pipe;
+      uint32_t used = 0;
+      bool ok = true;
+      for (int t = t0; t < sc.total && ok; t += tstep) {
+        const Tile tl = sc.tile(t);
+        const int half = tl.N / 2;
+        const CUtensorMap* a = MODE == kGrad && tl.down ? &ma2 : &ma;
+        const CUtensorMap* b = MODE == kGrad && tl.down ? &mb2 : &mb;
+        const int boxes = MODE == kGrad ? up(half, 64) : up(half, kRowBox);
+        const uint32_t bytes = kABytes + boxes * (MODE == kGrad ? 8192 : kRowBox * 128);
+        for (int k = 0; k < tl.k; k += kK) {
+          ok = pair::wait<0>(empty + 8 * pipe.s, pipe.ph ^ 1u, abort, p.status);
+          if (!ok) break;
+          const uint32_t bar = full + 8 * pipe.s, sa = base + pipe.s * kStageBytes, sb = sa + kABytes;
+          ptx::mbar_arrive_expect_tx(bar, bytes);
+          if (MODE == kGateUp) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // 32 gate rows, their 32 up rows, and again
+              ptx::tma_load_4d(sa + j * 4096, a, bar, k, tl.m0 + static_cast<int>(rank) * 64 + (j >> 1) * 32, j & 1, tl.e,
+                               pol);
+          } else if (MODE == kDown) {
+            pair::tma_load_3d(sa, a, bar, k, tl.m0 + static_cast<int>(rank) * 128, tl.e, pol);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int c = tl.m0 + static_cast<int>(rank) * 128 + j * 64;
+              if (MODE == kGrad)
+                ptx::tma_load_2d(sa + j * 8192, a, bar, c, tl.s0 + k, pol);
+              else
+                pair::tma_load_3d(sa + j * 8192, a, bar, c, k, tl.e, pol);
+            }
+          }
+          for (int j = 0; j < boxes; ++j) {
+            if (MODE == kGrad)
+              ptx::tma_load_2d(sb + j * 8192, b, bar, tl.n0 + static_cast<int>(rank) * half + j * 64, tl.s0 + k, pol);
+            else
+              ptx::tma_load_2d(sb + j * kRowBox * 128, b, bar, k, tl.n0 + static_cast<int>(rank) * half + j * kRowBox, pol);
+          }
+          pipe.next();
+          ++used;
+        }
+      }
+      // Nothing of this CTA is under way when it ends: every stage that was
+      // filled has been read (its release has arrived here), or, after an
+      // abort, its copies have landed.
+      for (uint32_t i = 0; i < kStages && i < used; ++i) {
+        const uint32_t s = (pipe.s + kStages - 1 - i) % kStages;
+        const uint32_t ph = s < pipe.s ? pipe.ph : pipe.ph ^ 1u;  // of the stage's last use
+        if (ok)
+          ok = pair::wait<64>(empty + 8 * s, ph, abort, p.status);
+        if (!ok) pair::drain(full + 8 * s, ph);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMAs, or relay
+    Pipe pipe;
+    int acc = 0;
+    uint32_t aph = 0;
+    bool ok = true;
+    for (int t = t0; t < sc.total && ok; t += tstep) {
+      const Tile tl = sc.tile(t);
+      if (tl.k == 0) continue;
+      const uint32_t id = pair::idesc(tl.N, kAMn<MODE>, b_mn(MODE));
+      const uint32_t d = tmem + acc * 256;
+      if (rank == 0) {
+        ok = pair::wait_warp<0>(accempty + 8 * acc, aph ^ 1u, abort, p.status);
+        if (!ok) break;
+        ptx::tc_fence_after();
+      }
+      for (int k = 0; k < tl.k; k += kK) {
+        ok = pair::wait_warp<0>(full + 8 * pipe.s, pipe.ph, abort, p.status);
+        if (!ok) break;
+        const uint32_t sa = base + pipe.s * kStageBytes, sb = sa + kABytes;
+        const int left = tl.k - k, steps = left >= kK ? kK / 16 : up(left, 16);
+        if (MODE == kGrad && left < kK && (left & 15) != 0) {
+          // Rows of the next expert (or none) stand behind the segment's last
+          // one: zeros, for whatever they hold times zero need not be zero.
+          const uint32_t at = sa + (lane >> 3) * 8192 + (lane & 7) * 16;
+          for (int r = left; r < steps * 16; ++r)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + r * 128), "r"(0) : "memory");
+          pair::fence_smem_async();
+        }
+        __syncwarp();
+        if (rank == 1) {
+          if (lane == 0) {
+            pair::fence_smem_async();
+            pair::arrive_at(pfull + 8 * pipe.s, 0);
+          }
+        } else {
+          ok = pair::wait_warp<0>(pfull + 8 * pipe.s, pipe.ph, abort, p.status);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (lane == 0) {
+            for (int kk = 0; kk < steps; ++kk)
+              pair::mma(d, kAMn<MODE> ? pair::sdesc_mn_sw128(sa + kk * 2048) : ptx::sdesc_k_sw128(sa + kk * 32),
+                        b_mn(MODE) ? pair::sdesc_mn_sw128(sb + kk * 2048) : ptx::sdesc_k_sw128(sb + kk * 32), id,
+                        (k | kk) != 0 ? 1u : 0u);
+            pair::commit_both(empty + 8 * pipe.s);
+          }
+          __syncwarp();
+        }
+        pipe.next();
+      }
+      if (rank == 0 && ok && lane == 0) pair::commit_both(accfull + 8 * acc);
+      acc ^= 1;
+      if (acc == 0) aph ^= 1u;
+    }
+    if (!ok && rank == 0 && lane == 0) {  // the MMAs that were issued
+      pair::commit_both(done);
+      pair::drain(done, 0);
+    }
+  } else {
+    // -------------------------------------------------------------- results
+    const int q = warp & 3, group = (warp - 2) >> 2;
+    int acc = 0;
+    uint32_t aph = 0, turn = 0;
+    for (int t = t0; t < sc.total; t += tstep) {
+      const Tile tl = sc.tile(t);
+      if (tl.k != 0) {
+        if (!pair::wait_warp<32>(accfull + 8 * acc, aph, abort, p.status)) break;
+        ptx::tc_fence_after();
+      }
+      const uint32_t d = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
+      if (MODE == kGateUp) {
+        // Even warps hold 32 gate features, odd ones the same up features: of
+        // 16 rows each gives the other eight.
+        const int i = tl.m0 + static_cast<int>(rank) * 64 + (q >> 1) * 32 + lane;
+        float* mine = swap + ((group * 2 + (q >> 1)) * 2 * 2) * 256;
+        for (int c = group * 16; c < tl.N; c += 32) {
+          float v[16];
+          ptx::tmem_ld16(d + c, v);
+          float* out = mine + (turn * 2 + (q & 1)) * 256 + lane;
+          const float* in = mine + (turn * 2 + (1 - (q & 1))) * 256 + lane;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) out[j * 32] = (q & 1) ? v[j] : v[8 + j];
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + group * 2 + (q >> 1)) : "memory");
+          float g[8], u[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float o = in[j * 32];
+            g[j] = (q & 1) ? o : v[j];
+            u[j] = (q & 1) ? v[8 + j] : o;
+          }
+          turn ^= 1u;
+          const int c8 = c + (q & 1) * 8;
+          gate_up(p, g, u, static_cast<int64_t>(tl.n0) + c8, tl.n - c8, i);
+        }
+      } else if (MODE == kDh) {
+        const int i = tl.m0 + static_cast<int>(rank) * 128 + q * 32 + lane;
+        for (int c = group * 16; c < tl.n; c += 32) {
+          float v[16];
+          ptx::tmem_ld16(d + c, v);
+          d_gate_up(p, v, static_cast<int64_t>(tl.n0) + c, tl.n - c, i);
+        }
+      } else if (MODE == kGrad) {
+        const int m = tl.m0 + static_cast<int>(rank) * 128 + q * 32 + lane;
+        const int M = tl.down ? p.H : 2 * p.I, cols = tl.down ? p.I : p.H;
+        if (tl.k != 0 || !p.accumulate) {
+          for (int c = group * 32; c < tl.n; c += 64) {
+            float v[32];
+            if (tl.k != 0) {
+              pair::tmem_ld32(d + c, v);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            }
+            if (m < M)
+              store_grad(p, tl.down ? p.dwd : p.dwgu, v, (static_cast<int64_t>(tl.e) * M + m) * cols + tl.n0 + c,
+                         tl.n - c);
+          }
+        }
+      } else {
+        const int m = tl.m0 + static_cast<int>(rank) * 128 + q * 32 + lane;
+        for (int c = group * 32; c < tl.n; c += 64) {
+          float v[32];
+          pair::tmem_ld32(d + c, v);
+          store_rows(p.out, v, static_cast<int64_t>(tl.n0) + c, tl.n - c, m, p.H);
+        }
+      }
+      if (tl.k != 0) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) pair::arrive_at(accempty + 8 * acc, 0);
+        acc ^= 1;
+        if (acc == 0) aph ^= 1u;
+      }
+    }
+  }
+
+  __syncwarp();
+  ptx::tc_fence_before();
+  pair::cluster_sync();
+  ptx::tc_fence_after();
+  if (warp == 1) pair::tmem_dealloc(tmem);
 }
 
-inline int up(int a, int b) { return (a + b - 1) / b; }
+// ------------------------------------------------------------------ host
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// bf16 tensor, innermost dimension first (its elements adjacent), boxes of 64
+// elements x box1 x ...; reads outside give zeros.
+bool make_map(CUtensorMap* m, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* stride_elems,
+              cuuint32_t box1) {
+  const auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t strides[3];
+  for (int i = 0; i + 1 < rank; ++i) strides[i] = stride_elems[i] * 2;
+  const cuuint32_t box[4] = {kK, box1, 1, 1}, ones[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(p), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map_rows(CUtensorMap* m, const void* p, int64_t ld, int R, int width, int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(R)};
+  const cuuint64_t str[1] = {static_cast<cuuint64_t>(R > 1 ? ld : up(width, 8) * 8)};
+  return make_map(m, p, 2, dims, str, box_rows);
+}
+
+// [E][rows][width], contiguous
+bool map_weights(CUtensorMap* m, const void* p, int E, int rows, int width, int box_rows) {
+  const cuuint64_t w = width, r = rows;
+  const cuuint64_t dims[3] = {w, r, static_cast<cuuint64_t>(E)};
+  const cuuint64_t str[2] = {w, w * r};
+  return make_map(m, p, 3, dims, str, box_rows);
+}
 
 template <int MODE>
-cudaError_t go(const P& p, cudaStream_t st) {
-  const dim3 grid = MODE == kGateUp     ? dim3(up(p.I, 32), p.E)
-                    : MODE == kDh       ? dim3(up(p.I, kTile), p.E)
-                    : MODE == kDwGateUp ? dim3(up(2 * p.I, kTile), up(p.H, kTile), p.E)
-                    : MODE == kDwDown   ? dim3(up(p.H, kTile), up(p.I, kTile), p.E)
-                                        : dim3(up(p.H, kTile), p.E);
-  return launch_pdl(ffn_simple_kernel<MODE>, grid, dim3(256), 0, st, p);
+cudaError_t go(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2, const CUtensorMap& b2, const P& p,
+               int64_t tiles, cudaStream_t st) {
+  auto kern = ffn_kernel<MODE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  const int64_t pairs = std::max(1, sm_count() / 2);
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, tiles)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a, b, a2, b2, p);
 }
 
-#define FFN_TRY(call)                            \
-  do {                                           \
-    const cudaError_t e_ = (call);               \
-    if (e_ != cudaSuccess) return e_;            \
+// Tiles of rows that R rows of E experts can have at most.
+inline int64_t row_tiles(int R, int E, int mt) { return static_cast<int64_t>(mt) * (up(R, 256) + std::min(R, E)); }
+
+#define FFN_TRY(call)                 \
+  do {                                \
+    const cudaError_t e_ = (call);    \
+    if (e_ != cudaSuccess) return e_; \
   } while (0)
+#define FFN_MAP(call) \
+  if (!(call)) return cudaErrorInvalidValue
 
 }  // namespace
 
@@ -170,20 +630,20 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st) {
   P p{};
   p.offsets = a.offsets;
   p.R = a.R, p.E = a.E, p.H = a.H, p.I = a.I;
-  p.a = a.w_gateup;
-  p.b = static_cast<const uint16_t*>(a.x.p);
-  p.ldb = a.x.ld;
   p.act = a.act;
   p.h = a.h;
-  FFN_TRY(go<kGateUp>(p, st));
+  p.status = a.status;
+  CUtensorMap ma, mb;
+  const cuuint64_t H = a.H, I = a.I;
+  const cuuint64_t dims[4] = {H, I, 2, static_cast<cuuint64_t>(a.E)}, str[3] = {H, H * I, 2 * H * I};
+  FFN_MAP(make_map(&ma, a.w_gateup, 4, dims, str, 32));
+  FFN_MAP(map_rows(&mb, a.x.p, a.x.ld, a.R, a.H, kRowBox));
+  FFN_TRY(go<kGateUp>(ma, mb, ma, mb, p, row_tiles(a.R, a.E, up(a.I, 128)), st));
   if (a.y.p == nullptr) return cudaSuccess;
-  p.a = a.w_down;
-  p.b = a.h;
-  p.ldb = a.I;
-  p.out = a.y.p;
-  p.ld_out = a.y.ld;
-  p.out_type = a.y.type;
-  return go<kDown>(p, st);
+  p.out = Out{a.y.p, a.y.ld, a.y.type};
+  FFN_MAP(map_weights(&ma, a.w_down, a.E, a.H, a.I, 128));
+  FFN_MAP(map_rows(&mb, a.h, a.I, a.R, a.I, kRowBox));
+  return go<kDown>(ma, mb, ma, mb, p, row_tiles(a.R, a.E, up(a.H, 256)), st);
 }
 
 cudaError_t launch_ffn_grad(const FfnGradArgs& a, cudaStream_t st) {
@@ -196,41 +656,36 @@ cudaError_t launch_ffn_grad(const FfnGradArgs& a, cudaStream_t st) {
   P p{};
   p.offsets = a.offsets;
   p.R = a.R, p.E = a.E, p.H = a.H, p.I = a.I;
-  p.a = a.w_down;
-  p.b = static_cast<const uint16_t*>(a.dy.p);
-  p.ldb = a.dy.ld;
   p.act = a.act;
   p.da = a.da;
   p.h = a.h;
-  FFN_TRY(go<kDh>(p, st));
+  p.status = a.status;
+  CUtensorMap ma, mb, ma2, mb2;
+  FFN_MAP(map_weights(&ma, a.w_down, a.E, a.H, a.I, 64));
+  FFN_MAP(map_rows(&mb, a.dy.p, a.dy.ld, a.R, a.H, kRowBox));
+  FFN_TRY(go<kDh>(ma, mb, ma, mb, p, row_tiles(a.R, a.E, up(a.I, 256)), st));
   if (a.dx.p != nullptr) {
-    p.a = a.w_gateup;
-    p.b = a.da;
-    p.ldb = 2 * a.I;
-    p.out = a.dx.p;
-    p.ld_out = a.dx.ld;
-    p.out_type = a.dx.type;
-    FFN_TRY(go<kDx>(p, st));
+    p.out = Out{a.dx.p, a.dx.ld, a.dx.type};
+    FFN_MAP(map_weights(&ma, a.w_gateup, a.E, 2 * a.I, a.H, 64));
+    FFN_MAP(map_rows(&mb, a.da, 2 * a.I, a.R, 2 * a.I, kRowBox));
+    FFN_TRY(go<kDx>(ma, mb, ma, mb, p, row_tiles(a.R, a.E, up(a.H, 256)), st));
   }
-  p.out_type = a.dw_type;
+  if (a.dw_gateup == nullptr && a.dw_down == nullptr) return cudaSuccess;
+  p.dwgu = a.dw_gateup;
+  p.dwd = a.dw_down;
+  p.dw_type = a.dw_type;
   p.accumulate = a.accumulate;
+  int64_t tiles = 0;
   if (a.dw_gateup != nullptr) {
-    p.a = a.da;
-    p.lda = 2 * a.I;
-    p.b = static_cast<const uint16_t*>(a.x.p);
-    p.ldb = a.x.ld;
-    p.out = a.dw_gateup;
-    FFN_TRY(go<kDwGateUp>(p, st));
+    FFN_MAP(map_rows(&ma, a.da, 2 * a.I, a.R, 2 * a.I, 64));
+    FFN_MAP(map_rows(&mb, a.x.p, a.x.ld, a.R, a.H, 64));
+    tiles += static_cast<int64_t>(up(2 * a.I, 256)) * up(a.H, tile_cols(a.H));
   }
-  if (a.dw_down != nullptr) {
-    p.a = static_cast<const uint16_t*>(a.dy.p);
-    p.lda = a.dy.ld;
-    p.b = a.h;
-    p.ldb = a.I;
-    p.out = a.dw_down;
-    FFN_TRY(go<kDwDown>(p, st));
-  }
-  return cudaSuccess;
+  FFN_MAP(map_rows(&ma2, a.dy.p, a.dy.ld, a.R, a.H, 64));
+  FFN_MAP(map_rows(&mb2, a.h, a.I, a.R, a.I, 64));
+  if (a.dw_down != nullptr) tiles += static_cast<int64_t>(up(a.H, 256)) * up(a.I, tile_cols(a.I));
+  if (a.dw_gateup == nullptr) ma = ma2, mb = mb2;
+  return go<kGrad>(ma, mb, ma2, mb2, p, tiles * a.E, st);
 }
 
 }  // namespace blk
