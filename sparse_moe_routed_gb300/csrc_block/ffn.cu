@@ -16,10 +16,11 @@
 // are the MMA's M (they come in whole tiles), an expert's rows its N, which can
 // be any multiple of 32 up to 256: experts of a few hundred rows waste little.
 //
-// Warp 0 of each CTA loads operands by TMA into six stages; warp 1 of the even
-// CTA issues the MMAs for both, warp 1 of the odd one passes on that its half of
-// a stage has arrived; warps 2 to 9 turn accumulators into results while the
-// next tile's MMAs run (two accumulators of 256 columns fill tensor memory).
+// Warp 0 of each CTA loads operands by TMA into six stages, counted on the even
+// CTA's barriers; warp 1 of the even CTA issues the MMAs for both; warps 2 to 9
+// turn accumulators into results while the next tile's MMAs run (two
+// accumulators of 256 columns fill tensor memory).  Where a sum over rows ends
+// inside 16 of them, warp 1 of each CTA first clears the rows behind in its half.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -45,7 +46,7 @@ constexpr int kK = 64;  // contraction per stage: one 128-byte swizzled row
 constexpr int kABytes = 128 * kK * 2, kBBytes = 128 * kK * 2, kStageBytes = kABytes + kBBytes;
 constexpr int kRowBox = 32;                     // rows of the second operand per copy
 constexpr int kSwap = 2 * 2 * 2 * 2 * 8 * 32;   // floats: (group, pair of warps, parity, direction, row, lane)
-constexpr int kBars = 3 * kStages + 4 + 1;
+constexpr int kBars = 4 * kStages + 4 + 1;
 constexpr int kSmem = 1024 + kStages * kStageBytes + kSwap * 4 + kBars * 8 + 16 + 2 * (kMaxE + 1) * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
@@ -145,6 +146,9 @@ struct Sched {
 template <int MODE>
 constexpr bool kAMn = MODE == kDh || MODE == kDx || MODE == kGrad;  // features contiguous
 constexpr bool b_mn(int mode) { return mode == kGrad; }
+
+// Whether a sum over rows, `left` of them in this stage, ends inside a step of 16.
+__device__ __forceinline__ bool ends_inside(int left) { return left < kK && (left & 15) != 0; }
 
 struct Pipe {
   uint32_t s = 0, ph = 0;
@@ -288,8 +292,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sm = smem_raw + (base - ptx::smem_u32(smem_raw));
   float* swap = reinterpret_cast<float*>(sm + kStages * kStageBytes);
   const uint32_t bars = base + kStages * kStageBytes + kSwap * 4;
-  const uint32_t full = bars, empty = bars + 8 * kStages, pfull = bars + 16 * kStages, accfull = bars + 24 * kStages,
-                 accempty = accfull + 16, done = accempty + 16;
+  // full: both halves of a stage (even CTA).  Where the rows behind a sum are
+  // cleared: full, the even half alone; tfull, the odd half (odd CTA); ready, the
+  // odd half cleared (even CTA).
+  const uint32_t full = bars, empty = bars + 8 * kStages, ready = bars + 16 * kStages, tfull = bars + 24 * kStages,
+                 accfull = bars + 32 * kStages, accempty = accfull + 16, done = accempty + 16;
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + kStages * kStageBytes + kSwap * 4 + kBars * 8);
   volatile uint32_t* abort = misc + 1;
   int* soff = reinterpret_cast<int*>(misc + 4);
@@ -302,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(full + 8 * i, 1);
       ptx::mbar_init(empty + 8 * i, 1);
-      ptx::mbar_init(pfull + 8 * i, 1);
+      ptx::mbar_init(ready + 8 * i, 1);
+      ptx::mbar_init(tfull + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(accfull + 8 * i, 1);
@@ -364,30 +372,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < tl.k; k += kK) {
           ok = pair::wait<0>(empty + 8 * pipe.s, pipe.ph ^ 1u, abort, p.status);
           if (!ok) break;
-          const uint32_t bar = full + 8 * pipe.s, sa = base + pipe.s * kStageBytes, sb = sa + kABytes;
-          ptx::mbar_arrive_expect_tx(bar, bytes);
+          const uint32_t sa = base + pipe.s * kStageBytes, sb = sa + kABytes;
+          const bool alone = MODE == kGrad && ends_inside(tl.k - k);
+          uint32_t bar = full + 8 * pipe.s;
+          if (alone && rank == 1) bar = tfull + 8 * pipe.s;
+          if (alone || rank == 0) ptx::mbar_arrive_expect_tx(bar, alone ? bytes : 2 * bytes);
+          bar = pair::at_rank(bar, alone ? rank : 0);
           if (MODE == kGateUp) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)  // 32 gate rows, their 32 up rows, and again
-              ptx::tma_load_4d(sa + j * 4096, a, bar, k, tl.m0 + static_cast<int>(rank) * 64 + (j >> 1) * 32, j & 1, tl.e,
-                               pol);
+              pair::tma_4d(sa + j * 4096, a, bar, k, tl.m0 + static_cast<int>(rank) * 64 + (j >> 1) * 32, j & 1, tl.e,
+                           pol);
           } else if (MODE == kDown) {
-            pair::tma_load_3d(sa, a, bar, k, tl.m0 + static_cast<int>(rank) * 128, tl.e, pol);
+            pair::tma_3d(sa, a, bar, k, tl.m0 + static_cast<int>(rank) * 128, tl.e, pol);
           } else {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int c = tl.m0 + static_cast<int>(rank) * 128 + j * 64;
               if (MODE == kGrad)
-                ptx::tma_load_2d(sa + j * 8192, a, bar, c, tl.s0 + k, pol);
+                pair::tma_2d(sa + j * 8192, a, bar, c, tl.s0 + k, pol);
               else
-                pair::tma_load_3d(sa + j * 8192, a, bar, c, k, tl.e, pol);
+                pair::tma_3d(sa + j * 8192, a, bar, c, k, tl.e, pol);
             }
           }
           for (int j = 0; j < boxes; ++j) {
             if (MODE == kGrad)
-              ptx::tma_load_2d(sb + j * 8192, b, bar, tl.n0 + static_cast<int>(rank) * half + j * 64, tl.s0 + k, pol);
+              pair::tma_2d(sb + j * 8192, b, bar, tl.n0 + static_cast<int>(rank) * half + j * 64, tl.s0 + k, pol);
             else
-              ptx::tma_load_2d(sb + j * kRowBox * 128, b, bar, k, tl.n0 + static_cast<int>(rank) * half + j * kRowBox, pol);
+              pair::tma_2d(sb + j * kRowBox * 128, b, bar, k, tl.n0 + static_cast<int>(rank) * half + j * kRowBox, pol);
           }
           pipe.next();
           ++used;
@@ -401,16 +413,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ph = s < pipe.s ? pipe.ph : pipe.ph ^ 1u;  // of the stage's last use
         if (ok)
           ok = pair::wait<64>(empty + 8 * s, ph, abort, p.status);
-        if (!ok) pair::drain(full + 8 * s, ph);
+        if (!ok && rank == 0) pair::drain(full + 8 * s, ph);
       }
+      if (!ok && rank == 1) pair::pause_10ms();
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------ MMAs, or relay
+    // ----------------------------------------------------------------- MMAs
     Pipe pipe;
     int acc = 0;
-    uint32_t aph = 0;
+    uint32_t aph = 0, tph = 0;  // tph: a bit per stage, the phase of its ready / tfull
     bool ok = true;
     for (int t = t0; t < sc.total && ok; t += tstep) {
+      if (MODE != kGrad && rank == 1) break;
       const Tile tl = sc.tile(t);
       if (tl.k == 0) continue;
       const uint32_t id = pair::idesc(tl.N, kAMn<MODE>, b_mn(MODE));
@@ -421,27 +435,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
       }
       for (int k = 0; k < tl.k; k += kK) {
-        ok = pair::wait_warp<0>(full + 8 * pipe.s, pipe.ph, abort, p.status);
-        if (!ok) break;
-        const uint32_t sa = base + pipe.s * kStageBytes, sb = sa + kABytes;
         const int left = tl.k - k, steps = left >= kK ? kK / 16 : up(left, 16);
-        if (MODE == kGrad && left < kK && (left & 15) != 0) {
+        const uint32_t sa = base + pipe.s * kStageBytes, sb = sa + kABytes;
+        const bool alone = MODE == kGrad && ends_inside(left);
+        if (rank == 0 || alone) {
+          ok = rank == 0 ? pair::wait_warp<0>(full + 8 * pipe.s, pipe.ph, abort, p.status)
+                         : pair::wait_warp<0>(tfull + 8 * pipe.s, (tph >> pipe.s) & 1u, abort, p.status);
+          if (!ok) break;
+        }
+        if (alone) {
           // Rows of the next expert (or none) stand behind the segment's last
           // one: zeros, for whatever they hold times zero need not be zero.
           const uint32_t at = sa + (lane >> 3) * 8192 + (lane & 7) * 16;
           for (int r = left; r < steps * 16; ++r)
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + r * 128), "r"(0) : "memory");
           pair::fence_smem_async();
-        }
-        __syncwarp();
-        if (rank == 1) {
-          if (lane == 0) {
-            pair::fence_smem_async();
-            pair::arrive_at(pfull + 8 * pipe.s, 0);
+          __syncwarp();
+          if (rank == 1) {
+            if (lane == 0) pair::arrive_at(ready + 8 * pipe.s, 0);
+          } else {
+            ok = pair::wait_warp<0>(ready + 8 * pipe.s, (tph >> pipe.s) & 1u, abort, p.status);
+            if (!ok) break;
           }
-        } else {
-          ok = pair::wait_warp<0>(pfull + 8 * pipe.s, pipe.ph, abort, p.status);
-          if (!ok) break;
+          tph ^= 1u << pipe.s;
+        }
+        if (rank == 0) {
           ptx::tc_fence_after();
           if (lane == 0) {
             for (int kk = 0; kk < steps; ++kk)
@@ -597,19 +615,23 @@ cudaError_t go(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int64_t pairs = std::max(1, sm_count() / 2);
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, tiles)));
+  cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int pairs = 0;
+  e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+  if (e != cudaSuccess) return e;
   cfg.numAttrs = 2;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(std::max(pairs, 1), tiles)));
   return cudaLaunchKernelEx(&cfg, kern, a, b, a2, b2, p);
 }
 

@@ -27,12 +27,14 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Arrive on the barrier at the same place in CTA `rank` of the pair.
+// Arrive on the barrier at the same place in CTA `rank` of the pair.  (Release at
+// cluster scope would wait for everything this SM has under way: a microsecond.
+// What is handed over here goes by the async proxy's own order, or by a fence.)
 __device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\t"
       "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}\n" ::"r"(bar),
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}\n" ::"r"(bar),
       "r"(rank)
       : "memory");
 }
@@ -41,7 +43,7 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -71,13 +73,16 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uin
   }
 }
 
-// The same for a whole warp.
+// The same for a whole warp, of which one lane polls: polls by all lanes of ten
+// warps keep the barriers' unit busy enough to slow every arrival.
 template <uint32_t SLEEP_NS>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int32_t* status) {
-  return __all_sync(0xffffffffu, wait<SLEEP_NS>(bar, parity, abort, status));
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = wait<SLEEP_NS>(bar, parity, abort, status);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-// After an abort: for copies that are still on their way into this CTA.
+// After an abort: for copies and MMAs that are still under way.
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (!try_wait(bar, parity)) {
@@ -85,15 +90,45 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
     if (globaltimer_ns() - t0 > kWaitNs) return;
   }
 }
+// ... and for those that only the other CTA's barriers count: they land within
+// microseconds.
+__device__ __forceinline__ void pause_10ms() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 10000000ull) __nanosleep(1000);
+}
 
 __device__ __forceinline__ void fence_smem_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
-                                            uint64_t policy) {
+// Address in the pair of what lies at `addr` in CTA `rank`.
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+
+// Tile loads into this CTA whose bytes count on a barrier of either CTA of the
+// pair (`bar` from at_rank).
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
+                                       uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, int c3,
+                                       uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
       : "memory");
 }
 
