@@ -16,11 +16,12 @@
 // are the MMA's M (they come in whole tiles), an expert's rows its N, which can
 // be any multiple of 32 up to 256: experts of a few hundred rows waste little.
 //
-// Warp 0 of each CTA loads operands by TMA into six stages, counted on the even
-// CTA's barriers; warp 1 of the even CTA issues the MMAs for both; warps 2 to 9
-// turn accumulators into results while the next tile's MMAs run (two
-// accumulators of 256 columns fill tensor memory).  Where a sum over rows ends
-// inside 16 of them, warp 1 of each CTA first clears the rows behind in its half.
+// One thread of each CTA (warp 0) loads the first operand by TMA, one (warp 10)
+// the second, into six stages counted on the even CTA's barriers; one thread of
+// the even CTA (warp 1) issues the MMAs for both; warps 2 to 9 turn accumulators
+// into results while the next tile's MMAs run (two accumulators of 256 columns
+// fill tensor memory).  Where a sum over rows ends inside 16 of them, warp 11 of
+// each CTA first clears the rows behind in its half.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -39,15 +40,19 @@ namespace {
 
 enum Mode { kGateUp, kDown, kDh, kDx, kGrad };
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kStages = 6;
 constexpr int kK = 64;  // contraction per stage: one 128-byte swizzled row
 constexpr int kABytes = 128 * kK * 2, kBBytes = 128 * kK * 2, kStageBytes = kABytes + kBBytes;
-constexpr int kRowBox = 32;                     // rows of the second operand per copy
-constexpr int kSwap = 2 * 2 * 2 * 2 * 8 * 32;   // floats: (group, pair of warps, parity, direction, row, lane)
-constexpr int kBars = 4 * kStages + 4 + 1;
-constexpr int kSmem = 1024 + kStages * kStageBytes + kSwap * 4 + kBars * 8 + 16 + 2 * (kMaxE + 1) * 4;
+constexpr int kRowBox = 32;              // rows of the second operand per copy
+constexpr int kTurnRows = 16;            // rows that a warp turns at a time,
+constexpr int kTurnLd = 36;              // 32 features each: a row and 16 bytes, so that reads of 8 rows spread over the banks
+constexpr int kTurn = kTurnRows * kTurnLd;
+constexpr int kList = 128;               // tiles of a pair that are looked up ahead
+constexpr int kBars = 3 * kStages + 4 + 1;
+constexpr int kTail = kEpiWarps * kTurn * 4;
+constexpr int kSmem = 1024 + kStages * kStageBytes + kTail + kList * 16 + 16 + kBars * 8 + 8 + 2 * (kMaxE + 1) * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct Out {
@@ -95,9 +100,11 @@ struct Sched {
   int mt;            // 256-feature tiles (gate/up: 128 gate and 128 up)
   int tgu, tall;     // gradient: tiles of dW_gu per expert, of both
   int total;
+  const int4* list;  // the pair's first tiles: e, m0, n0, n
   const P& p;
 
-  __device__ __forceinline__ Sched(const P& p_, const int* first_, const int* off_) : first(first_), off(off_), p(p_) {
+  __device__ __forceinline__ Sched(const P& p_, const int* first_, const int* off_, const int4* list_)
+      : first(first_), off(off_), list(list_), p(p_) {
     const int H = p.H, I = p.I;
     mt = MODE == kGateUp ? up(I, 128) : MODE == kDh ? up(I, 256) : up(H, 256);
     tgu = MODE == kGrad && p.dwgu != nullptr ? up(2 * I, 256) * up(H, tile_cols(H)) : 0;
@@ -105,7 +112,27 @@ struct Sched {
     total = 0;
   }
 
-  __device__ __forceinline__ Tile tile(int t) const {
+  // The pair's j-th tile, tile t of all.
+  __device__ __forceinline__ Tile tile(int t, int j) const {
+    if (MODE == kGrad || j >= kList) return find(t);
+    const int4 v = list[j];
+    Tile r;
+    r.e = v.x;
+    r.m0 = v.y;
+    r.n0 = v.z;
+    r.n = v.w;
+    r.s0 = 0;
+    r.down = false;
+    r.k = length();
+    r.N = up(r.n, 32) * 32;
+    return r;
+  }
+
+  __device__ __forceinline__ int length() const {
+    return MODE == kGateUp || MODE == kDh ? p.H : MODE == kDown ? p.I : 2 * p.I;
+  }
+
+  __device__ __forceinline__ Tile find(int t) const {
     Tile r;
     if (MODE == kGrad) {
       r.e = t / tall;
@@ -136,7 +163,7 @@ struct Sched {
       r.n = min(each, len - c * each);
       r.s0 = 0;
       r.down = false;
-      r.k = MODE == kGateUp || MODE == kDh ? p.H : MODE == kDown ? p.I : 2 * p.I;
+      r.k = length();
     }
     r.N = up(r.n, 32) * 32;
     return r;
@@ -161,21 +188,39 @@ struct Pipe {
 };
 
 // --------------------------------------------------------------- epilogues
-// Each thread holds one feature (lane of tensor memory) of `C` rows.
+// Tensor memory gives a thread one feature of many rows.  Results are rows of
+// features, so a warp turns 16 rows of its 32 features in shared memory: four
+// lanes then have a row, eight features each, and global accesses are 16 bytes of
+// 64 adjacent ones instead of one element per lane.
+__device__ __forceinline__ void turn_in(float* buf, const float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) buf[j * kTurnLd + (threadIdx.x & 31)] = v[j];
+}
+__device__ __forceinline__ V8 turn_out(const float* buf, int row) {
+  const float4* q = reinterpret_cast<const float4*>(buf + row * kTurnLd + (threadIdx.x & 3) * 8);
+  const float4 a = q[0], b = q[1];
+  V8 v;
+  v.v[0] = make_float2(a.x, a.y);
+  v.v[1] = make_float2(a.z, a.w);
+  v.v[2] = make_float2(b.x, b.y);
+  v.v[3] = make_float2(b.z, b.w);
+  return v;
+}
 
-// Results of down and dx: rows of features; a warp writes 32 adjacent features.
-__device__ __forceinline__ void store_rows(const Out& o, const float (&v)[32], int64_t row, int n, int col, int width) {
-  if (col >= width) return;
+__device__ __forceinline__ void store_bf16(uint16_t* q, const V8& v) {
+  Raw8<bf16_t> r;
+  pack(v, r);
+  store_vec(q, r);
+}
+
+// Eight features of a row of down's or dx's result.
+__device__ __forceinline__ void store_row(const Out& o, const V8& v, int64_t row, int col) {
   if (o.type == MOE_ROW_F32) {
-    float* q = static_cast<float*>(o.p) + row * o.ld + col;
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) q[j * o.ld] = v[j];
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(o.p) + row * o.ld + col);
+    q[0] = make_float4(v.v[0].x, v.v[0].y, v.v[1].x, v.v[1].y);
+    q[1] = make_float4(v.v[2].x, v.v[2].y, v.v[3].x, v.v[3].y);
   } else {
-    uint16_t* q = static_cast<uint16_t*>(o.p) + row * o.ld + col;
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) put(q + j * o.ld, v[j]);
+    store_bf16(static_cast<uint16_t*>(o.p) + row * o.ld + col, v);
   }
 }
 
@@ -199,6 +244,19 @@ __device__ __forceinline__ void store_grad(const P& p, void* base, float (&v)[32
     }
   } else {
     bf16_t* q = static_cast<bf16_t*>(base) + at;
+    if (!p.accumulate && n >= 32 && (reinterpret_cast<uintptr_t>(q) & 31) == 0) {
+      // whole 32-byte sectors
+#pragma unroll
+      for (int j = 0; j < 32; j += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack2(v[j + 2 * i], v[j + 2 * i + 1]);
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(q + j), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+      }
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < 32; j += 8) {
       if (j >= n) break;
@@ -218,67 +276,126 @@ __device__ __forceinline__ void store_grad(const P& p, void* base, float (&v)[32
 
 __device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + expf(-g)); }
 
-// Gate and up values of 8 rows, one feature per lane: h, and what is kept.
-__device__ __forceinline__ void gate_up(const P& p, const float (&g)[8], const float (&u)[8], int64_t row, int n, int i) {
-  const int I = p.I, lane = threadIdx.x & 31;
+// Eight bytes of a row in 8 bits, at any alignment.
+__device__ __forceinline__ uint2 load_q8(const uint8_t* q, bool whole) {
+  if (whole) return *reinterpret_cast<const uint2*>(q);
+  uint2 v = make_uint2(0, 0);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (j >= n) break;
-    const int64_t s = row + j;
-    if (p.act.kind == MOE_ACT_Q8) {
-      const uint32_t eg = exp_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(g[j]) & 0x7fffffffu));
-      const uint32_t eu = exp_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(u[j]) & 0x7fffffffu));
-      uint8_t* q = static_cast<uint8_t*>(p.act.p) + s * p.act.ld;
-      if (i < I) {
-        q[i] = static_cast<uint8_t>(to_q8(g[j], inv_scale(eg)));
-        q[I + i] = static_cast<uint8_t>(to_q8(u[j], inv_scale(eu)));
-        uint8_t* x = p.act.exp.p + s * p.act.exp.ld + i / kGroup;
-        if (lane < 2) x[lane == 0 ? 0 : up(I, kGroup)] = static_cast<uint8_t>(lane == 0 ? eg : eu);
-      }
-    } else if (p.act.kind == MOE_ACT_BF16 && i < I) {
-      uint16_t* a = static_cast<uint16_t*>(p.act.p) + s * p.act.ld + i;
-      put(a, g[j]);
-      put(a + I, u[j]);
-    }
-    if (i < I) put(p.h + s * I + i, g[j] * sigmoid(g[j]) * u[j]);
+  for (int i = 0; i < 4; ++i) {
+    v.x |= static_cast<uint32_t>(q[i]) << (8 * i);
+    v.y |= static_cast<uint32_t>(q[4 + i]) << (8 * i);
+  }
+  return v;
+}
+__device__ __forceinline__ void store_q8(uint8_t* q, uint2 v, bool whole) {
+  if (whole) {
+    *reinterpret_cast<uint2*>(q) = v;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    q[i] = static_cast<uint8_t>(v.x >> (8 * i));
+    q[4 + i] = static_cast<uint8_t>(v.y >> (8 * i));
   }
 }
+__device__ __forceinline__ bool act_whole(const Act& a) {
+  return ((reinterpret_cast<uintptr_t>(a.p) | static_cast<uintptr_t>(a.ld)) & 7) == 0;
+}
 
-// dh of 16 rows, one feature per lane: dg, du and h from the kept values.
-__device__ __forceinline__ void d_gate_up(const P& p, const float (&dh)[16], int64_t row, int n, int i) {
+// Eight features of a group of 32 (four lanes) to 8 bits; their exponent byte.
+__device__ __forceinline__ uint2 to_bytes(const V8& v, uint32_t& e) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(el(v, i)) & 0x7fffffffu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  e = exp_byte(m);
+  const float inv = inv_scale(e);
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = static_cast<uint32_t>(to_q8(el(v, i), inv)) & 255u;
+  return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+}
+__device__ __forceinline__ V8 from_bytes(uint2 q, uint32_t e) {
+  const float s = scale_of(e);
+  V8 v;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    el(v, i) = static_cast<float>(static_cast<int8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)))) * s;
+  return v;
+}
+
+// Gate and up values, eight features i.. of row `row` (`in`: the row and the
+// features are there): h, and what is kept.
+__device__ __forceinline__ void gate_up(const P& p, const V8& g, const V8& u, int64_t row, int i, bool in) {
   const int I = p.I;
-  if (i >= I) return;
-  float g[16], u[16];
   if (p.act.kind == MOE_ACT_Q8) {
-    const int G = up(I, kGroup);
-    const int8_t* q = static_cast<const int8_t*>(p.act.p) + row * p.act.ld + i;
-    const uint8_t* x = p.act.exp.p + row * p.act.exp.ld + i / kGroup;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (j < n) {
-        g[j] = static_cast<float>(q[j * p.act.ld]) * scale_of(x[j * p.act.exp.ld]);
-        u[j] = static_cast<float>(q[j * p.act.ld + I]) * scale_of(x[j * p.act.exp.ld + G]);
-      }
-    }
-  } else {
-    const uint16_t* a = static_cast<const uint16_t*>(p.act.p) + row * p.act.ld + i;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (j < n) {
-        g[j] = bf16_to_f32(a[j * p.act.ld]);
-        u[j] = bf16_to_f32(a[j * p.act.ld + I]);
+    const bool whole = act_whole(p.act);
+    uint32_t eg, eu;
+    const uint2 qg = to_bytes(g, eg), qu = to_bytes(u, eu);
+    if (in) {
+      uint8_t* q = static_cast<uint8_t*>(p.act.p) + row * p.act.ld + i;
+      store_q8(q, qg, whole);
+      store_q8(q + I, qu, whole);
+      if ((threadIdx.x & 3) == 0) {
+        uint8_t* x = p.act.exp.p + row * p.act.exp.ld + i / kGroup;
+        x[0] = static_cast<uint8_t>(eg);
+        x[up(I, kGroup)] = static_cast<uint8_t>(eu);
       }
     }
   }
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (j >= n) break;
-    const float r = sigmoid(g[j]), gr = g[j] * r;
-    uint16_t* d = p.da + (row + j) * 2 * I + i;
-    put(d, dh[j] * u[j] * (r + gr * (1.f - r)));
-    put(d + I, dh[j] * gr);
-    put(p.h + (row + j) * I + i, gr * u[j]);
+  if (!in) return;
+  if (p.act.kind == MOE_ACT_BF16) {
+    uint16_t* a = static_cast<uint16_t*>(p.act.p) + row * p.act.ld + i;
+    store_bf16(a, g);
+    store_bf16(a + I, u);
   }
+  V8 h;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) el(h, j) = el(g, j) * sigmoid(el(g, j)) * el(u, j);
+  store_bf16(p.h + row * I + i, h);
+}
+
+// Kept gate and up values as they lie in memory: eight features of a row.
+struct Kept {
+  uint4 g, u;
+  __device__ __forceinline__ void load(const P& p, int64_t row, int i) {
+    if (p.act.kind == MOE_ACT_Q8) {
+      const bool whole = act_whole(p.act);
+      const uint8_t* q = static_cast<const uint8_t*>(p.act.p) + row * p.act.ld + i;
+      const uint8_t* x = p.act.exp.p + row * p.act.exp.ld + i / kGroup;
+      const uint2 a = load_q8(q, whole), b = load_q8(q + p.I, whole);
+      g = make_uint4(a.x, a.y, x[0], 0);
+      u = make_uint4(b.x, b.y, x[up(p.I, kGroup)], 0);
+    } else {
+      const uint16_t* a = static_cast<const uint16_t*>(p.act.p) + row * p.act.ld + i;
+      g = *reinterpret_cast<const uint4*>(a);
+      u = *reinterpret_cast<const uint4*>(a + p.I);
+    }
+  }
+  static __device__ __forceinline__ V8 value(const P& p, const uint4& r) {
+    if (p.act.kind == MOE_ACT_Q8) return from_bytes(make_uint2(r.x, r.y), r.z);
+    V8 v;
+    v.v[0] = widen(r.x);
+    v.v[1] = widen(r.y);
+    v.v[2] = widen(r.z);
+    v.v[3] = widen(r.w);
+    return v;
+  }
+};
+
+// dg, du and h of eight features of a row from dh and the kept values.
+__device__ __forceinline__ void d_gate_up(const P& p, const V8& dh, const Kept& k, int64_t row, int i) {
+  const V8 g = Kept::value(p, k.g), u = Kept::value(p, k.u);
+  V8 r;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) el(r, j) = sigmoid(el(g, j));
+  const V8 gr = g * r;
+  const V8 slope = fma8(gr * -1.f, r, gr + r);  // r + g r (1 - r)
+  uint16_t* d = p.da + row * 2 * p.I + i;
+  store_bf16(d, dh * u * slope);
+  store_bf16(d + p.I, dh * gr);
+  store_bf16(p.h + row * p.I + i, gr * u);
 }
 
 // ------------------------------------------------------------------ kernel
@@ -290,16 +407,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - ptx::smem_u32(smem_raw));
-  float* swap = reinterpret_cast<float*>(sm + kStages * kStageBytes);
-  const uint32_t bars = base + kStages * kStageBytes + kSwap * 4;
-  // full: both halves of a stage (even CTA).  Where the rows behind a sum are
-  // cleared: full, the even half alone; tfull, the odd half (odd CTA); ready, the
-  // odd half cleared (even CTA).
-  const uint32_t full = bars, empty = bars + 8 * kStages, ready = bars + 16 * kStages, tfull = bars + 24 * kStages,
-                 accfull = bars + 32 * kStages, accempty = accfull + 16, done = accempty + 16;
-  uint32_t* misc = reinterpret_cast<uint32_t*>(sm + kStages * kStageBytes + kSwap * 4 + kBars * 8);
+  float* turn = reinterpret_cast<float*>(sm + kStages * kStageBytes);
+  int4* list = reinterpret_cast<int4*>(sm + kStages * kStageBytes + kTail);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(list + kList);  // tensor memory, abort, tiles
   volatile uint32_t* abort = misc + 1;
-  int* soff = reinterpret_cast<int*>(misc + 4);
+  const uint32_t bars = ptx::smem_u32(misc + 4);
+  // full: both halves of a stage (even CTA); empty: both have been read (both);
+  // tfull: this CTA's half, where the rows behind a sum are cleared (both)
+  const uint32_t full = bars, empty = bars + 8 * kStages, tfull = bars + 16 * kStages, accfull = bars + 24 * kStages,
+                 accempty = accfull + 16, done = accempty + 16;
+  int* soff = reinterpret_cast<int*>(misc + 4 + 2 * kBars);
   int* first = soff + kMaxE + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -307,9 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     misc[1] = 0;
     for (int i = 0; i < kStages; ++i) {
-      ptx::mbar_init(full + 8 * i, 1);
+      ptx::mbar_init(full + 8 * i, MODE == kGrad ? 2 : 1);
       ptx::mbar_init(empty + 8 * i, 1);
-      ptx::mbar_init(ready + 8 * i, 1);
       ptx::mbar_init(tfull + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -330,7 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Offsets, kept inside the buffers and rising, whatever they hold.
   for (int i = threadIdx.x; i <= p.E; i += kThreads) soff[i] = min(max(__ldcg(p.offsets + i), 0), p.R);
   __syncthreads();
-  Sched<MODE> sc(p, first, soff);
+  Sched<MODE> sc(p, first, soff, list);
+  const int t0 = blockIdx.x >> 1, tstep = gridDim.x >> 1;
   if (MODE == kGrad) {
     sc.total = sc.tall * p.E;
   } else {
@@ -352,18 +469,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     sc.total = misc[2];
+    for (int j = threadIdx.x; j < kList && t0 + j * tstep < sc.total; j += kThreads) {
+      const Tile tl = sc.find(t0 + j * tstep);
+      list[j] = make_int4(tl.e, tl.m0, tl.n0, tl.n);
+    }
+    __syncthreads();
   }
-  const int t0 = blockIdx.x >> 1, tstep = gridDim.x >> 1;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 10) {
     // ------------------------------------------------------------- operands
     if (lane == 0) {
       const uint64_t pol = ptx::policy_evict_normal();
+      const int r = static_cast<int>(rank);
       Pipe pipe;
       uint32_t used = 0;
       bool ok = true;
-      for (int t = t0; t < sc.total && ok; t += tstep) {
-        const Tile tl = sc.tile(t);
+      for (int t = t0, j = 0; t < sc.total && ok; t += tstep, ++j) {
+        const Tile tl = sc.tile(t, j);
         const int half = tl.N / 2;
         const CUtensorMap* a = MODE == kGrad && tl.down ? &ma2 : &ma;
         const CUtensorMap* b = MODE == kGrad && tl.down ? &mb2 : &mb;
@@ -374,32 +496,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           const uint32_t sa = base + pipe.s * kStageBytes, sb = sa + kABytes;
           const bool alone = MODE == kGrad && ends_inside(tl.k - k);
-          uint32_t bar = full + 8 * pipe.s;
-          if (alone && rank == 1) bar = tfull + 8 * pipe.s;
-          if (alone || rank == 0) ptx::mbar_arrive_expect_tx(bar, alone ? bytes : 2 * bytes);
-          bar = pair::at_rank(bar, alone ? rank : 0);
-          if (MODE == kGateUp) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)  // 32 gate rows, their 32 up rows, and again
-              pair::tma_4d(sa + j * 4096, a, bar, k, tl.m0 + static_cast<int>(rank) * 64 + (j >> 1) * 32, j & 1, tl.e,
-                           pol);
-          } else if (MODE == kDown) {
-            pair::tma_3d(sa, a, bar, k, tl.m0 + static_cast<int>(rank) * 128, tl.e, pol);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int c = tl.m0 + static_cast<int>(rank) * 128 + j * 64;
-              if (MODE == kGrad)
-                pair::tma_2d(sa + j * 8192, a, bar, c, tl.s0 + k, pol);
-              else
-                pair::tma_3d(sa + j * 8192, a, bar, c, k, tl.e, pol);
-            }
+          uint32_t bar = (alone ? tfull : full) + 8 * pipe.s;
+          if (warp == 0) {
+            if (alone || rank == 0)
+              ptx::mbar_arrive_expect_tx(bar, alone ? bytes : 2 * bytes);
+            else if (MODE == kGrad)
+              pair::arrive_at(bar, 0);
           }
-          for (int j = 0; j < boxes; ++j) {
-            if (MODE == kGrad)
-              pair::tma_2d(sb + j * 8192, b, bar, tl.n0 + static_cast<int>(rank) * half + j * 64, tl.s0 + k, pol);
-            else
-              pair::tma_2d(sb + j * kRowBox * 128, b, bar, k, tl.n0 + static_cast<int>(rank) * half + j * kRowBox, pol);
+          bar = pair::at_rank(bar, alone ? rank : 0);
+          if (warp == 0) {
+            if (MODE == kGateUp) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)  // 32 gate rows, their 32 up rows, and again
+                pair::tma_4d(sa + i * 4096, a, bar, k, tl.m0 + r * 64 + (i >> 1) * 32, i & 1, tl.e, pol);
+            } else if (MODE == kDown) {
+              pair::tma_3d(sa, a, bar, k, tl.m0 + r * 128, tl.e, pol);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int c = tl.m0 + r * 128 + i * 64;
+                if (MODE == kGrad)
+                  pair::tma_2d(sa + i * 8192, a, bar, c, tl.s0 + k, pol);
+                else
+                  pair::tma_3d(sa + i * 8192, a, bar, c, k, tl.e, pol);
+              }
+            }
+          } else {
+            for (int i = 0; i < boxes; ++i) {
+              if (MODE == kGrad)
+                pair::tma_2d(sb + i * 8192, b, bar, tl.n0 + r * half + i * 64, tl.s0 + k, pol);
+              else
+                pair::tma_2d(sb + i * kRowBox * 128, b, bar, k, tl.n0 + r * half + i * kRowBox, pol);
+            }
           }
           pipe.next();
           ++used;
@@ -411,119 +539,94 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t i = 0; i < kStages && i < used; ++i) {
         const uint32_t s = (pipe.s + kStages - 1 - i) % kStages;
         const uint32_t ph = s < pipe.s ? pipe.ph : pipe.ph ^ 1u;  // of the stage's last use
-        if (ok)
-          ok = pair::wait<64>(empty + 8 * s, ph, abort, p.status);
-        if (!ok && rank == 0) pair::drain(full + 8 * s, ph);
+        if (ok) ok = pair::wait<64>(empty + 8 * s, ph, abort, p.status);
       }
-      if (!ok && rank == 1) pair::pause_10ms();
+      if (!ok) pair::pause_10ms();
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMAs
-    Pipe pipe;
-    int acc = 0;
-    uint32_t aph = 0, tph = 0;  // tph: a bit per stage, the phase of its ready / tfull
-    bool ok = true;
-    for (int t = t0; t < sc.total && ok; t += tstep) {
-      if (MODE != kGrad && rank == 1) break;
-      const Tile tl = sc.tile(t);
-      if (tl.k == 0) continue;
-      const uint32_t id = pair::idesc(tl.N, kAMn<MODE>, b_mn(MODE));
-      const uint32_t d = tmem + acc * 256;
-      if (rank == 0) {
-        ok = pair::wait_warp<0>(accempty + 8 * acc, aph ^ 1u, abort, p.status);
+    if (rank == 0 && lane == 0) {
+      Pipe pipe;
+      int acc = 0;
+      uint32_t aph = 0;
+      bool ok = true;
+      const uint64_t da0 = kAMn<MODE> ? pair::sdesc_mn_sw128(base) : ptx::sdesc_k_sw128(base);
+      const uint64_t db0 = b_mn(MODE) ? pair::sdesc_mn_sw128(base + kABytes) : ptx::sdesc_k_sw128(base + kABytes);
+      constexpr uint32_t kStepA = (kAMn<MODE> ? 2048 : 32) >> 4, kStepB = (b_mn(MODE) ? 2048 : 32) >> 4;
+      for (int t = t0, j = 0; t < sc.total && ok; t += tstep, ++j) {
+        const Tile tl = sc.tile(t, j);
+        if (tl.k == 0) continue;
+        const uint32_t id = pair::idesc(tl.N, kAMn<MODE>, b_mn(MODE));
+        const uint32_t d = tmem + acc * 256;
+        ok = pair::wait<0>(accempty + 8 * acc, aph ^ 1u, abort, p.status);
         if (!ok) break;
         ptx::tc_fence_after();
-      }
-      for (int k = 0; k < tl.k; k += kK) {
-        const int left = tl.k - k, steps = left >= kK ? kK / 16 : up(left, 16);
-        const uint32_t sa = base + pipe.s * kStageBytes, sb = sa + kABytes;
-        const bool alone = MODE == kGrad && ends_inside(left);
-        if (rank == 0 || alone) {
-          ok = rank == 0 ? pair::wait_warp<0>(full + 8 * pipe.s, pipe.ph, abort, p.status)
-                         : pair::wait_warp<0>(tfull + 8 * pipe.s, (tph >> pipe.s) & 1u, abort, p.status);
+        for (int left = tl.k; left > 0; left -= kK) {
+          ok = pair::wait<0>(full + 8 * pipe.s, pipe.ph, abort, p.status);
           if (!ok) break;
+          const uint64_t da = da0 + pipe.s * (kStageBytes >> 4), db = db0 + pipe.s * (kStageBytes >> 4);
+          pair::mma(d, da, db, id, left != tl.k);
+          if (left >= kK) {
+#pragma unroll
+            for (int kk = 1; kk < kK / 16; ++kk) pair::mma(d, da + kk * kStepA, db + kk * kStepB, id, 1);
+          } else {
+#pragma unroll
+            for (int kk = 1; kk < kK / 16; ++kk)
+              if (kk * 16 < left) pair::mma(d, da + kk * kStepA, db + kk * kStepB, id, 1);
+          }
+          pair::commit_both(empty + 8 * pipe.s);
+          pipe.next();
         }
-        if (alone) {
-          // Rows of the next expert (or none) stand behind the segment's last
-          // one: zeros, for whatever they hold times zero need not be zero.
-          const uint32_t at = sa + (lane >> 3) * 8192 + (lane & 7) * 16;
-          for (int r = left; r < steps * 16; ++r)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + r * 128), "r"(0) : "memory");
+        if (ok) pair::commit_both(accfull + 8 * acc);
+        acc ^= 1;
+        if (acc == 0) aph ^= 1u;
+      }
+      if (!ok) {  // the MMAs that were issued
+        pair::commit_both(done);
+        pair::drain(done, 0);
+      }
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------ rows behind a sum's last
+    if (MODE == kGrad) {
+      Pipe pipe;
+      uint32_t tph = 0;  // a bit per stage: the phase of its tfull
+      bool ok = true;
+      for (int t = t0, j = 0; t < sc.total && ok; t += tstep, ++j) {
+        const Tile tl = sc.tile(t, j);
+        for (int left = tl.k; left > 0; left -= kK, pipe.next()) {
+          if (!ends_inside(left)) continue;
+          ok = pair::wait_warp<0>(tfull + 8 * pipe.s, (tph >> pipe.s) & 1u, abort, p.status);
+          if (!ok) break;
+          tph ^= 1u << pipe.s;
+          // The next expert's rows stand there (or none): zeros, for whatever
+          // they hold times zero need not be zero.
+          const uint32_t at = base + pipe.s * kStageBytes + (lane >> 3) * 8192 + (lane & 7) * 16;
+          for (int i = left; i < up(left, 16) * 16; ++i)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * 128), "r"(0) : "memory");
           pair::fence_smem_async();
           __syncwarp();
-          if (rank == 1) {
-            if (lane == 0) pair::arrive_at(ready + 8 * pipe.s, 0);
-          } else {
-            ok = pair::wait_warp<0>(ready + 8 * pipe.s, (tph >> pipe.s) & 1u, abort, p.status);
-            if (!ok) break;
-          }
-          tph ^= 1u << pipe.s;
+          if (lane == 0) pair::arrive_at(full + 8 * pipe.s, 0);
         }
-        if (rank == 0) {
-          ptx::tc_fence_after();
-          if (lane == 0) {
-            for (int kk = 0; kk < steps; ++kk)
-              pair::mma(d, kAMn<MODE> ? pair::sdesc_mn_sw128(sa + kk * 2048) : ptx::sdesc_k_sw128(sa + kk * 32),
-                        b_mn(MODE) ? pair::sdesc_mn_sw128(sb + kk * 2048) : ptx::sdesc_k_sw128(sb + kk * 32), id,
-                        (k | kk) != 0 ? 1u : 0u);
-            pair::commit_both(empty + 8 * pipe.s);
-          }
-          __syncwarp();
-        }
-        pipe.next();
       }
-      if (rank == 0 && ok && lane == 0) pair::commit_both(accfull + 8 * acc);
-      acc ^= 1;
-      if (acc == 0) aph ^= 1u;
-    }
-    if (!ok && rank == 0 && lane == 0) {  // the MMAs that were issued
-      pair::commit_both(done);
-      pair::drain(done, 0);
     }
   } else {
     // -------------------------------------------------------------- results
     const int q = warp & 3, group = (warp - 2) >> 2;
+    float* buf = turn + (warp - 2) * kTurn;
+    // the warp with the other half of the gate and up features (q ^ 1)
+    const float* other = turn + ((group << 2) + ((q ^ 1) + 2) % 4) * kTurn;
+    const int tr = lane >> 2, tc = (lane & 3) * 8;  // row and first feature once turned
     int acc = 0;
-    uint32_t aph = 0, turn = 0;
-    for (int t = t0; t < sc.total; t += tstep) {
-      const Tile tl = sc.tile(t);
+    uint32_t aph = 0;
+    for (int t = t0, jt = 0; t < sc.total; t += tstep, ++jt) {
+      const Tile tl = sc.tile(t, jt);
       if (tl.k != 0) {
         if (!pair::wait_warp<32>(accfull + 8 * acc, aph, abort, p.status)) break;
         ptx::tc_fence_after();
       }
       const uint32_t d = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-      if (MODE == kGateUp) {
-        // Even warps hold 32 gate features, odd ones the same up features: of
-        // 16 rows each gives the other eight.
-        const int i = tl.m0 + static_cast<int>(rank) * 64 + (q >> 1) * 32 + lane;
-        float* mine = swap + ((group * 2 + (q >> 1)) * 2 * 2) * 256;
-        for (int c = group * 16; c < tl.N; c += 32) {
-          float v[16];
-          ptx::tmem_ld16(d + c, v);
-          float* out = mine + (turn * 2 + (q & 1)) * 256 + lane;
-          const float* in = mine + (turn * 2 + (1 - (q & 1))) * 256 + lane;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) out[j * 32] = (q & 1) ? v[j] : v[8 + j];
-          asm volatile("bar.sync %0, 64;" ::"r"(1 + group * 2 + (q >> 1)) : "memory");
-          float g[8], u[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float o = in[j * 32];
-            g[j] = (q & 1) ? o : v[j];
-            u[j] = (q & 1) ? v[8 + j] : o;
-          }
-          turn ^= 1u;
-          const int c8 = c + (q & 1) * 8;
-          gate_up(p, g, u, static_cast<int64_t>(tl.n0) + c8, tl.n - c8, i);
-        }
-      } else if (MODE == kDh) {
-        const int i = tl.m0 + static_cast<int>(rank) * 128 + q * 32 + lane;
-        for (int c = group * 16; c < tl.n; c += 32) {
-          float v[16];
-          ptx::tmem_ld16(d + c, v);
-          d_gate_up(p, v, static_cast<int64_t>(tl.n0) + c, tl.n - c, i);
-        }
-      } else if (MODE == kGrad) {
+      if (MODE == kGrad) {
         const int m = tl.m0 + static_cast<int>(rank) * 128 + q * 32 + lane;
         const int M = tl.down ? p.H : 2 * p.I, cols = tl.down ? p.I : p.H;
         if (tl.k != 0 || !p.accumulate) {
@@ -540,12 +643,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                          tl.n - c);
           }
         }
+      } else if (MODE == kGateUp) {
+        // Even warps hold 32 gate features, odd ones the same up features; of 16
+        // rows each pair of warps turns, either takes eight.
+        const int i = tl.m0 + static_cast<int>(rank) * 64 + (q >> 1) * 32 + tc;
+        for (int c = group * 16; c < tl.N; c += 32) {
+          float v[16];
+          ptx::tmem_ld16(d + c, v);
+          turn_in(buf, v);
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + group * 2 + (q >> 1)) : "memory");
+          const int row = (q & 1) * 8 + tr;
+          const V8 a = turn_out(buf, row), b = turn_out(other, row);
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + group * 2 + (q >> 1)) : "memory");
+          gate_up(p, (q & 1) ? b : a, (q & 1) ? a : b, static_cast<int64_t>(tl.n0) + c + row, i,
+                  c + row < tl.n && i < p.I);
+        }
       } else {
-        const int m = tl.m0 + static_cast<int>(rank) * 128 + q * 32 + lane;
-        for (int c = group * 32; c < tl.n; c += 64) {
-          float v[32];
-          pair::tmem_ld32(d + c, v);
-          store_rows(p.out, v, static_cast<int64_t>(tl.n0) + c, tl.n - c, m, p.H);
+        const int width = MODE == kDh ? p.I : p.H;
+        const int m = tl.m0 + static_cast<int>(rank) * 128 + q * 32 + tc;
+        for (int c = group * 16; c < tl.n; c += 32) {
+          const int64_t row = static_cast<int64_t>(tl.n0) + c + tr;
+          Kept k[2];
+          if (MODE == kDh) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (m < width && c + tr + h * 8 < tl.n) k[h].load(p, row + h * 8, m);
+          }
+          float v[16];
+          ptx::tmem_ld16(d + c, v);
+          turn_in(buf, v);
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const V8 x = turn_out(buf, tr + h * 8);
+            if (m < width && c + tr + h * 8 < tl.n) {
+              if (MODE == kDh)
+                d_gate_up(p, x, k[h], row + h * 8, m);
+              else
+                store_row(p.out, x, row + h * 8, m);
+            }
+          }
+          __syncwarp();
         }
       }
       if (tl.k != 0) {
