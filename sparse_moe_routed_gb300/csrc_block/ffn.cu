@@ -26,6 +26,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "launch.h"
@@ -45,7 +46,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kStages = 6;
 constexpr int kK = 64;  // contraction per stage: one 128-byte swizzled row
 constexpr int kABytes = 128 * kK * 2, kBBytes = 128 * kK * 2, kStageBytes = kABytes + kBBytes;
-constexpr int kRowBox = 32;              // rows of the second operand per copy
+constexpr int kRowBox = 128, kFewBox = 64;  // rows of the second operand per copy: tiles of more than 128 rows, others
 constexpr int kTurnRows = 16;            // rows that a warp turns at a time,
 constexpr int kTurnLd = 36;              // 32 features each: a row and 16 bytes, so that reads of 8 rows spread over the banks
 constexpr int kTurn = kTurnRows * kTurnLd;
@@ -69,6 +70,10 @@ struct P {
   uint16_t *da, *h;   // gate/up: h; dh: both
   void *dwgu, *dwd;   // weight gradients (either may be null)
   int dw_type, accumulate;
+  bool a_one, b_one, a2_one, b2_one;  // operands whose half of a stage is one copy
+  int mt;             // row launches: 256-feature tiles (gate/up: 128 gate and 128 up)
+  int tgu, tall;      // gradients: tiles of dW_gu per expert, of both;
+  int tc[2], nt[2];   // columns per tile and tiles along a row, of dW_gu and dW_d
   int32_t* status;
 };
 
@@ -97,75 +102,81 @@ template <int MODE>
 struct Sched {
   const int* first;  // tiles before each expert
   const int* off;
-  int mt;            // 256-feature tiles (gate/up: 128 gate and 128 up)
-  int tgu, tall;     // gradient: tiles of dW_gu per expert, of both
-  int total;
   const int4* list;  // the pair's first tiles: e, m0, n0, n
+  int total;
   const P& p;
 
-  __device__ __forceinline__ Sched(const P& p_, const int* first_, const int* off_, const int4* list_)
-      : first(first_), off(off_), list(list_), p(p_) {
-    const int H = p.H, I = p.I;
-    mt = MODE == kGateUp ? up(I, 128) : MODE == kDh ? up(I, 256) : up(H, 256);
-    tgu = MODE == kGrad && p.dwgu != nullptr ? up(2 * I, 256) * up(H, tile_cols(H)) : 0;
-    tall = tgu + (MODE == kGrad && p.dwd != nullptr ? up(H, 256) * up(I, tile_cols(I)) : 0);
-    total = 0;
-  }
+  __device__ __forceinline__ Sched(const P& p_, const int* first_, const int* off_, const int4* list_, int total_)
+      : first(first_), off(off_), list(list_), total(total_), p(p_) {}
 
-  // The pair's j-th tile, tile t of all.
-  __device__ __forceinline__ Tile tile(int t, int j) const {
-    if (MODE == kGrad || j >= kList) return find(t);
-    const int4 v = list[j];
+  __device__ __forceinline__ Tile rows_tile(int e, int m0, int n0, int n) const {
     Tile r;
-    r.e = v.x;
-    r.m0 = v.y;
-    r.n0 = v.z;
-    r.n = v.w;
+    r.e = e;
+    r.m0 = m0;
+    r.n0 = n0;
+    r.n = n;
+    r.N = up(n, 32) * 32;
     r.s0 = 0;
+    r.k = MODE == kGateUp || MODE == kDh ? p.H : MODE == kDown ? p.I : 2 * p.I;
     r.down = false;
-    r.k = length();
-    r.N = up(r.n, 32) * 32;
     return r;
   }
 
-  __device__ __forceinline__ int length() const {
-    return MODE == kGateUp || MODE == kDh ? p.H : MODE == kDown ? p.I : 2 * p.I;
-  }
-
   __device__ __forceinline__ Tile find(int t) const {
-    Tile r;
-    if (MODE == kGrad) {
-      r.e = t / tall;
-      int l = t - r.e * tall;
-      r.down = l >= tgu;
-      if (r.down) l -= tgu;
-      const int cols = r.down ? p.I : p.H, tc = tile_cols(cols), nt = up(cols, tc);
-      r.m0 = l / nt * 256;
-      r.n0 = l % nt * tc;
-      r.n = min(tc, cols - r.n0);
-      r.s0 = off[r.e];
-      r.k = max(off[r.e + 1] - r.s0, 0);
-    } else {
-      int lo = 0, hi = p.E;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first[mid] <= t) lo = mid; else hi = mid;
-      }
-      r.e = lo;
-      const int s0 = off[lo], len = off[lo + 1] - s0, chunks = up(len, 256);
-      const int each = up(up(len, chunks), 32) * 32;
-      int l = t - first[lo];
-      const int band = l / (kBand * mt), in_band = min(kBand, chunks - band * kBand);
-      l -= band * kBand * mt;
-      const int c = band * kBand + l % in_band;
-      r.m0 = l / in_band * (MODE == kGateUp ? 128 : 256);
-      r.n0 = s0 + c * each;
-      r.n = min(each, len - c * each);
-      r.s0 = 0;
-      r.down = false;
-      r.k = length();
+    int lo = 0, hi = p.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= t) lo = mid; else hi = mid;
     }
+    const int s0 = off[lo], len = off[lo + 1] - s0, chunks = up(len, 256);
+    const int each = up(up(len, chunks), 32) * 32;
+    int l = t - first[lo];
+    const int band = l / (kBand * p.mt), in_band = min(kBand, chunks - band * kBand);
+    l -= band * kBand * p.mt;
+    const int c = band * kBand + l % in_band;
+    return rows_tile(lo, l / in_band * (MODE == kGateUp ? 128 : 256), s0 + c * each, min(each, len - c * each));
+  }
+};
+
+// A role's way through the pair's tiles.
+template <int MODE>
+struct Walk {
+  const Sched<MODE>& sc;
+  int t, j = 0, e, l;  // tile, which of the pair's; gradient: expert, tile in it
+  const int step, de, dl;
+
+  __device__ __forceinline__ Walk(const Sched<MODE>& s)
+      : sc(s), t(blockIdx.x >> 1), step(gridDim.x >> 1), de(MODE == kGrad ? step / s.p.tall : 0),
+        dl(MODE == kGrad ? step % s.p.tall : 0) {
+    e = MODE == kGrad ? t / s.p.tall : 0;
+    l = MODE == kGrad ? t % s.p.tall : 0;
+  }
+  __device__ __forceinline__ bool more() const { return t < sc.total; }
+  __device__ __forceinline__ void next() {
+    t += step;
+    ++j;
+    if (MODE == kGrad) {
+      e += de;
+      l += dl;
+      if (l >= sc.p.tall) l -= sc.p.tall, ++e;
+    }
+  }
+  __device__ __forceinline__ Tile tile() const {
+    if (MODE != kGrad) {
+      if (j >= kList) return sc.find(t);
+      const int4 v = sc.list[j];
+      return sc.rows_tile(v.x, v.y, v.z, v.w);
+    }
+    Tile r;
+    r.e = e;
+    r.down = l >= sc.p.tgu;
+    const int i = r.down, at = r.down ? l - sc.p.tgu : l, m = at / sc.p.nt[i];
+    r.m0 = m * 256;
+    r.n0 = (at - m * sc.p.nt[i]) * sc.p.tc[i];
+    r.n = min(sc.p.tc[i], (r.down ? sc.p.I : sc.p.H) - r.n0);
     r.N = up(r.n, 32) * 32;
+    r.s0 = sc.off[e];
+    r.k = max(sc.off[e + 1] - r.s0, 0);
     return r;
   }
 };
@@ -446,16 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Offsets, kept inside the buffers and rising, whatever they hold.
   for (int i = threadIdx.x; i <= p.E; i += kThreads) soff[i] = min(max(__ldcg(p.offsets + i), 0), p.R);
   __syncthreads();
-  Sched<MODE> sc(p, first, soff, list);
-  const int t0 = blockIdx.x >> 1, tstep = gridDim.x >> 1;
-  if (MODE == kGrad) {
-    sc.total = sc.tall * p.E;
-  } else {
+  if (MODE != kGrad) {
     if (warp == 0) {
       int running = 0;
       for (int e0 = 0; e0 < p.E; e0 += 32) {
         const int e = e0 + lane;
-        const int n = e < p.E ? up(max(soff[e + 1] - soff[e], 0), 256) * sc.mt : 0;
+        const int n = e < p.E ? up(max(soff[e + 1] - soff[e], 0), 256) * p.mt : 0;
         int incl = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -468,7 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) misc[2] = running;
     }
     __syncthreads();
-    sc.total = misc[2];
+  }
+  const Sched<MODE> sc(p, first, soff, list, MODE == kGrad ? p.tall * p.E : static_cast<int>(misc[2]));
+  if (MODE != kGrad) {
+    const int t0 = blockIdx.x >> 1, tstep = gridDim.x >> 1;
     for (int j = threadIdx.x; j < kList && t0 + j * tstep < sc.total; j += kThreads) {
       const Tile tl = sc.find(t0 + j * tstep);
       list[j] = make_int4(tl.e, tl.m0, tl.n0, tl.n);
@@ -479,18 +489,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 || warp == 10) {
     // ------------------------------------------------------------- operands
     if (lane == 0) {
-      const uint64_t pol = ptx::policy_evict_normal();
+      // Operands are read again by the tiles beside; results are not (weights and
+      // rows alike: 1 to 3 % over normal, at 4,096 and 16,384 tokens and dense).
+      const uint64_t pol = ptx::policy_evict_last();
       const int r = static_cast<int>(rank);
       Pipe pipe;
       uint32_t used = 0;
       bool ok = true;
-      for (int t = t0, j = 0; t < sc.total && ok; t += tstep, ++j) {
-        const Tile tl = sc.tile(t, j);
+      for (Walk<MODE> w(sc); w.more() && ok; w.next()) {
+        const Tile tl = w.tile();
         const int half = tl.N / 2;
         const CUtensorMap* a = MODE == kGrad && tl.down ? &ma2 : &ma;
-        const CUtensorMap* b = MODE == kGrad && tl.down ? &mb2 : &mb;
-        const int boxes = MODE == kGrad ? up(half, 64) : up(half, kRowBox);
-        const uint32_t bytes = kABytes + boxes * (MODE == kGrad ? 8192 : kRowBox * 128);
+        const CUtensorMap* b = MODE == kGrad ? (tl.down ? &mb2 : &mb) : half > kFewBox ? &mb : &mb2;
+        const bool a_one = MODE == kGrad && tl.down ? p.a2_one : p.a_one, b_one = tl.down ? p.b2_one : p.b_one;
+        const int boxes = MODE != kGrad || b_one ? 1 : up(half, 64);
+        const uint32_t bytes = kABytes + (MODE == kGrad ? (b_one ? kBBytes : boxes * 8192)
+                                                        : (half > kFewBox ? kRowBox : kFewBox) * 128);
         for (int k = 0; k < tl.k; k += kK) {
           ok = pair::wait<0>(empty + 8 * pipe.s, pipe.ph ^ 1u, abort, p.status);
           if (!ok) break;
@@ -505,29 +519,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           bar = pair::at_rank(bar, alone ? rank : 0);
           if (warp == 0) {
-            if (MODE == kGateUp) {
+            const int c = tl.m0 + r * (MODE == kGateUp ? 64 : 128);
+            if (MODE == kDown) {
+              pair::tma_3d(sa, a, bar, k, c, tl.e, pol);
+            } else if (a_one) {
+              if (MODE == kGateUp)
+                pair::tma_5d(sa, a, bar, k, 0, 0, c / 32, tl.e, pol);
+              else if (MODE == kGrad)
+                pair::tma_3d(sa, a, bar, 0, tl.s0 + k, c / 64, pol);
+              else
+                pair::tma_4d(sa, a, bar, 0, k, c / 64, tl.e, pol);
+            } else if (MODE == kGateUp) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)  // 32 gate rows, their 32 up rows, and again
-                pair::tma_4d(sa + i * 4096, a, bar, k, tl.m0 + r * 64 + (i >> 1) * 32, i & 1, tl.e, pol);
-            } else if (MODE == kDown) {
-              pair::tma_3d(sa, a, bar, k, tl.m0 + r * 128, tl.e, pol);
+                pair::tma_4d(sa + i * 4096, a, bar, k, c + (i >> 1) * 32, i & 1, tl.e, pol);
             } else {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const int c = tl.m0 + r * 128 + i * 64;
                 if (MODE == kGrad)
-                  pair::tma_2d(sa + i * 8192, a, bar, c, tl.s0 + k, pol);
+                  pair::tma_2d(sa + i * 8192, a, bar, c + i * 64, tl.s0 + k, pol);
                 else
-                  pair::tma_3d(sa + i * 8192, a, bar, c, k, tl.e, pol);
+                  pair::tma_3d(sa + i * 8192, a, bar, c + i * 64, k, tl.e, pol);
               }
             }
+          } else if (MODE != kGrad) {
+            pair::tma_2d(sb, b, bar, k, tl.n0 + r * half, pol);
+          } else if (b_one) {
+            pair::tma_3d(sb, b, bar, 0, tl.s0 + k, (tl.n0 + r * half) / 64, pol);
           } else {
-            for (int i = 0; i < boxes; ++i) {
-              if (MODE == kGrad)
-                pair::tma_2d(sb + i * 8192, b, bar, tl.n0 + r * half + i * 64, tl.s0 + k, pol);
-              else
-                pair::tma_2d(sb + i * kRowBox * 128, b, bar, k, tl.n0 + r * half + i * kRowBox, pol);
-            }
+            for (int i = 0; i < boxes; ++i)
+              pair::tma_2d(sb + i * 8192, b, bar, tl.n0 + r * half + i * 64, tl.s0 + k, pol);
           }
           pipe.next();
           ++used;
@@ -553,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t da0 = kAMn<MODE> ? pair::sdesc_mn_sw128(base) : ptx::sdesc_k_sw128(base);
       const uint64_t db0 = b_mn(MODE) ? pair::sdesc_mn_sw128(base + kABytes) : ptx::sdesc_k_sw128(base + kABytes);
       constexpr uint32_t kStepA = (kAMn<MODE> ? 2048 : 32) >> 4, kStepB = (b_mn(MODE) ? 2048 : 32) >> 4;
-      for (int t = t0, j = 0; t < sc.total && ok; t += tstep, ++j) {
-        const Tile tl = sc.tile(t, j);
+      for (Walk<MODE> w(sc); w.more() && ok; w.next()) {
+        const Tile tl = w.tile();
         if (tl.k == 0) continue;
         const uint32_t id = pair::idesc(tl.N, kAMn<MODE>, b_mn(MODE));
         const uint32_t d = tmem + acc * 256;
@@ -592,8 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       Pipe pipe;
       uint32_t tph = 0;  // a bit per stage: the phase of its tfull
       bool ok = true;
-      for (int t = t0, j = 0; t < sc.total && ok; t += tstep, ++j) {
-        const Tile tl = sc.tile(t, j);
+      for (Walk<MODE> w(sc); w.more() && ok; w.next()) {
+        const Tile tl = w.tile();
         for (int left = tl.k; left > 0; left -= kK, pipe.next()) {
           if (!ends_inside(left)) continue;
           ok = pair::wait_warp<0>(tfull + 8 * pipe.s, (tph >> pipe.s) & 1u, abort, p.status);
@@ -619,8 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tr = lane >> 2, tc = (lane & 3) * 8;  // row and first feature once turned
     int acc = 0;
     uint32_t aph = 0;
-    for (int t = t0, jt = 0; t < sc.total; t += tstep, ++jt) {
-      const Tile tl = sc.tile(t, jt);
+    for (Walk<MODE> w(sc); w.more(); w.next()) {
+      const Tile tl = w.tile();
       if (tl.k != 0) {
         if (!pair::wait_warp<32>(accfull + 8 * acc, aph, abort, p.status)) break;
         ptx::tc_fence_after();
@@ -718,42 +739,90 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// bf16 tensor, innermost dimension first (its elements adjacent), boxes of 64
-// elements x box1 x ...; reads outside give zeros.
-bool make_map(CUtensorMap* m, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* stride_elems,
-              cuuint32_t box1) {
+// bf16 tensor, innermost dimension first (its elements adjacent); reads outside
+// give zeros.
+bool make_map(CUtensorMap* m, const void* p, int rank, const cuuint64_t* dims, const int64_t* stride_elems,
+              const cuuint32_t* box) {
   const auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t strides[3];
-  for (int i = 0; i + 1 < rank; ++i) strides[i] = stride_elems[i] * 2;
-  const cuuint32_t box[4] = {kK, box1, 1, 1}, ones[4] = {1, 1, 1, 1};
+  cuuint64_t strides[4];
+  for (int i = 0; i + 1 < rank; ++i) strides[i] = static_cast<cuuint64_t>(stride_elems[i]) * 2;
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(p), dims, strides, box, ones,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+inline cuuint64_t u64(int v) { return static_cast<cuuint64_t>(v); }
 
+// Rows [R][width], ld apart: boxes of 64 columns x box_rows.
 bool map_rows(CUtensorMap* m, const void* p, int64_t ld, int R, int width, int box_rows) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(R)};
-  const cuuint64_t str[1] = {static_cast<cuuint64_t>(R > 1 ? ld : up(width, 8) * 8)};
-  return make_map(m, p, 2, dims, str, box_rows);
+  const cuuint64_t dims[2] = {u64(width), u64(R)};
+  const int64_t str[1] = {R > 1 ? ld : width};
+  const cuuint32_t box[2] = {kK, static_cast<cuuint32_t>(box_rows)};
+  return make_map(m, p, 2, dims, str, box);
 }
 
-// [E][rows][width], contiguous
-bool map_weights(CUtensorMap* m, const void* p, int E, int rows, int width, int box_rows) {
-  const cuuint64_t w = width, r = rows;
-  const cuuint64_t dims[3] = {w, r, static_cast<cuuint64_t>(E)};
-  const cuuint64_t str[2] = {w, w * r};
-  return make_map(m, p, 3, dims, str, box_rows);
+// The same as an operand whose columns are its features: 64 rows and two blocks
+// of 64 columns in one copy where the columns are whole blocks (a block may not
+// reach past a row's end), else block by block.
+bool map_sum_rows(CUtensorMap* m, bool* one, const void* p, int64_t ld, int R, int width, bool want_one) {
+  *one = want_one && width % 64 == 0;
+  if (!*one) return map_rows(m, p, ld, R, width, 64);
+  const cuuint64_t dims[3] = {64, u64(R), u64(width / 64)};
+  const int64_t str[2] = {R > 1 ? ld : width, 64};
+  const cuuint32_t box[3] = {64, 64, 2};
+  return make_map(m, p, 3, dims, str, box);
+}
+
+// Whether the halves of all tiles along a row begin on blocks of 64 columns.
+inline bool whole_halves(int width) { return width % 128 == 0 && tile_cols(width) % 128 == 0; }
+
+// Weights [E][rows][width] with the sum over the rows: as map_sum_rows.
+bool map_sum_weights(CUtensorMap* m, bool* one, const void* p, int E, int rows, int width) {
+  const int64_t w = width;
+  *one = width % 64 == 0;
+  if (*one) {
+    const cuuint64_t dims[4] = {64, u64(rows), u64(width / 64), u64(E)};
+    const int64_t str[3] = {w, 64, w * rows};
+    const cuuint32_t box[4] = {64, 64, 2, 1};
+    return make_map(m, p, 4, dims, str, box);
+  }
+  const cuuint64_t dims[3] = {u64(width), u64(rows), u64(E)};
+  const int64_t str[2] = {w, w * rows};
+  const cuuint32_t box[3] = {64, 64, 1};
+  return make_map(m, p, 3, dims, str, box);
+}
+
+// W_d [E][H][I], 128 rows.
+bool map_down(CUtensorMap* m, const void* p, int E, int H, int I) {
+  const cuuint64_t dims[3] = {u64(I), u64(H), u64(E)};
+  const int64_t str[2] = {I, static_cast<int64_t>(I) * H};
+  const cuuint32_t box[3] = {kK, 128, 1};
+  return make_map(m, p, 3, dims, str, box);
+}
+
+// W_gu [E][2][I][H]: 32 gate rows, their 32 up rows and the next 32 of each in
+// one copy where I is whole groups of 32, else 32 rows of one kind.
+bool map_gate_up(CUtensorMap* m, bool* one, const void* p, int E, int H, int I) {
+  const int64_t h = H, i = I;
+  *one = I % 32 == 0;
+  if (*one) {
+    const cuuint64_t dims[5] = {u64(H), 32, 2, u64(I / 32), u64(E)};
+    const int64_t str[4] = {h, h * i, 32 * h, 2 * h * i};
+    const cuuint32_t box[5] = {kK, 32, 2, 2, 1};
+    return make_map(m, p, 5, dims, str, box);
+  }
+  const cuuint64_t dims[4] = {u64(H), u64(I), 2, u64(E)};
+  const int64_t str[3] = {h, h * i, 2 * h * i};
+  const cuuint32_t box[4] = {kK, 32, 1, 1};
+  return make_map(m, p, 4, dims, str, box);
 }
 
 template <int MODE>
 cudaError_t go(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2, const CUtensorMap& b2, const P& p,
                int64_t tiles, cudaStream_t st) {
   auto kern = ffn_kernel<MODE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
@@ -764,12 +833,24 @@ cudaError_t go(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int pairs = 0;
-  e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+  // Pairs that run at a time on this device, 0 until the first launch there.
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  int pairs = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (pairs == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(2);
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    pairs = std::max(pairs, 1);
+    if (dev < 64) known[dev].store(pairs, std::memory_order_relaxed);
+  }
   cfg.numAttrs = 2;
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(std::max(pairs, 1), tiles)));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(pairs, tiles)));
   return cudaLaunchKernelEx(&cfg, kern, a, b, a2, b2, p);
 }
 
@@ -793,17 +874,19 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st) {
   p.act = a.act;
   p.h = a.h;
   p.status = a.status;
-  CUtensorMap ma, mb;
-  const cuuint64_t H = a.H, I = a.I;
-  const cuuint64_t dims[4] = {H, I, 2, static_cast<cuuint64_t>(a.E)}, str[3] = {H, H * I, 2 * H * I};
-  FFN_MAP(make_map(&ma, a.w_gateup, 4, dims, str, 32));
+  p.mt = up(a.I, 128);
+  CUtensorMap ma, mb, mb2;
+  FFN_MAP(map_gate_up(&ma, &p.a_one, a.w_gateup, a.E, a.H, a.I));
   FFN_MAP(map_rows(&mb, a.x.p, a.x.ld, a.R, a.H, kRowBox));
-  FFN_TRY(go<kGateUp>(ma, mb, ma, mb, p, row_tiles(a.R, a.E, up(a.I, 128)), st));
+  FFN_MAP(map_rows(&mb2, a.x.p, a.x.ld, a.R, a.H, kFewBox));
+  FFN_TRY(go<kGateUp>(ma, mb, ma, mb2, p, row_tiles(a.R, a.E, p.mt), st));
   if (a.y.p == nullptr) return cudaSuccess;
   p.out = Out{a.y.p, a.y.ld, a.y.type};
-  FFN_MAP(map_weights(&ma, a.w_down, a.E, a.H, a.I, 128));
+  p.mt = up(a.H, 256);
+  FFN_MAP(map_down(&ma, a.w_down, a.E, a.H, a.I));
   FFN_MAP(map_rows(&mb, a.h, a.I, a.R, a.I, kRowBox));
-  return go<kDown>(ma, mb, ma, mb, p, row_tiles(a.R, a.E, up(a.H, 256)), st);
+  FFN_MAP(map_rows(&mb2, a.h, a.I, a.R, a.I, kFewBox));
+  return go<kDown>(ma, mb, ma, mb2, p, row_tiles(a.R, a.E, p.mt), st);
 }
 
 cudaError_t launch_ffn_grad(const FfnGradArgs& a, cudaStream_t st) {
@@ -821,31 +904,37 @@ cudaError_t launch_ffn_grad(const FfnGradArgs& a, cudaStream_t st) {
   p.h = a.h;
   p.status = a.status;
   CUtensorMap ma, mb, ma2, mb2;
-  FFN_MAP(map_weights(&ma, a.w_down, a.E, a.H, a.I, 64));
+  p.mt = up(a.I, 256);
+  FFN_MAP(map_sum_weights(&ma, &p.a_one, a.w_down, a.E, a.H, a.I));
   FFN_MAP(map_rows(&mb, a.dy.p, a.dy.ld, a.R, a.H, kRowBox));
-  FFN_TRY(go<kDh>(ma, mb, ma, mb, p, row_tiles(a.R, a.E, up(a.I, 256)), st));
+  FFN_MAP(map_rows(&mb2, a.dy.p, a.dy.ld, a.R, a.H, kFewBox));
+  FFN_TRY(go<kDh>(ma, mb, ma, mb2, p, row_tiles(a.R, a.E, p.mt), st));
   if (a.dx.p != nullptr) {
     p.out = Out{a.dx.p, a.dx.ld, a.dx.type};
-    FFN_MAP(map_weights(&ma, a.w_gateup, a.E, 2 * a.I, a.H, 64));
+    p.mt = up(a.H, 256);
+    FFN_MAP(map_sum_weights(&ma, &p.a_one, a.w_gateup, a.E, 2 * a.I, a.H));
     FFN_MAP(map_rows(&mb, a.da, 2 * a.I, a.R, 2 * a.I, kRowBox));
-    FFN_TRY(go<kDx>(ma, mb, ma, mb, p, row_tiles(a.R, a.E, up(a.H, 256)), st));
+    FFN_MAP(map_rows(&mb2, a.da, 2 * a.I, a.R, 2 * a.I, kFewBox));
+    FFN_TRY(go<kDx>(ma, mb, ma, mb2, p, row_tiles(a.R, a.E, p.mt), st));
   }
   if (a.dw_gateup == nullptr && a.dw_down == nullptr) return cudaSuccess;
   p.dwgu = a.dw_gateup;
   p.dwd = a.dw_down;
   p.dw_type = a.dw_type;
   p.accumulate = a.accumulate;
-  int64_t tiles = 0;
+  p.tc[0] = tile_cols(a.H), p.tc[1] = tile_cols(a.I);
+  p.nt[0] = up(a.H, p.tc[0]), p.nt[1] = up(a.I, p.tc[1]);
+  p.tgu = a.dw_gateup != nullptr ? up(2 * a.I, 256) * p.nt[0] : 0;
+  p.tall = p.tgu + (a.dw_down != nullptr ? up(a.H, 256) * p.nt[1] : 0);
+  FFN_MAP(map_sum_rows(&ma2, &p.a2_one, a.dy.p, a.dy.ld, a.R, a.H, true));
+  FFN_MAP(map_sum_rows(&mb2, &p.b2_one, a.h, a.I, a.R, a.I, whole_halves(a.I)));
   if (a.dw_gateup != nullptr) {
-    FFN_MAP(map_rows(&ma, a.da, 2 * a.I, a.R, 2 * a.I, 64));
-    FFN_MAP(map_rows(&mb, a.x.p, a.x.ld, a.R, a.H, 64));
-    tiles += static_cast<int64_t>(up(2 * a.I, 256)) * up(a.H, tile_cols(a.H));
+    FFN_MAP(map_sum_rows(&ma, &p.a_one, a.da, 2 * a.I, a.R, 2 * a.I, true));
+    FFN_MAP(map_sum_rows(&mb, &p.b_one, a.x.p, a.x.ld, a.R, a.H, whole_halves(a.H)));
+  } else {
+    ma = ma2, mb = mb2;
   }
-  FFN_MAP(map_rows(&ma2, a.dy.p, a.dy.ld, a.R, a.H, 64));
-  FFN_MAP(map_rows(&mb2, a.h, a.I, a.R, a.I, 64));
-  if (a.dw_down != nullptr) tiles += static_cast<int64_t>(up(a.H, 256)) * up(a.I, tile_cols(a.I));
-  if (a.dw_gateup == nullptr) ma = ma2, mb = mb2;
-  return go<kGrad>(ma, mb, ma2, mb2, p, tiles * a.E, st);
+  return go<kGrad>(ma, mb, ma2, mb2, p, static_cast<int64_t>(p.tall) * a.E, st);
 }
 
 }  // namespace blk
