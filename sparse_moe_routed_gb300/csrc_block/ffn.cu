@@ -43,18 +43,23 @@ enum Mode { kGateUp, kDown, kDh, kDx, kGrad };
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
-constexpr int kStages = 6;
 constexpr int kK = 64;  // contraction per stage: one 128-byte swizzled row
 constexpr int kABytes = 128 * kK * 2, kBBytes = 128 * kK * 2, kStageBytes = kABytes + kBBytes;
-constexpr int kRowBox = 128, kFewBox = 64;  // rows of the second operand per copy: tiles of more than 128 rows, others
 constexpr int kTurnRows = 16;            // rows that a warp turns at a time,
 constexpr int kTurnLd = 36;              // 32 features each: a row and 16 bytes, so that reads of 8 rows spread over the banks
 constexpr int kTurn = kTurnRows * kTurnLd;
+constexpr int kOut = 32 * 128;           // bytes of a gradient that a warp hands to a copy: 32 rows of 128 bytes
 constexpr int kList = 128;               // tiles of a pair that are looked up ahead
-constexpr int kBars = 3 * kStages + 4 + 1;
-constexpr int kTail = kEpiWarps * kTurn * 4;
-constexpr int kSmem = 1024 + kStages * kStageBytes + kTail + kList * 16 + 16 + kBars * 8 + 8 + 2 * (kMaxE + 1) * 4;
-static_assert(kSmem <= 227 * 1024, "shared memory");
+
+template <int MODE>
+struct Smem {
+  static constexpr int kStages = MODE == kGrad ? 5 : 6;
+  static constexpr int kTail = kEpiWarps * (MODE == kGrad ? kOut : kTurn * 4);
+  static constexpr int kBars = 3 * kStages + 4 + 1;
+  static constexpr int kBytes =
+      1024 + kStages * kStageBytes + kTail + kList * 16 + 16 + kBars * 8 + 8 + 2 * (kMaxE + 1) * 4;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
 
 struct Out {
   void* p;
@@ -73,14 +78,11 @@ struct P {
   bool a_one, b_one, a2_one, b2_one;  // operands whose half of a stage is one copy
   int mt;             // row launches: 256-feature tiles (gate/up: 128 gate and 128 up)
   int tgu, tall;      // gradients: tiles of dW_gu per expert, of both;
-  int tc[2], nt[2];   // columns per tile and tiles along a row, of dW_gu and dW_d
+  int nt[2];          // tiles of 256 columns along a row, of dW_gu and dW_d
   int32_t* status;
 };
 
 inline __host__ __device__ int up(int a, int b) { return (a + b - 1) / b; }
-
-// Columns of a gradient tile: as even as multiples of 32 allow.
-inline __host__ __device__ int tile_cols(int n) { return up(up(n, up(n, 256)), 32) * 32; }
 
 struct Tile {
   int e;
@@ -172,8 +174,8 @@ struct Walk {
     r.down = l >= sc.p.tgu;
     const int i = r.down, at = r.down ? l - sc.p.tgu : l, m = at / sc.p.nt[i];
     r.m0 = m * 256;
-    r.n0 = (at - m * sc.p.nt[i]) * sc.p.tc[i];
-    r.n = min(sc.p.tc[i], (r.down ? sc.p.I : sc.p.H) - r.n0);
+    r.n0 = (at - m * sc.p.nt[i]) * 256;
+    r.n = min(256, (r.down ? sc.p.I : sc.p.H) - r.n0);
     r.N = up(r.n, 32) * 32;
     r.s0 = sc.off[e];
     r.k = max(sc.off[e + 1] - r.s0, 0);
@@ -188,6 +190,7 @@ constexpr bool b_mn(int mode) { return mode == kGrad; }
 // Whether a sum over rows, `left` of them in this stage, ends inside a step of 16.
 __device__ __forceinline__ bool ends_inside(int left) { return left < kK && (left & 15) != 0; }
 
+template <int kStages>
 struct Pipe {
   uint32_t s = 0, ph = 0;
   __device__ __forceinline__ void next() {
@@ -236,51 +239,24 @@ __device__ __forceinline__ void store_row(const Out& o, const V8& v, int64_t row
 }
 
 // 32 adjacent columns of a row of a weight gradient, n of them (a multiple of 8)
-// inside.
-__device__ __forceinline__ void store_grad(const P& p, void* base, float (&v)[32], int64_t at, int n) {
-  if (p.dw_type == MOE_ROW_F32) {
-    float* q = static_cast<float*>(base) + at;
+// inside, added to what is there.
+__device__ __forceinline__ void add_grad(const P& p, void* base, const float (&v)[32], int64_t at, int n) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      if (j >= n) break;
+  for (int j = 0; j < 32; j += 8) {
+    if (j >= n) break;
+    V8 s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.v[i] = make_float2(v[j + 2 * i], v[j + 2 * i + 1]);
+    if (p.dw_type == MOE_ROW_F32) {
       Raw8<float> r;
-      if (p.accumulate) {
-        load_vec(q + j, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j + i] += r.v[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r.v[i] = v[j + i];
-      store_vec(q + j, r);
-    }
-  } else {
-    bf16_t* q = static_cast<bf16_t*>(base) + at;
-    if (!p.accumulate && n >= 32 && (reinterpret_cast<uintptr_t>(q) & 31) == 0) {
-      // whole 32-byte sectors
-#pragma unroll
-      for (int j = 0; j < 32; j += 16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack2(v[j + 2 * i], v[j + 2 * i + 1]);
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(q + j), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-      }
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      if (j >= n) break;
+      load_vec(static_cast<float*>(base) + at + j, r);
+      pack(unpack(r) + s, r);
+      store_vec(static_cast<float*>(base) + at + j, r);
+    } else {
       Raw8<bf16_t> r;
-      if (p.accumulate) {
-        load_vec(q + j, r);
-        const V8 old = unpack(r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j + i] += el(old, i);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r.v[i] = pack2(v[j + 2 * i], v[j + 2 * i + 1]);
-      store_vec(q + j, r);
+      load_vec(static_cast<bf16_t*>(base) + at + j, r);
+      pack(unpack(r) + s, r);
+      store_vec(static_cast<bf16_t*>(base) + at + j, r);
     }
   }
 }
@@ -414,7 +390,9 @@ template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                const __grid_constant__ CUtensorMap ma2, const __grid_constant__ CUtensorMap mb2,
+               const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mo2,
                const __grid_constant__ P p) {
+  constexpr int kStages = Smem<MODE>::kStages, kTail = Smem<MODE>::kTail, kBars = Smem<MODE>::kBars;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - ptx::smem_u32(smem_raw));
@@ -493,18 +471,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows alike: 1 to 3 % over normal, at 4,096 and 16,384 tokens and dense).
       const uint64_t pol = ptx::policy_evict_last();
       const int r = static_cast<int>(rank);
-      Pipe pipe;
+      Pipe<kStages> pipe;
       uint32_t used = 0;
       bool ok = true;
       for (Walk<MODE> w(sc); w.more() && ok; w.next()) {
         const Tile tl = w.tile();
         const int half = tl.N / 2;
         const CUtensorMap* a = MODE == kGrad && tl.down ? &ma2 : &ma;
-        const CUtensorMap* b = MODE == kGrad ? (tl.down ? &mb2 : &mb) : half > kFewBox ? &mb : &mb2;
+        const int box = half <= 64 ? 64 : half <= 96 ? 96 : 128;
+        const CUtensorMap* b = MODE == kGrad ? (tl.down ? &mb2 : &mb) : box == 64 ? &mb2 : box == 96 ? &ma2 : &mb;
         const bool a_one = MODE == kGrad && tl.down ? p.a2_one : p.a_one, b_one = tl.down ? p.b2_one : p.b_one;
         const int boxes = MODE != kGrad || b_one ? 1 : up(half, 64);
-        const uint32_t bytes = kABytes + (MODE == kGrad ? (b_one ? kBBytes : boxes * 8192)
-                                                        : (half > kFewBox ? kRowBox : kFewBox) * 128);
+        const uint32_t bytes = kABytes + (MODE == kGrad ? (b_one ? kBBytes : boxes * 8192) : box * 128);
         for (int k = 0; k < tl.k; k += kK) {
           ok = pair::wait<0>(empty + 8 * pipe.s, pipe.ph ^ 1u, abort, p.status);
           if (!ok) break;
@@ -567,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMAs
     if (rank == 0 && lane == 0) {
-      Pipe pipe;
+      Pipe<kStages> pipe;
       int acc = 0;
       uint32_t aph = 0;
       bool ok = true;
@@ -610,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 11) {
     // ------------------------------------------------ rows behind a sum's last
     if (MODE == kGrad) {
-      Pipe pipe;
+      Pipe<kStages> pipe;
       uint32_t tph = 0;  // a bit per stage: the phase of its tfull
       bool ok = true;
       for (Walk<MODE> w(sc); w.more() && ok; w.next()) {
@@ -650,17 +628,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (MODE == kGrad) {
         const int m = tl.m0 + static_cast<int>(rank) * 128 + q * 32 + lane;
         const int M = tl.down ? p.H : 2 * p.I, cols = tl.down ? p.I : p.H;
-        if (tl.k != 0 || !p.accumulate) {
+        if (!p.accumulate) {
+          // 32 rows of 128 bytes at a time through shared memory, as a copy that
+          // writes whole lines: a lane's own row would go out as 32 pieces of 32
+          // bytes per store, one line each.
+          const uint32_t mine = base + kStages * kStageBytes + (warp - 2) * kOut + lane * 128;
+          const int mw = tl.m0 + static_cast<int>(rank) * 128 + q * 32;
+          const int wide = p.dw_type == MOE_ROW_F32 ? 32 : 64;  // columns of 128 bytes
+          for (int c = group * wide; c < tl.n && mw < M; c += 2 * wide) {
+            uint32_t o[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h == 1 && wide == 32) break;
+              float v[32];
+              if (tl.k != 0 && c + h * 32 < tl.N) {
+                pair::tmem_ld32(d + c + h * 32, v);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.f;
+              }
+              if (wide == 32) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(v[j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[h * 16 + j] = pack2(v[2 * j], v[2 * j + 1]);
+              }
+            }
+            if (lane == 0) pair::tma_store_read();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((j ^ (lane & 7)) << 4)), "r"(o[4 * j]),
+                           "r"(o[4 * j + 1]), "r"(o[4 * j + 2]), "r"(o[4 * j + 3])
+                           : "memory");
+            pair::fence_smem_async();
+            __syncwarp();
+            if (lane == 0)
+              pair::tma_store_3d(tl.down ? &mo2 : &mo, base + kStages * kStageBytes + (warp - 2) * kOut, tl.n0 + c, mw, tl.e);
+          }
+        } else if (tl.k != 0) {
           for (int c = group * 32; c < tl.n; c += 64) {
             float v[32];
-            if (tl.k != 0) {
-              pair::tmem_ld32(d + c, v);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 0.f;
-            }
+            pair::tmem_ld32(d + c, v);
             if (m < M)
-              store_grad(p, tl.down ? p.dwd : p.dwgu, v, (static_cast<int64_t>(tl.e) * M + m) * cols + tl.n0 + c,
+              add_grad(p, tl.down ? p.dwd : p.dwgu, v, (static_cast<int64_t>(tl.e) * M + m) * cols + tl.n0 + c,
                          tl.n - c);
           }
         }
@@ -715,6 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (acc == 0) aph ^= 1u;
       }
     }
+    if (MODE == kGrad && lane == 0) pair::tma_store_done();
   }
 
   __syncwarp();
@@ -739,16 +752,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// bf16 tensor, innermost dimension first (its elements adjacent); reads outside
-// give zeros.
+// Tensor, innermost dimension first (its elements adjacent); reads outside give
+// zeros.
 bool make_map(CUtensorMap* m, const void* p, int rank, const cuuint64_t* dims, const int64_t* stride_elems,
-              const cuuint32_t* box) {
+              const cuuint32_t* box, int type = MOE_ROW_BF16) {
   const auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t strides[4];
-  for (int i = 0; i + 1 < rank; ++i) strides[i] = static_cast<cuuint64_t>(stride_elems[i]) * 2;
+  for (int i = 0; i + 1 < rank; ++i) strides[i] = static_cast<cuuint64_t>(stride_elems[i]) * (type == MOE_ROW_F32 ? 4 : 2);
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(p), dims, strides, box, ones,
+  return fn(m, type == MOE_ROW_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(p), dims, strides, box, ones,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -764,7 +777,8 @@ bool map_rows(CUtensorMap* m, const void* p, int64_t ld, int R, int width, int b
 
 // The same as an operand whose columns are its features: 64 rows and two blocks
 // of 64 columns in one copy where the columns are whole blocks (a block may not
-// reach past a row's end), else block by block.
+// reach past a row's end), else block by block.  The second operand is read by
+// halves of a tile: `want_one` where the last tile's begin on whole blocks too.
 bool map_sum_rows(CUtensorMap* m, bool* one, const void* p, int64_t ld, int R, int width, bool want_one) {
   *one = want_one && width % 64 == 0;
   if (!*one) return map_rows(m, p, ld, R, width, 64);
@@ -774,8 +788,22 @@ bool map_sum_rows(CUtensorMap* m, bool* one, const void* p, int64_t ld, int R, i
   return make_map(m, p, 3, dims, str, box);
 }
 
-// Whether the halves of all tiles along a row begin on blocks of 64 columns.
-inline bool whole_halves(int width) { return width % 128 == 0 && tile_cols(width) % 128 == 0; }
+// A weight gradient [E][rows][width]: 32 rows of 128 bytes.
+bool map_grad(CUtensorMap* m, const void* p, int type, int E, int rows, int width) {
+  const cuuint64_t dims[3] = {u64(width), u64(rows), u64(E)};
+  const int64_t str[2] = {width, static_cast<int64_t>(width) * rows};
+  const cuuint32_t box[3] = {type == MOE_ROW_F32 ? 32u : 64u, 32, 1};
+  return make_map(m, p, 3, dims, str, box, type);
+}
+
+// The second operand of a row launch: boxes of 128, 96 and 64 rows.
+struct RowMaps {
+  CUtensorMap m128, m96, m64;
+  bool make(const void* p, int64_t ld, int R, int width) {
+    return map_rows(&m128, p, ld, R, width, 128) && map_rows(&m96, p, ld, R, width, 96) &&
+           map_rows(&m64, p, ld, R, width, 64);
+  }
+};
 
 // Weights [E][rows][width] with the sum over the rows: as map_sum_rows.
 bool map_sum_weights(CUtensorMap* m, bool* one, const void* p, int E, int rows, int width) {
@@ -819,12 +847,12 @@ bool map_gate_up(CUtensorMap* m, bool* one, const void* p, int E, int H, int I) 
 }
 
 template <int MODE>
-cudaError_t go(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2, const CUtensorMap& b2, const P& p,
-               int64_t tiles, cudaStream_t st) {
+cudaError_t go(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2, const CUtensorMap& b2,
+               const CUtensorMap& o, const CUtensorMap& o2, const P& p, int64_t tiles, cudaStream_t st) {
   auto kern = ffn_kernel<MODE>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = Smem<MODE>::kBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -840,7 +868,7 @@ cudaError_t go(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2
   if (e != cudaSuccess) return e;
   int pairs = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
   if (pairs == 0) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<MODE>::kBytes);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(2);
     cfg.numAttrs = 1;
@@ -851,7 +879,12 @@ cudaError_t go(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2
   }
   cfg.numAttrs = 2;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(pairs, tiles)));
-  return cudaLaunchKernelEx(&cfg, kern, a, b, a2, b2, p);
+  return cudaLaunchKernelEx(&cfg, kern, a, b, a2, b2, o, o2, p);
+}
+
+template <int MODE>
+cudaError_t go(const CUtensorMap& w, const RowMaps& r, const P& p, int64_t tiles, cudaStream_t st) {
+  return go<MODE>(w, r.m128, r.m96, r.m64, w, w, p, tiles, st);
 }
 
 // Tiles of rows that R rows of E experts can have at most.
@@ -875,18 +908,17 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st) {
   p.h = a.h;
   p.status = a.status;
   p.mt = up(a.I, 128);
-  CUtensorMap ma, mb, mb2;
-  FFN_MAP(map_gate_up(&ma, &p.a_one, a.w_gateup, a.E, a.H, a.I));
-  FFN_MAP(map_rows(&mb, a.x.p, a.x.ld, a.R, a.H, kRowBox));
-  FFN_MAP(map_rows(&mb2, a.x.p, a.x.ld, a.R, a.H, kFewBox));
-  FFN_TRY(go<kGateUp>(ma, mb, ma, mb2, p, row_tiles(a.R, a.E, p.mt), st));
+  CUtensorMap w;
+  RowMaps r;
+  FFN_MAP(map_gate_up(&w, &p.a_one, a.w_gateup, a.E, a.H, a.I));
+  FFN_MAP(r.make(a.x.p, a.x.ld, a.R, a.H));
+  FFN_TRY(go<kGateUp>(w, r, p, row_tiles(a.R, a.E, p.mt), st));
   if (a.y.p == nullptr) return cudaSuccess;
   p.out = Out{a.y.p, a.y.ld, a.y.type};
   p.mt = up(a.H, 256);
-  FFN_MAP(map_down(&ma, a.w_down, a.E, a.H, a.I));
-  FFN_MAP(map_rows(&mb, a.h, a.I, a.R, a.I, kRowBox));
-  FFN_MAP(map_rows(&mb2, a.h, a.I, a.R, a.I, kFewBox));
-  return go<kDown>(ma, mb, ma, mb2, p, row_tiles(a.R, a.E, p.mt), st);
+  FFN_MAP(map_down(&w, a.w_down, a.E, a.H, a.I));
+  FFN_MAP(r.make(a.h, a.I, a.R, a.I));
+  return go<kDown>(w, r, p, row_tiles(a.R, a.E, p.mt), st);
 }
 
 cudaError_t launch_ffn_grad(const FfnGradArgs& a, cudaStream_t st) {
@@ -903,38 +935,41 @@ cudaError_t launch_ffn_grad(const FfnGradArgs& a, cudaStream_t st) {
   p.da = a.da;
   p.h = a.h;
   p.status = a.status;
-  CUtensorMap ma, mb, ma2, mb2;
+  CUtensorMap w;
+  RowMaps r;
   p.mt = up(a.I, 256);
-  FFN_MAP(map_sum_weights(&ma, &p.a_one, a.w_down, a.E, a.H, a.I));
-  FFN_MAP(map_rows(&mb, a.dy.p, a.dy.ld, a.R, a.H, kRowBox));
-  FFN_MAP(map_rows(&mb2, a.dy.p, a.dy.ld, a.R, a.H, kFewBox));
-  FFN_TRY(go<kDh>(ma, mb, ma, mb2, p, row_tiles(a.R, a.E, p.mt), st));
+  FFN_MAP(map_sum_weights(&w, &p.a_one, a.w_down, a.E, a.H, a.I));
+  FFN_MAP(r.make(a.dy.p, a.dy.ld, a.R, a.H));
+  FFN_TRY(go<kDh>(w, r, p, row_tiles(a.R, a.E, p.mt), st));
   if (a.dx.p != nullptr) {
     p.out = Out{a.dx.p, a.dx.ld, a.dx.type};
     p.mt = up(a.H, 256);
-    FFN_MAP(map_sum_weights(&ma, &p.a_one, a.w_gateup, a.E, 2 * a.I, a.H));
-    FFN_MAP(map_rows(&mb, a.da, 2 * a.I, a.R, 2 * a.I, kRowBox));
-    FFN_MAP(map_rows(&mb2, a.da, 2 * a.I, a.R, 2 * a.I, kFewBox));
-    FFN_TRY(go<kDx>(ma, mb, ma, mb2, p, row_tiles(a.R, a.E, p.mt), st));
+    FFN_MAP(map_sum_weights(&w, &p.a_one, a.w_gateup, a.E, 2 * a.I, a.H));
+    FFN_MAP(r.make(a.da, 2 * a.I, a.R, 2 * a.I));
+    FFN_TRY(go<kDx>(w, r, p, row_tiles(a.R, a.E, p.mt), st));
   }
   if (a.dw_gateup == nullptr && a.dw_down == nullptr) return cudaSuccess;
   p.dwgu = a.dw_gateup;
   p.dwd = a.dw_down;
   p.dw_type = a.dw_type;
   p.accumulate = a.accumulate;
-  p.tc[0] = tile_cols(a.H), p.tc[1] = tile_cols(a.I);
-  p.nt[0] = up(a.H, p.tc[0]), p.nt[1] = up(a.I, p.tc[1]);
+  p.nt[0] = up(a.H, 256), p.nt[1] = up(a.I, 256);
   p.tgu = a.dw_gateup != nullptr ? up(2 * a.I, 256) * p.nt[0] : 0;
   p.tall = p.tgu + (a.dw_down != nullptr ? up(a.H, 256) * p.nt[1] : 0);
+  CUtensorMap ma, mb, ma2, mb2, mo, mo2;
   FFN_MAP(map_sum_rows(&ma2, &p.a2_one, a.dy.p, a.dy.ld, a.R, a.H, true));
-  FFN_MAP(map_sum_rows(&mb2, &p.b2_one, a.h, a.I, a.R, a.I, whole_halves(a.I)));
+  FFN_MAP(map_sum_rows(&mb2, &p.b2_one, a.h, a.I, a.R, a.I, a.I % 128 == 0));
   if (a.dw_gateup != nullptr) {
     FFN_MAP(map_sum_rows(&ma, &p.a_one, a.da, 2 * a.I, a.R, 2 * a.I, true));
-    FFN_MAP(map_sum_rows(&mb, &p.b_one, a.x.p, a.x.ld, a.R, a.H, whole_halves(a.H)));
+    FFN_MAP(map_sum_rows(&mb, &p.b_one, a.x.p, a.x.ld, a.R, a.H, a.H % 128 == 0));
+    FFN_MAP(map_grad(&mo, a.dw_gateup, a.dw_type, a.E, 2 * a.I, a.H));
   } else {
     ma = ma2, mb = mb2;
   }
-  return go<kGrad>(ma, mb, ma2, mb2, p, static_cast<int64_t>(p.tall) * a.E, st);
+  if (a.dw_down != nullptr) FFN_MAP(map_grad(&mo2, a.dw_down, a.dw_type, a.E, a.H, a.I));
+  if (a.dw_gateup == nullptr) mo = mo2;
+  if (a.dw_down == nullptr) mo2 = mo;
+  return go<kGrad>(ma, mb, ma2, mb2, mo, mo2, p, static_cast<int64_t>(p.tall) * a.E, st);
 }
 
 }  // namespace blk
