@@ -2,9 +2,8 @@
 //
 // Bound by HBM: save reads a row and writes a byte per element and a byte per
 // 32; load reads those and writes a row, or the k rows of a token's routes, so
-// that a token kept once is read once whatever k is.  One warp moves up to 1,024
-// columns of one row in pieces of 256 (rows.cuh), all its loads in flight
-// together; there is no barrier, and a group's largest value goes over the four
+// that a token kept once is read once whatever k is.  One warp moves a few pieces
+// of 256 columns of one row (rows.cuh), all its loads in flight together; there is no barrier, and a group's largest value goes over the four
 // lanes (sixteen, thirty-two for rows on even and odd elements) that hold it.
 #include <algorithm>
 #include <type_traits>
@@ -18,54 +17,77 @@ namespace blk {
 
 namespace {
 
-constexpr int kPieces = 4;  // of 256 columns, per warp
-constexpr int kWarps = 8;   // per CTA
+constexpr int kWarps = 8;  // per CTA
+// Pieces of 256 columns per warp.  Saving fp32 rows of 16,384 x 2,560: 39.6 us with
+// one, 38 with two and four; bf16 rows 32, 27.4, 27.1.  Loading them: 36 (fp32)
+// and 31.6 us (bf16) with one, 35 and 28.4 with four, no better with eight; but
+// 509 x 1,001 takes 2.5 us with one and 5 with four, so few rows get one.
+constexpr int kSavePieces = 2, kLoadPieces = 4;
 
 // Which row and which columns this warp has; false: none.
-__device__ __forceinline__ bool my_part(int T, int parts, int64_t& t, int& base) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  t = i / parts;
-  base = static_cast<int>(i - t * parts) * (kPieces * 256);
+template <int PIECES>
+__device__ __forceinline__ bool my_part(int T, int64_t& t, int& base) {
+  t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  base = blockIdx.y * (PIECES * 256);
   return t < T;
 }
 
 // Eight bytes of a row of bytes: one access for U = 8, pairs for U = 2.
 template <int U>
-__device__ __forceinline__ void load_bytes(const uint8_t* row, const Cols<U>& c, int H, uint8_t (&b)[8]) {
-  if (U == 8 && c.first + 8 <= H) {
-    const uint2 v = *reinterpret_cast<const uint2*>(row + c.first);
+__device__ __forceinline__ uint2 load_bytes(const uint8_t* row, const Cols<U>& c, int H) {
+  if (U == 8 && c.first + 8 <= H) return *reinterpret_cast<const uint2*>(row + c.first);
+  uint32_t v[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = static_cast<uint8_t>((i < 4 ? v.x : v.y) >> (8 * (i & 3)));
+  for (int i = 0; i < 8; i += 2) {
+    const int a = c.at(i);
+    uint32_t two;
+    if (U == 2 && a + 1 < H)
+      two = *reinterpret_cast<const uint16_t*>(row + a);
+    else
+      two = (a < H ? row[a] : 0) | (c.at(i + 1) < H ? row[c.at(i + 1)] : 0) << 8;
+    v[i / 4] |= two << (8 * (i & 3));
+  }
+  return make_uint2(v[0], v[1]);
+}
+template <int U>
+__device__ __forceinline__ void store_bytes(uint8_t* row, const Cols<U>& c, int H, uint2 b) {
+  if (U == 8 && c.first + 8 <= H) {
+    *reinterpret_cast<uint2*>(row + c.first) = b;
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     const int a = c.at(i);
+    const uint32_t two = (i < 4 ? b.x : b.y) >> (8 * (i & 3));
     if (U == 2 && a + 1 < H) {
-      const uint32_t v = *reinterpret_cast<const uint16_t*>(row + a);
-      b[i] = static_cast<uint8_t>(v);
-      b[i + 1] = static_cast<uint8_t>(v >> 8);
+      *reinterpret_cast<uint16_t*>(row + a) = static_cast<uint16_t>(two);
     } else {
-      b[i] = a < H ? row[a] : 0;
-      b[i + 1] = c.at(i + 1) < H ? row[c.at(i + 1)] : 0;
+      if (a < H) row[a] = static_cast<uint8_t>(two);
+      if (c.at(i + 1) < H) row[c.at(i + 1)] = static_cast<uint8_t>(two >> 8);
     }
   }
 }
+
+// Bits of the largest |x| of each of the lane's units.
 template <int U>
-__device__ __forceinline__ void store_bytes(uint8_t* row, const Cols<U>& c, int H, const uint32_t (&b)[8]) {
-  if (U == 8 && c.first + 8 <= H) {
-    *reinterpret_cast<uint2*>(row + c.first) =
-        make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
-    return;
-  }
+__device__ __forceinline__ void unit_max(const Raw8<float>& r, uint32_t (&m)[8 / U]) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const int a = c.at(i);
-    if (U == 2 && a + 1 < H) {
-      *reinterpret_cast<uint16_t*>(row + a) = static_cast<uint16_t>(b[i] | b[i + 1] << 8);
-    } else {
-      if (a < H) row[a] = static_cast<uint8_t>(b[i]);
-      if (c.at(i + 1) < H) row[c.at(i + 1)] = static_cast<uint8_t>(b[i + 1]);
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = __float_as_uint(r.v[i]) & 0x7fffffffu;
+    m[i / U] = i % U == 0 ? a : max(m[i / U], a);
+  }
+}
+template <int U>
+__device__ __forceinline__ void unit_max(const Raw8<bf16_t>& r, uint32_t (&m)[8 / U]) {
+  if constexpr (U == 8) {
+    const uint32_t two = __vmaxu2(__vmaxu2(r.v[0] & 0x7fff7fffu, r.v[1] & 0x7fff7fffu),
+                                  __vmaxu2(r.v[2] & 0x7fff7fffu, r.v[3] & 0x7fff7fffu));
+    m[0] = max(two << 16, two & 0x7fff0000u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t a = (i & 1 ? r.v[i / 2] : r.v[i / 2] << 16) & 0x7fff0000u;
+      m[i / U] = i % U == 0 ? a : max(m[i / U], a);
     }
   }
 }
@@ -88,55 +110,65 @@ __device__ __forceinline__ void group_max(uint32_t (&m)[8 / U]) {
 
 template <typename T_, int U>
 __global__ void __launch_bounds__(kWarps * 32)
-    save_kernel(const T_* __restrict__ x, int64_t ldx, int T, int H, int parts, uint8_t* q, int64_t ldq, uint8_t* exp,
+    save_kernel(const T_* __restrict__ x, int64_t ldx, int T, int H, uint8_t* q, int64_t ldq, uint8_t* exp,
                 int64_t ld_exp) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   int64_t t;
   int base;
-  if (!my_part(T, parts, t, base)) return;
-  Raw8<T_> r[kPieces];
+  if (!my_part<kSavePieces>(T, t, base)) return;
+  Raw8<T_> r[kSavePieces];
 #pragma unroll
-  for (int p = 0; p < kPieces; ++p)
+  for (int p = 0; p < kSavePieces; ++p)
     if (base + p * 256 < H) load8<U>(x + t * ldx, Cols<U>(base + p * 256, lane, 32), H, r[p]);
 #pragma unroll
-  for (int p = 0; p < kPieces; ++p) {
+  for (int p = 0; p < kSavePieces; ++p) {
     if (base + p * 256 >= H) break;
     const Cols<U> c(base + p * 256, lane, 32);
-    const V8 v = unpack(r[p]);
     uint32_t m[8 / U];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t a = __float_as_uint(el(v, i)) & 0x7fffffffu;
-      m[i / U] = i % U == 0 ? a : max(m[i / U], a);
-    }
+    unit_max<U>(r[p], m);
     group_max<U>(m);
-    uint32_t b[8];
+    const V8 v = unpack(r[p]);
+    float w[8], inv[8 / U];
+    bool top = false;
 #pragma unroll
     for (int i = 0; i < 8 / U; ++i) {
       const uint32_t e = exp_byte(m[i]);
-      const float inv = inv_scale(e);
-#pragma unroll
-      for (int j = 0; j < U; ++j) b[i * U + j] = static_cast<uint32_t>(to_q8(el(v, i * U + j), inv)) & 255u;
+      inv[i] = inv_scale(e);
+      top |= e == 248;
       const int a = c.at(i * U);
       if (a % kGroup == 0 && a < H) exp[t * ld_exp + a / kGroup] = static_cast<uint8_t>(e);
     }
-    store_bytes<U>(q + t * ldq, c, H, b);
+    // the values over their scales (exact), so that all eight go on alike
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = el(v, i) * inv[i / U];
+    store_bytes<U>(q + t * ldq, c, H,
+                   make_uint2(q8x4(w[0], w[1], w[2], w[3], 1.f, top), q8x4(w[4], w[5], w[6], w[7], 1.f, top)));
   }
 }
 
-template <typename T_, int U>
+template <typename T_, int U, int PIECES>
 __global__ void __launch_bounds__(kWarps * 32)
     load_kernel(const uint8_t* __restrict__ q, int64_t ldq, const uint8_t* __restrict__ exp, int64_t ld_exp, int T,
-                int H, int parts, const int32_t* __restrict__ slot_of, const float* __restrict__ w, int k, int R,
-                T_* out, int64_t ld_out, int32_t* status) {
+                int H, const int32_t* __restrict__ slot_of, const float* __restrict__ w, int k, int R, T_* out,
+                int64_t ld_out, int32_t* status) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   int64_t t;
   int base;
-  if (!my_part(T, parts, t, base)) return;
+  if (!my_part<PIECES>(T, t, base)) return;
+  uint2 b[PIECES];
+  uint32_t e[PIECES][8 / U];
+#pragma unroll
+  for (int p = 0; p < PIECES; ++p) {
+    if (base + p * 256 >= H) break;
+    const Cols<U> c(base + p * 256, lane, 32);
+    b[p] = load_bytes<U>(q + t * ldq, c, H);
+#pragma unroll
+    for (int i = 0; i < 8 / U; ++i) e[p][i] = c.at(i * U) < H ? exp[t * ld_exp + c.at(i * U) / kGroup] : 0;
+  }
   int slot = -1;
   float weight = 1.f;
   if (slot_of != nullptr && lane < k) {
@@ -147,30 +179,22 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     if (w != nullptr) weight = w[t * k + lane];
   }
-  uint8_t b[kPieces][8];
-  uint32_t e[kPieces][8 / U];
 #pragma unroll
-  for (int p = 0; p < kPieces; ++p) {
+  for (int p = 0; p < PIECES; ++p) {
     if (base + p * 256 >= H) break;
     const Cols<U> c(base + p * 256, lane, 32);
-    load_bytes<U>(q + t * ldq, c, H, b[p]);
+    V8 v;
 #pragma unroll
-    for (int i = 0; i < 8 / U; ++i) e[p][i] = c.at(i * U) < H ? exp[t * ld_exp + c.at(i * U) / kGroup] : 0;
-  }
-  V8 v[kPieces];
-#pragma unroll
-  for (int p = 0; p < kPieces; ++p)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      el(v[p], i) = base + p * 256 < H ? static_cast<float>(static_cast<int8_t>(b[p][i])) * scale_of(e[p][i / U]) : 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int64_t s = slot_of == nullptr ? t : __shfl_sync(0xffffffffu, slot, j);
-    const float f = __shfl_sync(0xffffffffu, weight, j);
-    if (s < 0) continue;
-#pragma unroll
-    for (int p = 0; p < kPieces; ++p)
-      if (base + p * 256 < H)
-        store8<U>(out + s * ld_out, Cols<U>(base + p * 256, lane, 32), H, w != nullptr ? v[p] * f : v[p]);
+    for (int i = 0; i < 8; ++i) el(v, i) = q8_value(i < 4 ? b[p].x : b[p].y, i & 3, scale_of(e[p][i / U]));
+    if (slot_of == nullptr) {
+      store8<U>(out + t * ld_out, c, H, v);
+      continue;
+    }
+    for (int j = 0; j < k; ++j) {
+      const int64_t s = __shfl_sync(0xffffffffu, slot, j);
+      const float f = __shfl_sync(0xffffffffu, weight, j);
+      if (s >= 0) store8<U>(out + s * ld_out, c, H, w != nullptr ? v * f : v);
+    }
   }
 }
 
@@ -192,32 +216,31 @@ cudaError_t by_type(int type, int unit, F&& f) {
   return type == MOE_ROW_F32 ? g(float()) : g(bf16_t());
 }
 
-struct Grid {
-  int parts;
-  int64_t ctas;
-  Grid(int T, int H)
-      : parts((H + kPieces * 256 - 1) / (kPieces * 256)), ctas((static_cast<int64_t>(T) * parts + kWarps - 1) / kWarps) {}
-};
+inline dim3 grid_of(int T, int H, int pieces) {
+  return dim3((T + kWarps - 1) / kWarps, (H + pieces * 256 - 1) / (pieces * 256));
+}
 
 }  // namespace
 
 cudaError_t launch_checkpoint_save(const Rows& x, int T, int H, const Bytes& q, const Bytes& exp, cudaStream_t st) {
-  const Grid g(T, H);
   return by_type(x.type, unit_of(x, q), [&](auto t, auto u) {
     using T_ = decltype(t);
-    return launch_pdl(save_kernel<T_, decltype(u)::value>, dim3(static_cast<unsigned>(g.ctas)), dim3(kWarps * 32), 0,
-                      st, static_cast<const T_*>(x.p), x.ld, T, H, g.parts, q.p, q.ld, exp.p, exp.ld);
+    return launch_pdl(save_kernel<T_, decltype(u)::value>, grid_of(T, H, kSavePieces), dim3(kWarps * 32), 0,
+                      st, static_cast<const T_*>(x.p), x.ld, T, H, q.p, q.ld, exp.p, exp.ld);
   });
 }
 
 cudaError_t launch_checkpoint_load(const Bytes& q, const Bytes& exp, int T, int H, const int32_t* slot_of,
                                    const float* w, int k, int R, const Rows& out, int32_t* status, cudaStream_t st) {
-  const Grid g(T, H);
+  const bool few = static_cast<int64_t>(T) * ((H + 1023) / 1024) < 16 * sm_count();  // warps of four pieces
   return by_type(out.type, unit_of(out, q), [&](auto t, auto u) {
     using T_ = decltype(t);
-    return launch_pdl(load_kernel<T_, decltype(u)::value>, dim3(static_cast<unsigned>(g.ctas)), dim3(kWarps * 32), 0,
-                      st, q.p, q.ld, exp.p, exp.ld, T, H, g.parts, slot_of, w, k, R, static_cast<T_*>(out.p), out.ld,
-                      status);
+    constexpr int U = decltype(u)::value;
+    auto go = [&](auto kern, int pieces) {
+      return launch_pdl(kern, grid_of(T, H, pieces), dim3(kWarps * 32), 0, st, q.p, q.ld, exp.p, exp.ld, T, H, slot_of, w,
+                        k, R, static_cast<T_*>(out.p), out.ld, status);
+    };
+    return few ? go(load_kernel<T_, U, 1>, 1) : go(load_kernel<T_, U, kLoadPieces>, kLoadPieces);
   });
 }
 

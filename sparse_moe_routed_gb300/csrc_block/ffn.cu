@@ -298,17 +298,16 @@ __device__ __forceinline__ uint2 to_bytes(const V8& v, uint32_t& e) {
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   e = exp_byte(m);
   const float inv = inv_scale(e);
-  uint32_t b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = static_cast<uint32_t>(to_q8(el(v, i), inv)) & 255u;
-  return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+  const bool top = e == 248;
+  return make_uint2(q8x4(el(v, 0), el(v, 1), el(v, 2), el(v, 3), inv, top),
+                    q8x4(el(v, 4), el(v, 5), el(v, 6), el(v, 7), inv, top));
 }
 __device__ __forceinline__ V8 from_bytes(uint2 q, uint32_t e) {
   const float s = scale_of(e);
   V8 v;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    el(v, i) = static_cast<float>(static_cast<int8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)))) * s;
+    el(v, i) = q8_value(i < 4 ? q.x : q.y, i & 3, s);
   return v;
 }
 
@@ -466,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0 || warp == 10) {
     // ------------------------------------------------------------- operands
-    if (lane == 0) {
+    if (pair::elect()) {
       // Operands are read again by the tiles beside; results are not (weights and
       // rows alike: 1 to 3 % over normal, at 4,096 and 16,384 tokens and dense).
       const uint64_t pol = ptx::policy_evict_last();
@@ -544,7 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMAs
-    if (rank == 0 && lane == 0) {
+    // The whole warp goes along, so that it is converged where one lane issues;
+    // nothing in the loop waits for its lanes, which may give up one by one.
+    if (rank == 0) {
+      const bool one = pair::elect();
       Pipe<kStages> pipe;
       int acc = 0;
       uint32_t aph = 0;
@@ -564,23 +566,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = pair::wait<0>(full + 8 * pipe.s, pipe.ph, abort, p.status);
           if (!ok) break;
           const uint64_t da = da0 + pipe.s * (kStageBytes >> 4), db = db0 + pipe.s * (kStageBytes >> 4);
-          pair::mma(d, da, db, id, left != tl.k);
-          if (left >= kK) {
+          if (one) {
+            pair::mma(d, da, db, id, left != tl.k);
+            if (left >= kK) {
 #pragma unroll
-            for (int kk = 1; kk < kK / 16; ++kk) pair::mma(d, da + kk * kStepA, db + kk * kStepB, id, 1);
-          } else {
+              for (int kk = 1; kk < kK / 16; ++kk) pair::mma(d, da + kk * kStepA, db + kk * kStepB, id, 1);
+            } else {
 #pragma unroll
-            for (int kk = 1; kk < kK / 16; ++kk)
-              if (kk * 16 < left) pair::mma(d, da + kk * kStepA, db + kk * kStepB, id, 1);
+              for (int kk = 1; kk < kK / 16; ++kk)
+                if (kk * 16 < left) pair::mma(d, da + kk * kStepA, db + kk * kStepB, id, 1);
+            }
+            pair::commit_both(empty + 8 * pipe.s);
           }
-          pair::commit_both(empty + 8 * pipe.s);
           pipe.next();
         }
-        if (ok) pair::commit_both(accfull + 8 * acc);
+        if (ok && one) pair::commit_both(accfull + 8 * acc);
         acc ^= 1;
         if (acc == 0) aph ^= 1u;
       }
-      if (!ok) {  // the MMAs that were issued
+      if (__any_sync(0xffffffffu, !ok) && one) {  // the MMAs that were issued
         pair::commit_both(done);
         pair::drain(done, 0);
       }

@@ -29,9 +29,27 @@ __device__ __forceinline__ uint32_t exp_byte(uint32_t amax_bits) {
 // group reads back as NaN whatever its q are).
 __device__ __forceinline__ float inv_scale(uint32_t b) { return __uint_as_float((254u - min(b, 253u)) << 23); }
 
-__device__ __forceinline__ int to_q8(float x, float inv) {
-  // NaN converts to 0
-  return min(max(__float2int_rn(x * inv), -127), 127);
+// Four values to four bytes.  Adding 1.5 * 2^23 rounds the (exact) product to a
+// whole number, ties to even, and leaves its two's complement in the low byte.
+// Only exponent byte 248 can hold values past 127.
+__device__ __forceinline__ uint32_t q8x4(float a, float b, float c, float d, float inv, bool top) {
+  if (top) {
+    const float most = 127.f / inv;
+    a = fminf(fmaxf(a, -most), most);
+    b = fminf(fmaxf(b, -most), most);
+    c = fminf(fmaxf(c, -most), most);
+    d = fminf(fmaxf(d, -most), most);
+  }
+  constexpr float kRound = 12582912.f;
+  const uint32_t ra = __float_as_uint(fmaf(a, inv, kRound)), rb = __float_as_uint(fmaf(b, inv, kRound)),
+                 rc = __float_as_uint(fmaf(c, inv, kRound)), rd = __float_as_uint(fmaf(d, inv, kRound));
+  return __byte_perm(__byte_perm(ra, rb, 0x0040), __byte_perm(rc, rd, 0x0040), 0x5410);
+}
+
+// Byte i of four as a value: 2^23 + 128 + q is a float whose low byte is q + 128.
+__device__ __forceinline__ float q8_value(uint32_t four, int i, float scale) {
+  const uint32_t f = __byte_perm(four ^ 0x80808080u, 0x4b000000u, 0x7440u | i);
+  return (__uint_as_float(f) - 8388736.f) * scale;
 }
 
 // 2^(b-127) for any byte: 2^-127 is below the normal range, 255 is NaN.
