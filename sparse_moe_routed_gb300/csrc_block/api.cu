@@ -424,7 +424,7 @@ moe_status moe_ffn(const uint16_t* x_perm, int64_t ldx, const uint16_t* w_gateup
 
 size_t moe_ffn_backward_workspace_size(int R, int I) {
   if (R < 0 || I <= 0 || I > kMaxH) return 0;
-  return (static_cast<size_t>(R) * 3 * I * 2 + 15) / 16 * 16;
+  return (static_cast<size_t>(R) * 3 * I * 2 + 15) / 16 * 16 + 16;
 }
 
 moe_status moe_ffn_backward(const uint16_t* dy_perm, int64_t lddy, const uint16_t* x_perm, int64_t ldx,
@@ -472,6 +472,7 @@ moe_status moe_ffn_backward(const uint16_t* dy_perm, int64_t lddy, const uint16_
   a.accumulate = accumulate != 0;
   a.da = static_cast<uint16_t*>(workspace);
   a.h = a.da + static_cast<size_t>(R) * 2 * I;
+  a.queue = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + moe_ffn_backward_workspace_size(R, I) - 16);
   a.status = dev_status;
   return cuda_status(moe::blk::launch_ffn_grad(a, static_cast<cudaStream_t>(stream)));
 }

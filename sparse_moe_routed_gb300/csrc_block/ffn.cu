@@ -21,7 +21,10 @@
 // the even CTA (warp 1) issues the MMAs for both; warps 2 to 9 turn accumulators
 // into results while the next tile's MMAs run (two accumulators of 256 columns
 // fill tensor memory).  Where a sum over rows ends inside 16 of them, warp 11 of
-// each CTA first clears the rows behind in its half.
+// each CTA first clears the rows behind in its half.  Tiles of rows are dealt out
+// in turn; tiles of gradients are claimed from a queue (warp 12 of the even CTA):
+// a pair that fell behind would find its operands gone from L2 and fall back
+// further (some pairs ended at 1,000 us where most did at 850).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -41,7 +44,7 @@ namespace {
 
 enum Mode { kGateUp, kDown, kDh, kDx, kGrad };
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
 constexpr int kEpiWarps = 8;
 constexpr int kK = 64;  // contraction per stage: one 128-byte swizzled row
 constexpr int kABytes = 128 * kK * 2, kBBytes = 128 * kK * 2, kStageBytes = kABytes + kBBytes;
@@ -50,14 +53,15 @@ constexpr int kTurnLd = 36;              // 32 features each: a row and 16 bytes
 constexpr int kTurn = kTurnRows * kTurnLd;
 constexpr int kOut = 32 * 128;           // bytes of a gradient that a warp hands to a copy: 32 rows of 128 bytes
 constexpr int kList = 128;               // tiles of a pair that are looked up ahead
+constexpr int kClaims = 4;               // tiles that are claimed ahead
 
 template <int MODE>
 struct Smem {
   static constexpr int kStages = MODE == kGrad ? 5 : 6;
   static constexpr int kTail = kEpiWarps * (MODE == kGrad ? kOut : kTurn * 4);
-  static constexpr int kBars = 3 * kStages + 4 + 1;
+  static constexpr int kBars = 3 * kStages + 4 + 1 + 2 * kClaims;
   static constexpr int kBytes =
-      1024 + kStages * kStageBytes + kTail + kList * 16 + 16 + kBars * 8 + 8 + 2 * (kMaxE + 1) * 4;
+      1024 + kStages * kStageBytes + kTail + kList * 16 + 16 + 4 * kClaims + kBars * 8 + 8 + 2 * (kMaxE + 1) * 4;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -79,6 +83,7 @@ struct P {
   int mt;             // row launches: 256-feature tiles (gate/up: 128 gate and 128 up)
   int tgu, tall;      // gradients: tiles of dW_gu per expert, of both;
   int nt[2];          // tiles of 256 columns along a row, of dW_gu and dW_d
+  int* queue;         // workspace: tiles of gradients claimed so far
   int32_t* status;
 };
 
@@ -140,28 +145,38 @@ struct Sched {
   }
 };
 
-// A role's way through the pair's tiles.
-template <int MODE>
+// Shared memory through which the claimed tiles go to the roles of both CTAs.
+struct Claims {
+  const volatile int* tile;  // [kClaims]
+  uint32_t full, empty;      // barriers; empty: the even CTA's, of all roles
+  volatile uint32_t* abort;
+  // Roles (one arrival each) that read a claim, of both CTAs: operands, results
+  // and clearing twice, MMAs once.
+  static constexpr int kReaders = 2 * (2 + kEpiWarps + 1) + 1;
+};
+
+// A role's way through the pair's tiles.  WARP: all lanes of a warp go along.
+template <int MODE, bool WARP>
 struct Walk {
   const Sched<MODE>& sc;
-  int t, j = 0, e, l;  // tile, which of the pair's; gradient: expert, tile in it
-  const int step, de, dl;
+  const Claims& cl;
+  int t, j = 0;  // tile, which of the pair's
 
-  __device__ __forceinline__ Walk(const Sched<MODE>& s)
-      : sc(s), t(blockIdx.x >> 1), step(gridDim.x >> 1), de(MODE == kGrad ? step / s.p.tall : 0),
-        dl(MODE == kGrad ? step % s.p.tall : 0) {
-    e = MODE == kGrad ? t / s.p.tall : 0;
-    l = MODE == kGrad ? t % s.p.tall : 0;
-  }
+  __device__ __forceinline__ Walk(const Sched<MODE>& s, const Claims& c) : sc(s), cl(c), t(blockIdx.x >> 1) {}
   __device__ __forceinline__ bool more() const { return t < sc.total; }
   __device__ __forceinline__ void next() {
-    t += step;
     ++j;
-    if (MODE == kGrad) {
-      e += de;
-      l += dl;
-      if (l >= sc.p.tall) l -= sc.p.tall, ++e;
+    if (MODE != kGrad) {
+      t += gridDim.x >> 1;
+      return;
     }
+    const int slot = (j - 1) % kClaims;
+    if (!WARP || (threadIdx.x & 31) == 0) {
+      const bool ok = pair::wait<32, true>(cl.full + 8 * slot, ((j - 1) / kClaims) & 1, cl.abort, sc.p.status);
+      t = ok ? cl.tile[slot] : sc.total;
+      pair::arrive_at(cl.empty + 8 * slot, 0);
+    }
+    if (WARP) t = __shfl_sync(0xffffffffu, t, 0);
   }
   __device__ __forceinline__ Tile tile() const {
     if (MODE != kGrad) {
@@ -170,15 +185,16 @@ struct Walk {
       return sc.rows_tile(v.x, v.y, v.z, v.w);
     }
     Tile r;
-    r.e = e;
+    r.e = t / sc.p.tall;
+    const int l = t - r.e * sc.p.tall;
     r.down = l >= sc.p.tgu;
     const int i = r.down, at = r.down ? l - sc.p.tgu : l, m = at / sc.p.nt[i];
     r.m0 = m * 256;
     r.n0 = (at - m * sc.p.nt[i]) * 256;
     r.n = min(256, (r.down ? sc.p.I : sc.p.H) - r.n0);
     r.N = up(r.n, 32) * 32;
-    r.s0 = sc.off[e];
-    r.k = max(sc.off[e + 1] - r.s0, 0);
+    r.s0 = sc.off[r.e];
+    r.k = max(sc.off[r.e + 1] - r.s0, 0);
     return r;
   }
 };
@@ -399,12 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   int4* list = reinterpret_cast<int4*>(sm + kStages * kStageBytes + kTail);
   uint32_t* misc = reinterpret_cast<uint32_t*>(list + kList);  // tensor memory, abort, tiles
   volatile uint32_t* abort = misc + 1;
-  const uint32_t bars = ptx::smem_u32(misc + 4);
+  int* claimed = reinterpret_cast<int*>(misc + 4);
+  const uint32_t bars = ptx::smem_u32(claimed + kClaims);
   // full: both halves of a stage (even CTA); empty: both have been read (both);
   // tfull: this CTA's half, where the rows behind a sum are cleared (both)
   const uint32_t full = bars, empty = bars + 8 * kStages, tfull = bars + 16 * kStages, accfull = bars + 24 * kStages,
-                 accempty = accfull + 16, done = accempty + 16;
-  int* soff = reinterpret_cast<int*>(misc + 4 + 2 * kBars);
+                 accempty = accfull + 16, done = accempty + 16, qfull = done + 8, qempty = qfull + 8 * kClaims;
+  int* soff = reinterpret_cast<int*>(misc + 4 + kClaims + 2 * kBars);
   int* first = soff + kMaxE + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -421,6 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(accempty + 8 * i, 2 * kEpiWarps);
     }
     ptx::mbar_init(done, 1);
+    for (int i = 0; i < kClaims; ++i) {
+      ptx::mbar_init(qfull + 8 * i, 1);
+      ptx::mbar_init(qempty + 8 * i, Claims::kReaders);
+    }
     ptx::fence_mbar_init();
   }
   if (warp == 1) pair::tmem_alloc(ptx::smem_u32(misc));
@@ -431,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   pdl_wait();
   pdl_trigger();
+  // The first launch of a gradient call empties the queue of its last one.
+  if (MODE == kDh && blockIdx.x == 0 && threadIdx.x == 0) *p.queue = 0;
   // Offsets, kept inside the buffers and rising, whatever they hold.
   for (int i = threadIdx.x; i <= p.E; i += kThreads) soff[i] = min(max(__ldcg(p.offsets + i), 0), p.R);
   __syncthreads();
@@ -463,6 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
 
+  const Claims claims{claimed, qfull, qempty, abort};
+
   if (warp == 0 || warp == 10) {
     // ------------------------------------------------------------- operands
     if (pair::elect()) {
@@ -473,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Pipe<kStages> pipe;
       uint32_t used = 0;
       bool ok = true;
-      for (Walk<MODE> w(sc); w.more() && ok; w.next()) {
+      for (Walk<MODE, false> w(sc, claims); w.more() && ok; w.next()) {
         const Tile tl = w.tile();
         const int half = tl.N / 2;
         const CUtensorMap* a = MODE == kGrad && tl.down ? &ma2 : &ma;
@@ -543,8 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMAs
-    // The whole warp goes along, so that it is converged where one lane issues;
-    // nothing in the loop waits for its lanes, which may give up one by one.
+    // The whole warp goes along, so that it is converged where one lane issues.
+    // Its lanes may give up one by one: nothing within a tile waits for all.
     if (rank == 0) {
       const bool one = pair::elect();
       Pipe<kStages> pipe;
@@ -554,12 +579,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t da0 = kAMn<MODE> ? pair::sdesc_mn_sw128(base) : ptx::sdesc_k_sw128(base);
       const uint64_t db0 = b_mn(MODE) ? pair::sdesc_mn_sw128(base + kABytes) : ptx::sdesc_k_sw128(base + kABytes);
       constexpr uint32_t kStepA = (kAMn<MODE> ? 2048 : 32) >> 4, kStepB = (b_mn(MODE) ? 2048 : 32) >> 4;
-      for (Walk<MODE> w(sc); w.more() && ok; w.next()) {
+      for (Walk<MODE, true> w(sc, claims); w.more() && ok; w.next()) {
         const Tile tl = w.tile();
         if (tl.k == 0) continue;
         const uint32_t id = pair::idesc(tl.N, kAMn<MODE>, b_mn(MODE));
         const uint32_t d = tmem + acc * 256;
-        ok = pair::wait<0>(accempty + 8 * acc, aph ^ 1u, abort, p.status);
+        ok = __all_sync(0xffffffffu, pair::wait<0>(accempty + 8 * acc, aph ^ 1u, abort, p.status));
         if (!ok) break;
         ptx::tc_fence_after();
         for (int left = tl.k; left > 0; left -= kK) {
@@ -580,11 +605,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           pipe.next();
         }
+        ok = __all_sync(0xffffffffu, ok);
         if (ok && one) pair::commit_both(accfull + 8 * acc);
         acc ^= 1;
         if (acc == 0) aph ^= 1u;
       }
-      if (__any_sync(0xffffffffu, !ok) && one) {  // the MMAs that were issued
+      if (!ok && one) {  // the MMAs that were issued
         pair::commit_both(done);
         pair::drain(done, 0);
       }
@@ -595,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Pipe<kStages> pipe;
       uint32_t tph = 0;  // a bit per stage: the phase of its tfull
       bool ok = true;
-      for (Walk<MODE> w(sc); w.more() && ok; w.next()) {
+      for (Walk<MODE, true> w(sc, claims); w.more() && ok; w.next()) {
         const Tile tl = w.tile();
         for (int left = tl.k; left > 0; left -= kK, pipe.next()) {
           if (!ends_inside(left)) continue;
@@ -613,6 +639,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  } else if (warp == 12) {
+    // --------------------------------------------------------------- claims
+    if (MODE == kGrad && rank == 0 && lane == 0) {
+      const int pairs = gridDim.x >> 1;
+      bool ok = true;
+      for (int j = 0, t = 0; t < sc.total && ok; ++j) {
+        const int slot = j % kClaims;
+        t = pairs + atomicAdd(p.queue, 1);
+        ok = pair::wait<32>(qempty + 8 * slot, ((j / kClaims) & 1) ^ 1, abort, p.status);
+        if (!ok) break;
+        for (uint32_t r = 0; r < 2; ++r)
+          pair::send_word(ptx::smem_u32(claimed + slot), qfull + 8 * slot, r, static_cast<uint32_t>(t));
+      }
+    }
   } else {
     // -------------------------------------------------------------- results
     const int q = warp & 3, group = (warp - 2) >> 2;
@@ -622,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tr = lane >> 2, tc = (lane & 3) * 8;  // row and first feature once turned
     int acc = 0;
     uint32_t aph = 0;
-    for (Walk<MODE> w(sc); w.more(); w.next()) {
+    for (Walk<MODE, true> w(sc, claims); w.more(); w.next()) {
       const Tile tl = w.tile();
       if (tl.k != 0) {
         if (!pair::wait_warp<32>(accfull + 8 * acc, aph, abort, p.status)) break;
@@ -938,6 +978,7 @@ cudaError_t launch_ffn_grad(const FfnGradArgs& a, cudaStream_t st) {
   p.act = a.act;
   p.da = a.da;
   p.h = a.h;
+  p.queue = a.queue;
   p.status = a.status;
   CUtensorMap w;
   RowMaps r;

@@ -146,7 +146,8 @@ struct FfnGradArgs {
   Rows dx;
   void *dw_gateup, *dw_down;
   int dw_type, accumulate;
-  uint16_t *da, *h;  // workspace: [R,2I], [R,I]
+  uint16_t *da, *h;  // workspace: [R,2I], [R,I],
+  int* queue;        // a word
   int32_t* status;
 };
 cudaError_t launch_ffn_grad(const FfnGradArgs& a, cudaStream_t st);

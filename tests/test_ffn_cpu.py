@@ -54,7 +54,7 @@ REFUSALS = [
     (ffn_b, dict(e=None), EINVAL), (ffn_b, dict(kind=0), EINVAL), (ffn_b, dict(wgu=None), EINVAL),
     (ffn_b, dict(wd=None), EINVAL), (ffn_b, dict(off=None), EINVAL), (ffn_b, dict(dx=A[0]), EINVAL),
     (ffn_b, dict(dwd=A[8]), EINVAL), (ffn_b, dict(dx=None, dwgu=None, dwd=None), EINVAL), (ffn_b, dict(ws=None), EWS),
-    (ffn_b, dict(wsb=16 * 3 * 32 * 2 - 1), EWS), (ffn_b, dict(ws=EIGHT), EINVAL), (ffn_b, dict(ws=A[7]), EINVAL),
+    (ffn_b, dict(wsb=16 * 3 * 32 * 2 + 15), EWS), (ffn_b, dict(ws=EIGHT), EINVAL), (ffn_b, dict(ws=A[7]), EINVAL),
     (ffn_b, dict(dwgu=C.c_void_p((1 << 20) + 16)), EINVAL), (ffn_b, dict(dxtype=5), EINVAL), (ffn_b, dict(dwtype=2), EINVAL),
     (ffn_b, dict(lddy=8), ESHAPE), (ffn_b, dict(I=12), ENOTSUP), (ffn_b, dict(R=-1), ESHAPE),
 ]
@@ -69,10 +69,11 @@ def test_refused_on_the_host(name, change, want):
 
 
 def test_workspace_size():
-    assert M.moe_ffn_backward_workspace_size(5, 8) == 240
-    assert M.moe_ffn_backward_workspace_size(1, 8) == 48
-    assert M.moe_ffn_backward_workspace_size(40960, 640) == 40960 * 640 * 6
-    assert M.moe_ffn_backward_workspace_size(1 << 20, 65536) == (1 << 36) * 6
+    """dg and du, h, and a word for the queue of tiles, in whole 16 bytes."""
+    assert M.moe_ffn_backward_workspace_size(5, 8) == 240 + 16
+    assert M.moe_ffn_backward_workspace_size(1, 8) == 48 + 16
+    assert M.moe_ffn_backward_workspace_size(40960, 640) == 40960 * 640 * 6 + 16
+    assert M.moe_ffn_backward_workspace_size(1 << 20, 65536) == (1 << 36) * 6 + 16
     assert M.moe_ffn_backward_workspace_size(-1, 8) == 0 == M.moe_ffn_backward_workspace_size(1, 0)
 
 
