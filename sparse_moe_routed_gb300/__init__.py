@@ -12,8 +12,9 @@ from ._block import (moe_block_norm, moe_block_norm_backward, moe_block_norm_wor
                      moe_ffn, moe_ffn_backward, moe_ffn_backward_workspace_size, moe_route_backward,
                      moe_route_backward_workspace_size)
 from .layer import CachedMoELayer, MoELayer, MoEStack, PrefillRing, pack_layer_experts
+from .train import MoETrainLayer
 
-__all__ = ["_lib", "MoEError", "MoELayer", "CachedMoELayer", "MoEStack", "PrefillRing", "pack_layer_experts",
+__all__ = ["_lib", "MoEError", "MoELayer", "CachedMoELayer", "MoEStack", "MoETrainLayer", "PrefillRing", "pack_layer_experts",
            "moe_cache_plan", "moe_cache_fetch", "moe_expert_swiglu_cached", "moe_route", "moe_permute", "moe_expert_gateup", "moe_expert_down",
            "moe_grouped_swiglu", "moe_combine", "route_block_dedup", "moe_rmsnorm", "moe_route_noalloc",
            "moe_route_recall", "moe_dispatch", "moe_dispatch_backward", "moe_collect", "moe_collect_backward",

@@ -22,7 +22,7 @@
 // into results while the next tile's MMAs run (two accumulators of 256 columns
 // fill tensor memory).  Where a sum over rows ends inside 16 of them, warp 11 of
 // each CTA first clears the rows behind in its half.  Tiles of rows are dealt out
-// in turn; tiles of gradients are claimed from a queue (warp 12 of the even CTA):
+// in turn; tiles of gradients are claimed from a queue (warp 12):
 // a pair that fell behind would find its operands gone from L2 and fall back
 // further (some pairs ended at 1,000 us where most did at 850).
 #include <cuda.h>
@@ -61,7 +61,7 @@ struct Smem {
   static constexpr int kTail = kEpiWarps * (MODE == kGrad ? kOut : kTurn * 4);
   static constexpr int kBars = 3 * kStages + 4 + 1 + 2 * kClaims;
   static constexpr int kBytes =
-      1024 + kStages * kStageBytes + kTail + kList * 16 + 16 + 4 * kClaims + kBars * 8 + 8 + 2 * (kMaxE + 1) * 4;
+      1024 + kStages * kStageBytes + kTail + kList * 16 + 16 + 8 * kClaims + kBars * 8 + 8 + 2 * (kMaxE + 1) * 4;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -145,10 +145,14 @@ struct Sched {
   }
 };
 
-// Shared memory through which the claimed tiles go to the roles of both CTAs.
+// Shared memory through which the claimed tiles go to a CTA's roles.  The claim
+// itself crosses over as 64 bits that the odd CTA polls for: its number, so that it
+// is known when it is there, and the tile.  (Sent with an arrival and its bytes
+// counted on the odd CTA's barrier, claims were missed by some roles, once in some
+// 10^7: the barrier was found a phase off.)
 struct Claims {
-  const volatile int* tile;  // [kClaims]
-  uint32_t full, empty;      // barriers; empty: the even CTA's, of all roles
+  uint32_t at;           // [kClaims] 64 bits: number + 1 (upper half), tile
+  uint32_t full, empty;  // barriers; empty: the even CTA's, of both CTAs' roles
   volatile uint32_t* abort;
   // Roles (one arrival each) that read a claim, of both CTAs: operands, results
   // and clearing twice, MMAs once.
@@ -172,8 +176,8 @@ struct Walk {
     }
     const int slot = (j - 1) % kClaims;
     if (!WARP || (threadIdx.x & 31) == 0) {
-      const bool ok = pair::wait<32, true>(cl.full + 8 * slot, ((j - 1) / kClaims) & 1, cl.abort, sc.p.status);
-      t = ok ? cl.tile[slot] : sc.total;
+      const bool ok = pair::wait<32>(cl.full + 8 * slot, ((j - 1) / kClaims) & 1, cl.abort, sc.p.status);
+      t = ok ? static_cast<int>(pair::get64(cl.at + 8 * slot, pair::cta_rank())) : sc.total;
       pair::arrive_at(cl.empty + 8 * slot, 0);
     }
     if (WARP) t = __shfl_sync(0xffffffffu, t, 0);
@@ -277,7 +281,10 @@ __device__ __forceinline__ void add_grad(const P& p, void* base, const float (&v
   }
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + expf(-g)); }
+// The fast exponential and quotient are off by 2 + 1.2 |g| and 2 units in the
+// last place of fp32 (a 2^-17th of the value at |g| = 80); what comes of it is
+// rounded to bf16.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
 // Eight bytes of a row in 8 bits, at any alignment.
 __device__ __forceinline__ uint2 load_q8(const uint8_t* q, bool whole) {
@@ -415,19 +422,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   int4* list = reinterpret_cast<int4*>(sm + kStages * kStageBytes + kTail);
   uint32_t* misc = reinterpret_cast<uint32_t*>(list + kList);  // tensor memory, abort, tiles
   volatile uint32_t* abort = misc + 1;
-  int* claimed = reinterpret_cast<int*>(misc + 4);
-  const uint32_t bars = ptx::smem_u32(claimed + kClaims);
+  const uint32_t claimed = ptx::smem_u32(misc + 4), bars = claimed + 8 * kClaims;
   // full: both halves of a stage (even CTA); empty: both have been read (both);
   // tfull: this CTA's half, where the rows behind a sum are cleared (both)
   const uint32_t full = bars, empty = bars + 8 * kStages, tfull = bars + 16 * kStages, accfull = bars + 24 * kStages,
                  accempty = accfull + 16, done = accempty + 16, qfull = done + 8, qempty = qfull + 8 * kClaims;
-  int* soff = reinterpret_cast<int*>(misc + 4 + kClaims + 2 * kBars);
+  int* soff = reinterpret_cast<int*>(misc + 4 + 2 * kClaims + 2 * kBars);
   int* first = soff + kMaxE + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = pair::cta_rank();
   if (threadIdx.x == 0) {
     misc[1] = 0;
+    for (int i = 0; i < kClaims; ++i) pair::put64(claimed + 8 * i, 0);
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(full + 8 * i, MODE == kGrad ? 2 : 1);
       ptx::mbar_init(empty + 8 * i, 1);
@@ -569,7 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMAs
     // The whole warp goes along, so that it is converged where one lane issues.
-    // Its lanes may give up one by one: nothing within a tile waits for all.
+    // Every lane has seen a phase end before that lane's commit lets the barrier
+    // go on: one that came late would find the next phase of the same parity.
     if (rank == 0) {
       const bool one = pair::elect();
       Pipe<kStages> pipe;
@@ -588,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ptx::tc_fence_after();
         for (int left = tl.k; left > 0; left -= kK) {
-          ok = pair::wait<0>(full + 8 * pipe.s, pipe.ph, abort, p.status);
+          ok = __all_sync(0xffffffffu, pair::wait<0>(full + 8 * pipe.s, pipe.ph, abort, p.status));
           if (!ok) break;
           const uint64_t da = da0 + pipe.s * (kStageBytes >> 4), db = db0 + pipe.s * (kStageBytes >> 4);
           if (one) {
@@ -605,7 +613,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           pipe.next();
         }
-        ok = __all_sync(0xffffffffu, ok);
         if (ok && one) pair::commit_both(accfull + 8 * acc);
         acc ^= 1;
         if (acc == 0) aph ^= 1u;
@@ -641,16 +648,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 12) {
     // --------------------------------------------------------------- claims
-    if (MODE == kGrad && rank == 0 && lane == 0) {
+    if (MODE == kGrad && lane == 0) {
       const int pairs = gridDim.x >> 1;
       bool ok = true;
       for (int j = 0, t = 0; t < sc.total && ok; ++j) {
         const int slot = j % kClaims;
-        t = pairs + atomicAdd(p.queue, 1);
-        ok = pair::wait<32>(qempty + 8 * slot, ((j / kClaims) & 1) ^ 1, abort, p.status);
+        if (rank == 0) {
+          t = pairs + atomicAdd(p.queue, 1);
+          ok = pair::wait<32>(qempty + 8 * slot, ((j / kClaims) & 1) ^ 1, abort, p.status);
+        } else {
+          uint64_t v = 0;
+          ok = pair::poll<32>([&] { return ((v = pair::get64(claimed + 8 * slot, 0)) >> 32) == j + 1u; }, abort, p.status);
+          t = static_cast<int>(v);
+        }
         if (!ok) break;
-        for (uint32_t r = 0; r < 2; ++r)
-          pair::send_word(ptx::smem_u32(claimed + slot), qfull + 8 * slot, r, static_cast<uint32_t>(t));
+        pair::put64(claimed + 8 * slot, static_cast<uint64_t>(j + 1u) << 32 | static_cast<uint32_t>(t));
+        ptx::mbar_arrive(qfull + 8 * slot);
       }
     }
   } else {
@@ -662,8 +675,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tr = lane >> 2, tc = (lane & 3) * 8;  // row and first feature once turned
     int acc = 0;
     uint32_t aph = 0;
+    Kept ahead[2];
+    auto load_ahead = [&](const Tile& tl, int c) {
+      const int m = tl.m0 + static_cast<int>(rank) * 128 + q * 32 + tc;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (m < p.I && c + tr + h * 8 < tl.n) ahead[h].load(p, static_cast<int64_t>(tl.n0) + c + tr + h * 8, m);
+    };
     for (Walk<MODE, true> w(sc, claims); w.more(); w.next()) {
       const Tile tl = w.tile();
+      if (MODE == kDh) load_ahead(tl, group * 16);
       if (tl.k != 0) {
         if (!pair::wait_warp<32>(accfull + 8 * acc, aph, abort, p.status)) break;
         ptx::tc_fence_after();
@@ -742,9 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t row = static_cast<int64_t>(tl.n0) + c + tr;
           Kept k[2];
           if (MODE == kDh) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (m < width && c + tr + h * 8 < tl.n) k[h].load(p, row + h * 8, m);
+            // loaded with the last 16 rows' turn (or before the wait), for the next
+            k[0] = ahead[0], k[1] = ahead[1];
+            load_ahead(tl, c + 32);
           }
           float v[16];
           ptx::tmem_ld16(d + c, v);

@@ -51,26 +51,13 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// For what the other CTA wrote by itself.
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Waits at most kWaitNs (the clock is read every 1,024 polls and starts at the
 // first read), then sets the CTA's abort word and the status.  False: give up.
-template <uint32_t SLEEP_NS, bool CLUSTER = false>
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int32_t* status) {
+template <uint32_t SLEEP_NS, typename F>
+__device__ __forceinline__ bool poll(F&& there, volatile uint32_t* abort, int32_t* status) {
   uint64_t t0 = 0;
   for (uint32_t it = 0;; ++it) {
-    if (CLUSTER ? try_wait_cluster(bar, parity) : try_wait(bar, parity)) return true;
+    if (there()) return true;
     if (SLEEP_NS != 0 && it >= 2) __nanosleep(SLEEP_NS);
     if ((it & 1023u) == 1023u) {
       if (*abort) return false;
@@ -84,6 +71,11 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uin
       }
     }
   }
+}
+
+template <uint32_t SLEEP_NS>
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int32_t* status) {
+  return poll<SLEEP_NS>([=] { return try_wait(bar, parity); }, abort, status);
 }
 
 // The same for a whole warp, of which one lane polls: polls by all lanes of ten
@@ -166,17 +158,21 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src,
 __device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// A word into CTA `rank`'s shared memory at `dst`, with its arrival on the barrier
-// `bar` there (one arrival and four bytes).
-__device__ __forceinline__ void send_word(uint32_t dst, uint32_t bar, uint32_t rank, uint32_t v) {
+// 64 bits of shared memory that one thread writes and any of the pair reads whole,
+// without a barrier.
+__device__ __forceinline__ void put64(uint32_t addr, uint64_t v) {
+  asm volatile("st.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint64_t get64(uint32_t addr, uint32_t rank) {
+  uint64_t v;
   asm volatile(
-      "{\n\t.reg .b32 d, b;\n\t"
-      "mapa.shared::cluster.u32 d, %0, %2;\n\t"
-      "mapa.shared::cluster.u32 b, %1, %2;\n\t"
-      "mbarrier.arrive.expect_tx.shared::cluster.b64 _, [b], 4;\n\t"
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [d], %3, [b];\n\t}\n" ::"r"(dst),
-      "r"(bar), "r"(rank), "r"(v)
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.relaxed.cluster.shared::cluster.b64 %0, [a];\n\t}\n"
+      : "=l"(v)
+      : "r"(addr), "r"(rank)
       : "memory");
+  return v;
 }
 
 // One lane of a converged warp.  tcgen05 instructions take their operands from

@@ -1,0 +1,132 @@
+"""One routed-expert layer in training: its forward pass, what it keeps, its backward pass.
+
+    moe_route -> moe_permute -> moe_dispatch -> moe_ffn -> moe_collect
+
+keeps the routes and their weights, the expert outputs, and, in 8 bits or
+bf16, the tokens and the experts' gate and up values:
+
+    keep     tokens [T,H]        gate and up values [T*k, 2I]
+    "q8"     1 + 1/32 bytes      1 + 1/32 bytes each
+    "bf16"   2 bytes             2 bytes each
+
+and the backward pass is
+
+    moe_collect_backward -> (moe_checkpoint_load | moe_dispatch) ->
+    moe_ffn_backward -> moe_dispatch_backward -> moe_route_backward
+
+Every step runs in the CUDA libraries; this class only owns memory.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _block, _lib
+
+
+class MoETrainLayer:
+    """w_router [E,H], w_gateup [E,2I,H], w_down [E,H,I] bf16, bias [E] f32 or None; top k of E experts, up to T_max
+    tokens a pass.  H % 128 == 0 and I % 64 == 0 (moe_route's and the layer's geometry).
+
+    The weight gradients are in dw_router [E,H] f32, dbias [E] f32 (None without
+    bias), dw_gateup and dw_down (of dw_type), overwritten by every backward
+    pass, or added to with accumulate (the router's always overwritten).  A
+    backward pass belongs to the last forward pass of the layer.
+    """
+
+    def __init__(self, w_router, bias, w_gateup, w_down, k: int, T_max: int, keep: str = "q8",
+                 dw_type=torch.float32):
+        assert keep in ("q8", "bf16")
+        assert w_router.is_cuda and w_router.dtype == torch.bfloat16
+        self.E, self.H = w_router.shape
+        self.I = w_down.shape[2]
+        assert w_gateup.shape == (self.E, 2 * self.I, self.H) and w_down.shape == (self.E, self.H, self.I)
+        assert self.H % 128 == 0 and self.I % 64 == 0
+        self.w_router, self.bias, self.w_gateup, self.w_down = w_router, bias, w_gateup, w_down
+        self.k, self.T_max, self.q8 = k, T_max, keep == "q8"
+        self.device = dev = w_router.device
+        E, H, I, R = self.E, self.H, self.I, T_max * k
+        bf, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+        def new(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        # kept from the forward pass to the backward pass
+        self.ids, self.w = new((T_max, k), i32), new((T_max, k), f32)
+        self.offsets, self.perm, self.inv = new((E + 1,), i32), new((R,), i32), new((T_max, k), i32)
+        if self.q8:
+            self.x, self.x_exp = new((T_max, H), torch.int8), new((T_max, H // 32), u8)
+            self.act, self.act_exp = new((R, 2 * I), torch.int8), new((R, 2 * I // 32), u8)
+        else:
+            self.x, self.x_exp = new((T_max, H), bf), None
+            self.act, self.act_exp = new((R, 2 * I), bf), None
+        self.y_perm = new((R, H), bf)
+        # of one pass
+        self.gap, self.counts = new((T_max,), f32), new((E,), i32)
+        self.x_perm, self.dy_perm, self.h = new((R, H), bf), new((R, H), bf), new((R, I), bf)
+        self.tokens = new((T_max, H), bf) if self.q8 else self.x
+        self.dw, self.dlogits = new((T_max, k), f32), new((T_max, k), f32)
+        self.dw_router = new((E, H), f32)
+        self.dbias = new((E,), f32) if bias is not None else None
+        self.dw_gateup, self.dw_down = new(w_gateup.shape, dw_type), new(w_down.shape, dw_type)
+        self.status = torch.zeros((1,), dtype=i32, device=dev)
+        size = max(_lib.route_workspace_size(T_max, E), _lib.moe_permute_workspace_size(T_max, k, E),
+                   _block.moe_ffn_backward_workspace_size(R, I),
+                   _block.moe_route_backward_workspace_size(T_max, k, E, H))
+        self.ws = new((max(size, 256),), u8)
+        self.T = None
+
+    def forward(self, x, out, stream=None):
+        """out [T,H] = the layer of x [T,H] bf16 (contiguous); out bf16 or fp32."""
+        T, k, E = len(x), self.k, self.E
+        assert 0 < T <= self.T_max and x.shape[1] == self.H and x.dtype == torch.bfloat16 and x.is_contiguous()
+        R = T * k
+        with torch.cuda.device(self.device):
+            ids, w, inv, perm = self.ids[:T], self.w[:T], self.inv[:T], self.perm[:R]
+            _lib.moe_route(x, self.w_router, self.bias, k, ids, w, self.gap, self.ws, stream)
+            _lib.moe_permute_ws(ids, E, None, self.counts, self.offsets, perm, inv, None, self.ws, self.status, stream)
+            if self.q8:
+                _block.moe_checkpoint_save(x, self.x[:T], self.x_exp[:T], stream=stream)
+            else:
+                # a copy, as a dispatch of every token to its own place would make
+                s = stream if stream is not None else torch.cuda.current_stream()
+                with torch.cuda.stream(s):
+                    self.x[:T].copy_(x)
+            x_perm, y_perm = self.x_perm[:R], self.y_perm[:R]
+            _block.moe_dispatch(x, inv, x_perm, dev_status=self.status, stream=stream)
+            _block.moe_ffn(x_perm, self.w_gateup, self.w_down, self.offsets, self.h[:R], y_perm, act=self.act[:R],
+                           act_exp=self.act_exp[:R] if self.q8 else None, dev_status=self.status, stream=stream)
+            _block.moe_collect(y_perm, inv, w, out, dev_status=self.status, stream=stream)
+        self.T = T
+        return out
+
+    def backward(self, dout, dx, add=None, accumulate=False, stream=None):
+        """dx [T,H] (bf16 or fp32) = add + the gradient of the last forward pass's x for dout [T,H] of its output;
+        the weights' gradients with it.  add: a gradient that is already there (of dx's type, may be dx), or None."""
+        T = self.T
+        assert T is not None and dout.shape == dx.shape == (T, self.H)
+        R = T * self.k
+        with torch.cuda.device(self.device):
+            w, inv = self.w[:T], self.inv[:T]
+            x_perm, dy_perm = self.x_perm[:R], self.dy_perm[:R]
+            act, act_exp = self.act[:R], self.act_exp[:R] if self.q8 else None
+            _block.moe_collect_backward(dout, self.y_perm[:R], inv, w, dy_perm, self.dw[:T], dev_status=self.status,
+                                        stream=stream)
+            if self.q8:
+                x, e = self.x[:T], self.x_exp[:T]
+                _block.moe_checkpoint_load(x, e, x_perm, inv_perm=inv, dev_status=self.status, stream=stream)
+                _block.moe_checkpoint_load(x, e, self.tokens[:T], stream=stream)
+            else:
+                _block.moe_dispatch(self.x[:T], inv, x_perm, dev_status=self.status, stream=stream)
+            dx_perm = self.y_perm[:R]  # its values have been read
+            _block.moe_ffn_backward(dy_perm, x_perm, act, self.w_gateup, self.w_down, self.offsets, dx_perm,
+                                    self.dw_gateup, self.dw_down, self.ws, act_exp=act_exp, accumulate=accumulate,
+                                    dev_status=self.status, stream=stream)
+            _block.moe_dispatch_backward(dx_perm, inv, dx, add=add, dev_status=self.status, stream=stream)
+            _block.moe_route_backward(self.dw[:T], w, self.ids[:T], self.tokens[:T], self.w_router, self.offsets,
+                                      self.perm[:R], self.dlogits[:T], dx, self.dw_router, self.dbias, self.ws, add=dx,
+                                      dev_status=self.status, stream=stream)
+        self.T = None
+        return dx
+
+    def read_status(self) -> int:
+        return int(self.status.item())

@@ -381,3 +381,28 @@ def test_refusals_of_the_binding():
         with pytest.raises(MoEError):
             call()
             pytest.fail(f"call {i} was accepted")
+
+
+def test_many_passes_with_few_rows():
+    """Mostly experts without rows or with a few, many launches in a row: every wait ends and the bits stay."""
+    E, H, I, T = 512, 256, 128, 160
+    g = gen(29)
+    ids = torch.randint(0, E, (T,), generator=g, device=DEV).sort().values
+    off = torch.searchsorted(ids, torch.arange(E + 1, device=DEV)).to(torch.int32)
+    x, dy = (torch.randn((T, H), generator=g, device=DEV).to(BF16) for _ in range(2))
+    wgu, wd = (torch.randn(s, generator=g, device=DEV).to(BF16) / 16 for s in ((E, 2 * I, H), (E, H, I)))
+    a, e = keep("q8", T, I)
+    h, y, dx = matrix(T, I, BF16), matrix(T, H, BF16), matrix(T, H, BF16)
+    dwgu, dwd = torch.empty_like(wgu), torch.empty_like(wd)
+    ws = torch.empty(M.moe_ffn_backward_workspace_size(T, I), dtype=torch.uint8, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    want = None
+    for i in range(300):
+        M.moe_ffn(x, wgu, wd, off, h, y, act=a, act_exp=e, dev_status=st)
+        M.moe_ffn_backward(dy, x, a, wgu, wd, off, dx, dwgu, dwd, ws, act_exp=e, dev_status=st)
+        if i % 50 == 0:
+            assert int(st) == 0
+            got = [t.clone() for t in (y, dx, dwgu, dwd)]
+            want = want or got
+            assert all(torch.equal(p, q) for p, q in zip(want, got))
+    assert int(st) == 0
