@@ -861,12 +861,17 @@ bool map_grad(CUtensorMap* m, const void* p, int type, int E, int rows, int widt
   return make_map(m, p, 3, dims, str, box, type);
 }
 
-// The second operand of a row launch: boxes of 128, 96 and 64 rows.
+// The second operand of a row launch: boxes of 128, 96 and 64 rows.  (No tile of
+// 128 rows or fewer needs more than 64 for its half.)
 struct RowMaps {
   CUtensorMap m128, m96, m64;
   bool make(const void* p, int64_t ld, int R, int width) {
-    return map_rows(&m128, p, ld, R, width, 128) && map_rows(&m96, p, ld, R, width, 96) &&
-           map_rows(&m64, p, ld, R, width, 64);
+    if (!map_rows(&m64, p, ld, R, width, 64)) return false;
+    if (R <= 128) {
+      m128 = m96 = m64;
+      return true;
+    }
+    return map_rows(&m128, p, ld, R, width, 128) && map_rows(&m96, p, ld, R, width, 96);
   }
 };
 
