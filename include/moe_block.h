@@ -288,8 +288,10 @@ MOE_API moe_status moe_checkpoint_load(const int8_t *q, int64_t ldq, const uint8
  *            and up columns each as moe_checkpoint_save keeps a matrix of width I
  *   y_perm   [R,H] y_type (out), or NULL when only h and act are wanted
  * Rows from offsets[E] on are not read for any result and not written.
- * H % 8 == 0, I % 8 == 0, H, I <= 65536; bf16 and f32 matrices start on 16 byte
- * boundaries with ld % 8 == 0.  offsets outside [0,R] or falling are clamped.
+ * H % 8 == 0, I % 8 == 0, H, I <= 65536, R <= 2^30; bf16 and f32 matrices start on
+ * 16 byte boundaries with ld % 8 == 0 and ld < 2^38 (act in 8 bits: any, fastest on
+ * 8 byte boundaries).  offsets outside [0,R] are clamped to it, and a segment that
+ * would end before it begins is empty.
  * dev_status gets MOE_DEV_TIMEOUT if a bounded pipeline wait ran out (the
  * launch then stops early; outputs are incomplete).
  * Source: AFN-019 "Hide SSD misses before the router knows they exist", section

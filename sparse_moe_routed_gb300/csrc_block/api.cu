@@ -82,10 +82,13 @@ moe_status check_routes(int T, int k, int H, int R, const int32_t* slots, const 
   return MOE_OK;
 }
 
-// The contractions read and write whole 16-byte pieces.
+// The contractions read and write whole 16-byte pieces, and rows are less than 2^40
+// bytes apart (a tensor map's limit).
 moe_status check_operand(const Rows& r, int64_t n, int H) {
   MOE_TRY(check_rows(r, n, H));
-  return r.p == nullptr || (aligned(r.p, 16) && r.ld % 8 == 0) ? MOE_OK : MOE_EINVAL;
+  if (r.p == nullptr) return MOE_OK;
+  if (!aligned(r.p, 16) || r.ld % 8 != 0) return MOE_EINVAL;
+  return r.ld < (INT64_C(1) << 38) ? MOE_OK : MOE_ENOTSUP;
 }
 
 moe_status check_ffn(int R, int E, int H, int I, const int32_t* offsets, const int32_t* status) {

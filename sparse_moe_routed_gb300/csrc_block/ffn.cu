@@ -47,21 +47,26 @@ enum Mode { kGateUp, kDown, kDh, kDx, kGrad };
 constexpr int kThreads = 416;
 constexpr int kEpiWarps = 8;
 constexpr int kK = 64;  // contraction per stage: one 128-byte swizzled row
-constexpr int kABytes = 128 * kK * 2, kBBytes = 128 * kK * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kABytes = 128 * kK * 2, kStageBytes = 2 * kABytes;  // a CTA's half of a stage, of one and both operands
 constexpr int kTurnRows = 16;            // rows that a warp turns at a time,
 constexpr int kTurnLd = 36;              // 32 features each: a row and 16 bytes, so that reads of 8 rows spread over the banks
 constexpr int kTurn = kTurnRows * kTurnLd;
 constexpr int kOut = 32 * 128;           // bytes of a gradient that a warp hands to a copy: 32 rows of 128 bytes
 constexpr int kList = 128;               // tiles of a pair that are looked up ahead
+constexpr int kRun = 3;                  // tiles of a gradient that share the first operand, at most
 constexpr int kClaims = 4;               // tiles that are claimed ahead
 
 template <int MODE>
 struct Smem {
-  static constexpr int kStages = MODE == kGrad ? 5 : 6;
+  // Row launches: stages of both operands.  Gradients: stages of either, so that
+  // the first one's can stay while a run of tiles goes over the second's columns.
+  static constexpr int kA = 6, kB = 5;
+  static constexpr int kStages = MODE == kGrad ? kA + kB : 6;
+  static constexpr int kRing = MODE == kGrad ? (kA + kB) * kABytes : kStages * kStageBytes;
   static constexpr int kTail = kEpiWarps * (MODE == kGrad ? kOut : kTurn * 4);
   static constexpr int kBars = 3 * kStages + 4 + 1 + 2 * kClaims;
   static constexpr int kBytes =
-      1024 + kStages * kStageBytes + kTail + kList * 16 + 16 + 8 * kClaims + kBars * 8 + 8 + 2 * (kMaxE + 1) * 4;
+      1024 + kRing + kTail + kList * 16 + 16 + 8 * kClaims + kBars * 8 + 8 + 2 * (kMaxE + 1) * 4;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -81,8 +86,9 @@ struct P {
   int dw_type, accumulate;
   bool a_one, b_one, a2_one, b2_one;  // operands whose half of a stage is one copy
   int mt;             // row launches: 256-feature tiles (gate/up: 128 gate and 128 up)
-  int tgu, tall;      // gradients: tiles of dW_gu per expert, of both;
-  int nt[2];          // tiles of 256 columns along a row, of dW_gu and dW_d
+  int tgu, tall;        // gradients: runs of tiles of dW_gu per expert, of both;
+  int nt[2];            // tiles of 256 columns along a row, of dW_gu and dW_d;
+  int runs[2], run[2];  // runs of tiles along a row, tiles of a run at most
   int* queue;         // workspace: tiles of gradients claimed so far
   int32_t* status;
 };
@@ -164,11 +170,32 @@ template <int MODE, bool WARP>
 struct Walk {
   const Sched<MODE>& sc;
   const Claims& cl;
-  int t, j = 0;  // tile, which of the pair's
+  int t, j = 0;                     // tile (gradients: run), which of the pair's
+  int e, i, m, n, n_end;            // gradients: expert, which one, row of tiles, tile, the run's end
+  bool begins = true;               // the run
 
-  __device__ __forceinline__ Walk(const Sched<MODE>& s, const Claims& c) : sc(s), cl(c), t(blockIdx.x >> 1) {}
+  __device__ __forceinline__ Walk(const Sched<MODE>& s, const Claims& c) : sc(s), cl(c), t(blockIdx.x >> 1) { run(); }
   __device__ __forceinline__ bool more() const { return t < sc.total; }
+  __device__ __forceinline__ void run() {
+    if (MODE != kGrad) return;
+    e = t / sc.p.tall;
+    const int l = t - e * sc.p.tall;
+    i = l >= sc.p.tgu;
+    const int at = l - (i ? sc.p.tgu : 0);
+    m = at / sc.p.runs[i];
+    n = (at - m * sc.p.runs[i]) * sc.p.run[i];
+    n_end = min(n + sc.p.run[i], sc.p.nt[i]);
+    begins = true;
+  }
+  // Whether a gradient's tile loads its first operand, and whether it is the last
+  // to read it: always, but in a run whose first operand fits into the stages.
+  __device__ __forceinline__ bool loads(const Tile& tl) const { return begins || tl.k > Smem<MODE>::kA * kK; }
+  __device__ __forceinline__ bool ends(const Tile& tl) const { return n + 1 == n_end || tl.k > Smem<MODE>::kA * kK; }
   __device__ __forceinline__ void next() {
+    if (MODE == kGrad) {
+      begins = false;
+      if (++n < n_end) return;
+    }
     ++j;
     if (MODE != kGrad) {
       t += gridDim.x >> 1;
@@ -181,6 +208,7 @@ struct Walk {
       pair::arrive_at(cl.empty + 8 * slot, 0);
     }
     if (WARP) t = __shfl_sync(0xffffffffu, t, 0);
+    run();
   }
   __device__ __forceinline__ Tile tile() const {
     if (MODE != kGrad) {
@@ -189,13 +217,11 @@ struct Walk {
       return sc.rows_tile(v.x, v.y, v.z, v.w);
     }
     Tile r;
-    r.e = t / sc.p.tall;
-    const int l = t - r.e * sc.p.tall;
-    r.down = l >= sc.p.tgu;
-    const int i = r.down, at = r.down ? l - sc.p.tgu : l, m = at / sc.p.nt[i];
+    r.e = e;
+    r.down = i;
     r.m0 = m * 256;
-    r.n0 = (at - m * sc.p.nt[i]) * 256;
-    r.n = min(256, (r.down ? sc.p.I : sc.p.H) - r.n0);
+    r.n0 = n * 256;
+    r.n = min(256, (i ? sc.p.I : sc.p.H) - r.n0);
     r.N = up(r.n, 32) * 32;
     r.s0 = sc.off[r.e];
     r.k = max(sc.off[r.e + 1] - r.s0, 0);
@@ -415,11 +441,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mo2,
                const __grid_constant__ P p) {
   constexpr int kStages = Smem<MODE>::kStages, kTail = Smem<MODE>::kTail, kBars = Smem<MODE>::kBars;
+  constexpr int kRing = Smem<MODE>::kRing, kA = Smem<MODE>::kA, kB = Smem<MODE>::kB;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - ptx::smem_u32(smem_raw));
-  float* turn = reinterpret_cast<float*>(sm + kStages * kStageBytes);
-  int4* list = reinterpret_cast<int4*>(sm + kStages * kStageBytes + kTail);
+  float* turn = reinterpret_cast<float*>(sm + kRing);
+  int4* list = reinterpret_cast<int4*>(sm + kRing + kTail);
   uint32_t* misc = reinterpret_cast<uint32_t*>(list + kList);  // tensor memory, abort, tiles
   volatile uint32_t* abort = misc + 1;
   const uint32_t claimed = ptx::smem_u32(misc + 4), bars = claimed + 8 * kClaims;
@@ -495,7 +522,51 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const Claims claims{claimed, qfull, qempty, abort};
 
-  if (warp == 0 || warp == 10) {
+  if (MODE == kGrad && (warp == 0 || warp == 10)) {
+    // ------------------------------------------------ operands of gradients
+    if (pair::elect()) {
+      const uint64_t pol = ptx::policy_evict_last();
+      const int r = static_cast<int>(rank);
+      const bool is_a = warp == 0;
+      const uint32_t stage0 = is_a ? 0 : kA, stages = is_a ? kA : kB;
+      uint32_t s = 0, ph = 0, used = 0;
+      bool ok = true;
+      for (Walk<MODE, false> w(sc, claims); w.more() && ok; w.next()) {
+        const Tile tl = w.tile();
+        if (is_a && !w.loads(tl)) continue;
+        const CUtensorMap* map = is_a ? (tl.down ? &ma2 : &ma) : (tl.down ? &mb2 : &mb);
+        const bool one = is_a ? (tl.down ? p.a2_one : p.a_one) : (tl.down ? p.b2_one : p.b_one);
+        const int c = is_a ? tl.m0 + r * 128 : tl.n0 + r * (tl.N / 2);
+        const int boxes = is_a ? 2 : up(tl.N / 2, 64);
+        const uint32_t bytes = one ? kABytes : boxes * 8192;
+        for (int k = 0; k < tl.k; k += kK) {
+          const uint32_t st = stage0 + s;
+          ok = pair::wait<0>(empty + 8 * st, ph ^ 1u, abort, p.status);
+          if (!ok) break;
+          const bool alone = ends_inside(tl.k - k);
+          uint32_t bar = (alone ? tfull : full) + 8 * st;
+          if (alone || rank == 0)
+            ptx::mbar_arrive_expect_tx(bar, alone ? bytes : 2 * bytes);
+          else
+            pair::arrive_at(bar, 0);
+          bar = pair::at_rank(bar, alone ? rank : 0);
+          const uint32_t at = base + st * kABytes;
+          if (one) {
+            pair::tma_3d(at, map, bar, 0, tl.s0 + k, c / 64, pol);
+          } else {
+            for (int i = 0; i < boxes; ++i) pair::tma_2d(at + i * 8192, map, bar, c + i * 64, tl.s0 + k, pol);
+          }
+          if (++s == stages) s = 0, ph ^= 1u;
+          ++used;
+        }
+      }
+      for (uint32_t i = 1; i <= stages && i <= used && ok; ++i) {  // see the rows' operands
+        const uint32_t back = s >= i ? s - i : s + stages - i;
+        ok = pair::wait<64>(empty + 8 * (stage0 + back), s >= i ? ph : ph ^ 1u, abort, p.status);
+      }
+      if (!ok) pair::pause_10ms();
+    }
+  } else if (warp == 0 || warp == 10) {
     // ------------------------------------------------------------- operands
     if (pair::elect()) {
       // Operands are read again by the tiles beside; results are not (weights and
@@ -507,57 +578,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (Walk<MODE, false> w(sc, claims); w.more() && ok; w.next()) {
         const Tile tl = w.tile();
-        const int half = tl.N / 2;
-        const CUtensorMap* a = MODE == kGrad && tl.down ? &ma2 : &ma;
-        const int box = half <= 64 ? 64 : half <= 96 ? 96 : 128;
-        const CUtensorMap* b = MODE == kGrad ? (tl.down ? &mb2 : &mb) : box == 64 ? &mb2 : box == 96 ? &ma2 : &mb;
-        const bool a_one = MODE == kGrad && tl.down ? p.a2_one : p.a_one, b_one = tl.down ? p.b2_one : p.b_one;
-        const int boxes = MODE != kGrad || b_one ? 1 : up(half, 64);
-        const uint32_t bytes = kABytes + (MODE == kGrad ? (b_one ? kBBytes : boxes * 8192) : box * 128);
+        const int half = tl.N / 2, box = half <= 64 ? 64 : half <= 96 ? 96 : 128;
+        const CUtensorMap* b = box == 64 ? &mb2 : box == 96 ? &ma2 : &mb;
+        const int c = tl.m0 + r * (MODE == kGateUp ? 64 : 128), row = tl.n0 + r * half;
         for (int k = 0; k < tl.k; k += kK) {
           ok = pair::wait<0>(empty + 8 * pipe.s, pipe.ph ^ 1u, abort, p.status);
           if (!ok) break;
-          const uint32_t sa = base + pipe.s * kStageBytes, sb = sa + kABytes;
-          const bool alone = MODE == kGrad && ends_inside(tl.k - k);
-          uint32_t bar = (alone ? tfull : full) + 8 * pipe.s;
-          if (warp == 0) {
-            if (alone || rank == 0)
-              ptx::mbar_arrive_expect_tx(bar, alone ? bytes : 2 * bytes);
-            else if (MODE == kGrad)
-              pair::arrive_at(bar, 0);
-          }
-          bar = pair::at_rank(bar, alone ? rank : 0);
-          if (warp == 0) {
-            const int c = tl.m0 + r * (MODE == kGateUp ? 64 : 128);
-            if (MODE == kDown) {
-              pair::tma_3d(sa, a, bar, k, c, tl.e, pol);
-            } else if (a_one) {
-              if (MODE == kGateUp)
-                pair::tma_5d(sa, a, bar, k, 0, 0, c / 32, tl.e, pol);
-              else if (MODE == kGrad)
-                pair::tma_3d(sa, a, bar, 0, tl.s0 + k, c / 64, pol);
-              else
-                pair::tma_4d(sa, a, bar, 0, k, c / 64, tl.e, pol);
-            } else if (MODE == kGateUp) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)  // 32 gate rows, their 32 up rows, and again
-                pair::tma_4d(sa + i * 4096, a, bar, k, c + (i >> 1) * 32, i & 1, tl.e, pol);
+          const uint32_t sa = base + pipe.s * kStageBytes;
+          uint32_t bar = full + 8 * pipe.s;
+          if (warp == 0 && rank == 0) ptx::mbar_arrive_expect_tx(bar, 2 * (kABytes + box * 128));
+          bar = pair::at_rank(bar, 0);
+          if (warp != 0) {
+            pair::tma_2d(sa + kABytes, b, bar, k, row, pol);
+          } else if (MODE == kDown) {
+            pair::tma_3d(sa, &ma, bar, k, c, tl.e, pol);
+          } else if (MODE == kGateUp) {
+            if (p.a_one) {
+              pair::tma_5d(sa, &ma, bar, k, 0, 0, c / 32, tl.e, pol);
             } else {
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                if (MODE == kGrad)
-                  pair::tma_2d(sa + i * 8192, a, bar, c + i * 64, tl.s0 + k, pol);
-                else
-                  pair::tma_3d(sa + i * 8192, a, bar, c + i * 64, k, tl.e, pol);
-              }
+              for (int i = 0; i < 4; ++i)  // 32 gate rows, their 32 up rows, and again
+                pair::tma_4d(sa + i * 4096, &ma, bar, k, c + (i >> 1) * 32, i & 1, tl.e, pol);
             }
-          } else if (MODE != kGrad) {
-            pair::tma_2d(sb, b, bar, k, tl.n0 + r * half, pol);
-          } else if (b_one) {
-            pair::tma_3d(sb, b, bar, 0, tl.s0 + k, (tl.n0 + r * half) / 64, pol);
+          } else if (p.a_one) {
+            pair::tma_4d(sa, &ma, bar, 0, k, c / 64, tl.e, pol);
           } else {
-            for (int i = 0; i < boxes; ++i)
-              pair::tma_2d(sb + i * 8192, b, bar, tl.n0 + r * half + i * 64, tl.s0 + k, pol);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) pair::tma_3d(sa + i * 8192, &ma, bar, c + i * 64, k, tl.e, pol);
           }
           pipe.next();
           ++used;
@@ -580,25 +627,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     // go on: one that came late would find the next phase of the same parity.
     if (rank == 0) {
       const bool one = pair::elect();
-      Pipe<kStages> pipe;
+      // Row launches: one ring.  Gradients: the first operand's stages, then the
+      // second's.
+      Pipe<MODE == kGrad ? kA : kStages> pa;
+      Pipe<kB> pb;
       int acc = 0;
       uint32_t aph = 0;
       bool ok = true;
+      constexpr uint32_t kNextA = (MODE == kGrad ? kABytes : kStageBytes) >> 4, kNextB = MODE == kGrad ? kABytes >> 4 : kNextA;
+      const uint32_t b0 = base + (MODE == kGrad ? kA : 1) * kABytes;
       const uint64_t da0 = kAMn<MODE> ? pair::sdesc_mn_sw128(base) : ptx::sdesc_k_sw128(base);
-      const uint64_t db0 = b_mn(MODE) ? pair::sdesc_mn_sw128(base + kABytes) : ptx::sdesc_k_sw128(base + kABytes);
+      const uint64_t db0 = b_mn(MODE) ? pair::sdesc_mn_sw128(b0) : ptx::sdesc_k_sw128(b0);
       constexpr uint32_t kStepA = (kAMn<MODE> ? 2048 : 32) >> 4, kStepB = (b_mn(MODE) ? 2048 : 32) >> 4;
       for (Walk<MODE, true> w(sc, claims); w.more() && ok; w.next()) {
         const Tile tl = w.tile();
         if (tl.k == 0) continue;
+        const bool loads = MODE != kGrad || w.loads(tl), ends = MODE != kGrad || w.ends(tl);
         const uint32_t id = pair::idesc(tl.N, kAMn<MODE>, b_mn(MODE));
         const uint32_t d = tmem + acc * 256;
         ok = __all_sync(0xffffffffu, pair::wait<0>(accempty + 8 * acc, aph ^ 1u, abort, p.status));
         if (!ok) break;
         ptx::tc_fence_after();
+        const auto at_begin = pa;
         for (int left = tl.k; left > 0; left -= kK) {
-          ok = __all_sync(0xffffffffu, pair::wait<0>(full + 8 * pipe.s, pipe.ph, abort, p.status));
+          if (loads) ok = pair::wait<0>(full + 8 * pa.s, pa.ph, abort, p.status);
+          if (MODE == kGrad) ok = ok && pair::wait<0>(full + 8 * (kA + pb.s), pb.ph, abort, p.status);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint64_t da = da0 + pipe.s * (kStageBytes >> 4), db = db0 + pipe.s * (kStageBytes >> 4);
+          const uint64_t da = da0 + pa.s * kNextA, db = db0 + (MODE == kGrad ? pb.s : pa.s) * kNextB;
           if (one) {
             pair::mma(d, da, db, id, left != tl.k);
             if (left >= kK) {
@@ -609,10 +665,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int kk = 1; kk < kK / 16; ++kk)
                 if (kk * 16 < left) pair::mma(d, da + kk * kStepA, db + kk * kStepB, id, 1);
             }
-            pair::commit_both(empty + 8 * pipe.s);
+            if (MODE == kGrad) pair::commit_both(empty + 8 * (kA + pb.s));
+            if (ends) pair::commit_both(empty + 8 * pa.s);
           }
-          pipe.next();
+          pa.next();
+          pb.next();
         }
+        if (!ends) pa = at_begin;  // the next tile reads them again
         if (ok && one) pair::commit_both(accfull + 8 * acc);
         acc ^= 1;
         if (acc == 0) aph ^= 1u;
@@ -625,24 +684,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 11) {
     // ------------------------------------------------ rows behind a sum's last
     if (MODE == kGrad) {
-      Pipe<kStages> pipe;
+      Pipe<kA> pa;
+      Pipe<kB> pb;
       uint32_t tph = 0;  // a bit per stage: the phase of its tfull
       bool ok = true;
+      // The next expert's rows stand there (or none): zeros, for whatever they
+      // hold times zero need not be zero.  16 lanes clear a row of two blocks.
+      auto clear = [&](int stage, int left) {
+        ok = ok && pair::wait_warp<0>(tfull + 8 * stage, (tph >> stage) & 1u, abort, p.status);
+        if (!ok) return;
+        tph ^= 1u << stage;
+        const uint32_t at = base + stage * kABytes + ((lane >> 3) & 1) * 8192 + (lane & 7) * 16;
+        for (int i = left + (lane >> 4); i < up(left, 16) * 16; i += 2)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * 128), "r"(0) : "memory");
+        pair::fence_smem_async();
+        __syncwarp();
+        if (lane == 0) pair::arrive_at(full + 8 * stage, 0);
+      };
       for (Walk<MODE, true> w(sc, claims); w.more() && ok; w.next()) {
         const Tile tl = w.tile();
-        for (int left = tl.k; left > 0; left -= kK, pipe.next()) {
-          if (!ends_inside(left)) continue;
-          ok = pair::wait_warp<0>(tfull + 8 * pipe.s, (tph >> pipe.s) & 1u, abort, p.status);
-          if (!ok) break;
-          tph ^= 1u << pipe.s;
-          // The next expert's rows stand there (or none): zeros, for whatever
-          // they hold times zero need not be zero.
-          const uint32_t at = base + pipe.s * kStageBytes + (lane >> 3) * 8192 + (lane & 7) * 16;
-          for (int i = left; i < up(left, 16) * 16; ++i)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * 128), "r"(0) : "memory");
-          pair::fence_smem_async();
-          __syncwarp();
-          if (lane == 0) pair::arrive_at(full + 8 * pipe.s, 0);
+        const bool loads = w.loads(tl);
+        for (int left = tl.k; left > 0 && ok; left -= kK) {
+          if (ends_inside(left)) {
+            if (loads) clear(pa.s, left);
+            clear(kA + pb.s, left);
+          }
+          if (loads) pa.next();
+          pb.next();
         }
       }
     }
@@ -686,7 +754,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile tl = w.tile();
       if (MODE == kDh) load_ahead(tl, group * 16);
       if (tl.k != 0) {
-        if (!pair::wait_warp<32>(accfull + 8 * acc, aph, abort, p.status)) break;
+        bool ok = pair::wait_warp<32>(accfull + 8 * acc, aph, abort, p.status);
+        // the warps that turn gate and up features together give up together
+        if (MODE == kGateUp) ok = pair::both(ok, 1 + group * 2 + (q >> 1));
+        if (!ok) break;
         ptx::tc_fence_after();
       }
       const uint32_t d = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
@@ -697,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 32 rows of 128 bytes at a time through shared memory, as a copy that
           // writes whole lines: a lane's own row would go out as 32 pieces of 32
           // bytes per store, one line each.
-          const uint32_t mine = base + kStages * kStageBytes + (warp - 2) * kOut + lane * 128;
+          const uint32_t mine = base + kRing + (warp - 2) * kOut + lane * 128;
           const int mw = tl.m0 + static_cast<int>(rank) * 128 + q * 32;
           const int wide = p.dw_type == MOE_ROW_F32 ? 32 : 64;  // columns of 128 bytes
           for (int c = group * wide; c < tl.n && mw < M; c += 2 * wide) {
@@ -730,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             pair::fence_smem_async();
             __syncwarp();
             if (lane == 0)
-              pair::tma_store_3d(tl.down ? &mo2 : &mo, base + kStages * kStageBytes + (warp - 2) * kOut, tl.n0 + c, mw, tl.e);
+              pair::tma_store_3d(tl.down ? &mo2 : &mo, base + kRing + (warp - 2) * kOut, tl.n0 + c, mw, tl.e);
           }
         } else if (tl.k != 0) {
           for (int c = group * 32; c < tl.n; c += 64) {
@@ -800,6 +871,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pair::cluster_sync();
   ptx::tc_fence_after();
   if (warp == 1) pair::tmem_dealloc(tmem);
+  // Neither CTA leaves, and makes room for one that allocates, before both have
+  // given their tensor memory back: it is the pair's.
+  __syncwarp();
+  pair::cluster_sync();
 }
 
 // ------------------------------------------------------------------ host
@@ -1025,8 +1100,20 @@ cudaError_t launch_ffn_grad(const FfnGradArgs& a, cudaStream_t st) {
   p.dw_type = a.dw_type;
   p.accumulate = a.accumulate;
   p.nt[0] = up(a.H, 256), p.nt[1] = up(a.I, 256);
-  p.tgu = a.dw_gateup != nullptr ? up(2 * a.I, 256) * p.nt[0] : 0;
-  p.tall = p.tgu + (a.dw_down != nullptr ? up(a.H, 256) * p.nt[1] : 0);
+  // Runs of up to kRun tiles where an expert's rows fit into the first operand's
+  // stages on average, so that it is read from L2 once for all of them (16,384
+  // tokens, 512 experts: 1,341 us, with runs of one, two and eight 1,457, 1,352 and
+  // 1,394), and where runs are many (768 tiles in all: 33 us, one by one 28).
+  const int64_t tiles = a.E * (static_cast<int64_t>(a.dw_gateup ? up(2 * a.I, 256) * p.nt[0] : 0) +
+                               (a.dw_down ? up(a.H, 256) * p.nt[1] : 0));
+  const bool share = a.R <= static_cast<int64_t>(a.E) * Smem<kGrad>::kA * kK && tiles >= 8 * sm_count();
+  for (int i = 0; i < 2; ++i) {
+    const int longest = share ? kRun : 1;
+    p.runs[i] = up(p.nt[i], longest);
+    p.run[i] = up(p.nt[i], p.runs[i]);
+  }
+  p.tgu = a.dw_gateup != nullptr ? up(2 * a.I, 256) * p.runs[0] : 0;
+  p.tall = p.tgu + (a.dw_down != nullptr ? up(a.H, 256) * p.runs[1] : 0);
   CUtensorMap ma, mb, ma2, mb2, mo, mo2;
   FFN_MAP(map_sum_rows(&ma2, &p.a2_one, a.dy.p, a.dy.ld, a.R, a.H, true));
   FFN_MAP(map_sum_rows(&mb2, &p.b2_one, a.h, a.I, a.R, a.I, a.I % 128 == 0));

@@ -87,6 +87,20 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// Whether two warps (barrier `id`) both agree.
+__device__ __forceinline__ bool both(bool mine, int id) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(ok)
+      : "r"(static_cast<uint32_t>(mine)), "r"(id)
+      : "memory");
+  return ok != 0;
+}
+
 // After an abort: for copies and MMAs that are still under way.
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();

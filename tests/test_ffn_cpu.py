@@ -57,6 +57,7 @@ REFUSALS = [
     (ffn_b, dict(wsb=16 * 3 * 32 * 2 + 15), EWS), (ffn_b, dict(ws=EIGHT), EINVAL), (ffn_b, dict(ws=A[7]), EINVAL),
     (ffn_b, dict(dwgu=C.c_void_p((1 << 20) + 16)), EINVAL), (ffn_b, dict(dxtype=5), EINVAL), (ffn_b, dict(dwtype=2), EINVAL),
     (ffn_b, dict(lddy=8), ESHAPE), (ffn_b, dict(I=12), ENOTSUP), (ffn_b, dict(R=-1), ESHAPE),
+    (ffn, dict(ldx=1 << 38), ENOTSUP), (ffn_b, dict(lddy=1 << 38), ENOTSUP), (ffn_b, dict(ldx=1 << 38), ENOTSUP),
 ]
 
 

@@ -406,3 +406,67 @@ def test_many_passes_with_few_rows():
             want = want or got
             assert all(torch.equal(p, q) for p, q in zip(want, got))
     assert int(st) == 0
+
+
+def test_gate_and_up_alone():
+    """Without y: h and act, and no W_down is needed."""
+    b = Block([5, 40], 128, 64, 31, False)
+    h, y, a = matrix(b.R, 64, BF16), matrix(b.R, 128, F32), matrix(b.R, 128, BF16)
+    M.moe_ffn(b.x, b.wgu, b.wd, b.off, h, y, act=a)
+    h2, a2 = matrix(b.R, 64, BF16), matrix(b.R, 128, BF16)
+    M.moe_ffn(b.x, b.wgu, None, b.off, h2, None, act=a2)
+    assert torch.equal(h.nan_to_num(), h2.nan_to_num()) and torch.equal(a.nan_to_num(), a2.nan_to_num())
+
+
+def test_more_tiles_than_are_looked_up_ahead():
+    """128 tiles of a pair are found at the start; here each has more."""
+    H, I = 8, 8
+    counts = [1_300_001, 0, 1_300_003]
+    b = Block(counts, H, I, 37, True)
+    h, y = matrix(b.R, I, BF16), matrix(b.R, H, F32)
+    a, _ = b.kept("bf16", True)
+    dx, dwgu, dwd = matrix(b.R, H, F32), torch.empty_like(b.wgu), torch.empty_like(b.wd, dtype=F32)
+    ws = torch.empty(M.moe_ffn_backward_workspace_size(b.R, I), dtype=torch.uint8, device=DEV)
+    M.moe_ffn(b.x, b.wgu, b.wd, b.off, h, y)
+    M.moe_ffn_backward(b.dy, b.x, a, b.wgu, b.wd, b.off, dx, None, dwd, ws)
+    for k, s in b.experts():
+        x, wgu, wd = b.x[s].double(), b.wgu[k].double(), b.wd[k].double()
+        hh = ((x @ wgu[:I].t()).clamp_min(0) * (x @ wgu[I:].t())).to(BF16).double()
+        assert torch.equal(y[s].double(), hh @ wd.t())
+        g, u = a[s, :I].double(), a[s, I:].double()
+        dh = b.dy[s].double() @ wd
+        r = torch.where(g > 0, 1.0, 0.5)
+        assert torch.equal(dx[s].double(), torch.cat([dh * u * r, dh * g * r], 1) @ wgu)
+        want = b.dy[s].double().t() @ (g * r * u)
+        assert float(want.abs().max()) < 2 ** 24
+        assert torch.equal(dwd[k].double(), want)
+    assert bool((dwd[1] == 0).all())
+
+
+def test_two_streams_at_once():
+    """Launches of two calls that share the GPU: each as if it were alone."""
+    blocks = [Block([300, 0, 77, 500], 512, 256, s, False) for s in (41, 43)]
+    runs = []
+    for b in blocks:
+        a, e = keep("q8", b.R, 256)
+        o = [matrix(b.R, 256, BF16), matrix(b.R, 512, BF16), matrix(b.R, 512, BF16), torch.empty_like(b.wgu), torch.empty_like(b.wd)]
+        ws = torch.empty(M.moe_ffn_backward_workspace_size(b.R, 256), dtype=torch.uint8, device=DEV)
+        runs.append((b, a, e, o, ws))
+
+    def go(r, stream=None):
+        b, a, e, (h, y, dx, dwgu, dwd), ws = r
+        M.moe_ffn(b.x, b.wgu, b.wd, b.off, h, y, act=a, act_exp=e, stream=stream)
+        M.moe_ffn_backward(b.dy, b.x, a, b.wgu, b.wd, b.off, dx, dwgu, dwd, ws, act_exp=e, stream=stream)
+
+    want = []
+    for r in runs:
+        go(r)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in r[3]])
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(20):
+        for r, s in zip(runs, streams):
+            go(r, s)
+    torch.cuda.synchronize()
+    for r, w in zip(runs, want):
+        assert all(torch.equal(t.nan_to_num(), v.nan_to_num()) for t, v in zip(r[3], w))
