@@ -496,8 +496,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
 
-  pdl_wait();
-  pdl_trigger();
+  // A call's first launch waits for the stream before it reads anything.  The
+  // others may lay out their tiles before: the launch before them triggered after
+  // its own wait, so whoever wrote the offsets (and the weights, see the operands)
+  // has ended.
+  constexpr bool kFirst = MODE == kGateUp || MODE == kDh;
+  constexpr bool kEarlyA = MODE == kDown || MODE == kDx;
+  if (kFirst) {
+    pdl_wait();
+    pdl_trigger();
+  }
   // The first launch of a gradient call empties the queue of its last one.
   if (MODE == kDh && blockIdx.x == 0 && threadIdx.x == 0) *p.queue = 0;
   // Offsets, kept inside the buffers and rising, whatever they hold.
@@ -533,6 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   const Claims claims{claimed, qfull, qempty, abort};
+  if (!kFirst && !(kEarlyA && warp == 0)) {
+    pdl_wait();
+    pdl_trigger();
+  }
 
   if (MODE == kGrad && (warp == 0 || warp == 10)) {
     // ------------------------------------------------ operands of gradients
@@ -588,12 +600,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       Pipe<kStages> pipe;
       uint32_t used = 0;
       bool ok = true;
+      // Down's and dx's weights fill the stages once before the wait for the
+      // launch that makes their rows; no stage has to be waited for till then.
+      bool waited = !(kEarlyA && warp == 0);
       for (Walk<MODE, false> w(sc, claims); w.more() && ok; w.next()) {
         const Tile tl = w.tile();
         const int half = tl.N / 2, box = half <= 64 ? 64 : half <= 96 ? 96 : 128;
         const CUtensorMap* b = box == 64 ? &mb2 : box == 96 ? &ma2 : &mb;
         const int c = tl.m0 + r * (MODE == kGateUp ? 64 : 128), row = tl.n0 + r * half;
         for (int k = 0; k < tl.k; k += kK) {
+          if (!waited && used == kStages) {
+            pdl_wait();
+            waited = true;
+          }
           ok = pair::wait<0>(empty + 8 * pipe.s, pipe.ph ^ 1u, abort, p.status);
           if (!ok) break;
           const uint32_t sa = base + pipe.s * kStageBytes;
@@ -622,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++used;
         }
       }
+      if (!waited) pdl_wait();
       // Nothing of this CTA is under way when it ends: every stage that was
       // filled has been read (its release has arrived here), or, after an
       // abort, its copies have landed.
