@@ -27,14 +27,18 @@
 // further (some pairs ended at 1,000 us where most did at 850).
 //
 // What bounds it, in us of passes that follow one another:
-//   512 experts of 2,560 x 640, 80 rows each: forward 849, gradient 1,691: HBM
-//   (6.5 and 6.35 TB/s; each weight and its gradient pass once).
+//   512 experts of 2,560 x 640, 80 rows each: forward 842, gradient 1,685: HBM
+//   (6.6 and 6.4 TB/s; each weight and its gradient pass once).
 //   The same, 320 rows each: gate/up 880, down 498, dh 600, dx 872, weight
 //   gradients 1,350: HBM and the tensor cores both 50 to 60 % busy; 320 rows are
 //   two tiles that read the weights from L2 twice.
 //   One block of 4,096 x 8,192, 8,192 rows: forward 858, gradient 1,815: the
-//   tensor cores (1,923 and 1,817 TF/s; under the power cap 1,660 and 1,565).
-//   16 rows of 64 experts of 256 x 64: 6.5 + 6 forward: a launch's set-up.
+//   tensor cores (1,923 and 1,817 TF/s; under the power cap 1,688 and 1,600).
+//   16 rows of 64 experts of 256 x 64: 10 forward, 26 gradient; 2,700 rows of 64
+//   experts of 1,000 x 200: gradient 56 for 25 of bytes.  A launch takes 0.65 to
+//   begin as a pair, 1.8 to read offsets and lay out tiles, 1.5 (from L2) to 3
+//   (from HBM) for its first stage, 0.4 to 3 for its first results (code and kept
+//   values not in a cache), 1.2 to end as a pair.
 // Results turned in shared memory as bf16 pairs (down, dx), or a narrow last tile
 // split evenly over both CTAs, changed none of these by more than 1 %.
 #include <cuda.h>
@@ -499,7 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A call's first launch waits for the stream before it reads anything.  The
   // others may lay out their tiles before: the launch before them triggered after
   // its own wait, so whoever wrote the offsets (and the weights, see the operands)
-  // has ended.
+  // has ended (the gradient of 2,700 rows of 64 experts of 1,000 x 200: 56.2 us
+  // in a graph; waiting first, 59.4).
   constexpr bool kFirst = MODE == kGateUp || MODE == kDh;
   constexpr bool kEarlyA = MODE == kDown || MODE == kDx;
   if (kFirst) {

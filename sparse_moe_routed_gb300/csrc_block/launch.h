@@ -19,7 +19,8 @@ int sm_count();
 
 // Launch with programmatic stream serialization (see pdl_wait in
 // ../csrc/common.cuh): every kernel waits before its first global access and
-// before its trigger.  libmoe's int4 contractions may read offsets and packed
+// before its trigger.  (The later launches of an ffn.cu call read offsets and
+// weights before: the launch before them triggered after its wait.)  libmoe's int4 contractions may read offsets and packed
 // records while a launch of this library right before them still runs (see the
 // stream token in ../csrc/launch.h): no kernel that triggers writes those.
 template <typename... KArgs, typename... Args>
